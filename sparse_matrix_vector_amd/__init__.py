@@ -13,6 +13,13 @@ step of the computation runs in the HIP kernels of ``libnmspmv.so``.
     hyb = hybrid_pack(W, hybrid_select_rows(hybrid_row_loss(W), n_dense))
     y = spmv_hybrid(hyb, x)                        # sparse rows + dense rows
     ys = spmv_multi(parts, x, ws=workspace())      # K-split plan for batches on few rows
+
+and, between a decode layer's q+k+v and o projections (``include/nmattn.h``):
+
+    q, k = qk_norm_rope(q, k, positions, inv_freq, wq, wk)
+    cache = KVCache(n_pages, 64, heads, 128, torch.bfloat16, "mx8")
+    kv_write(cache, k, v, slots)                   # quantised as it is written
+    o = attn_decode(q, cache, page_table, lens)    # optionally behind a prefix shared by the batch
 """
 import ctypes
 
@@ -23,7 +30,8 @@ from ._lib import (NM_BF16, NM_ERR_BAD_MASK, NM_ERR_BAD_SHAPE, NM_ERR_HIP, NM_ER
 
 __all__ = ["pack", "spmv", "spmv_multi", "spmv_swiglu", "gemv_dense", "gemv_dense_multi", "gemv_dense_swiglu",
            "calib_accumulate", "calib_keep_mask", "hybrid_row_loss", "hybrid_select_rows", "hybrid_pack", "spmv_hybrid",
-           "Hybrid", "NmError", "dtype_code", "stream_handle", "workspace"]
+           "Hybrid", "NmError", "dtype_code", "stream_handle", "workspace", "qk_norm_rope", "KVCache", "kv_write",
+           "kv_read", "attn_decode", "attn_workspace"]
 
 _DT = {torch.float16: NM_FP16, torch.bfloat16: NM_BF16}
 
@@ -340,3 +348,6 @@ def spmv_hybrid(hyb, x, out=None, stream=None):
          hyb.W_dense.data_ptr(), hyb.rows_dense.data_ptr(), hyb.n_dense, hyb.R, K, hyb.n, hyb.m, dtype_code(x.dtype),
          x2.data_ptr(), B, y.data_ptr(), stream_handle(stream))
     return y[0] if squeeze else y
+
+
+from .attention import KVCache, attn_decode, attn_workspace, kv_read, kv_write, qk_norm_rope  # noqa: E402

@@ -12,6 +12,7 @@ LIB_PATH = os.path.join(HERE, "libnmspmv.so")
 NM_OK, NM_ERR_INVALID_ARG, NM_ERR_BAD_SHAPE, NM_ERR_UNSUPPORTED = 0, 1, 2, 3
 NM_ERR_BAD_MASK, NM_ERR_NONFINITE, NM_ERR_HIP = 4, 5, 6
 NM_FP16, NM_BF16 = 0, 1
+NM_KV_16, NM_KV_MX8, NM_KV_MX4 = 0, 1, 2
 
 # Every symbol the header declares, with its ctypes signature.
 _P, _I64, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -37,7 +38,28 @@ SIGNATURES = {
     "nm_version": (_I, []),
 }
 
+# Likewise for include/nmattn.h; bound by attn_lib().
+ATTN_SIGNATURES = {
+    "nm_qk_norm_rope": (_I, [_P, _I64, _P, _I64, _I64, _I, _I, _I, _I, _P, _P, ctypes.c_float, _P, _P, _I, _I, _P, _P,
+                             _P]),
+    "nm_kv_bytes": (_I64, [_I64, _I, _I, _I, _I]),
+    "nm_kv_scale_bytes": (_I64, [_I64, _I, _I, _I, _I]),
+    "nm_kv_write": (_I, [_P, _P, _I64, _P, _I64, _I64, _P, _P]),
+    "nm_kv_read": (_I, [_P, _P, _I64, _P, _P, _P]),
+    "nm_attn_workspace_bytes": (_I64, [_I64, _I, _I, _I, _I64, _I64]),
+    "nm_attn_decode": (_I, [_P, _I64, _I64, _I, _P, _P, _I64, _P, _I64, _P, _I64, ctypes.c_float, _P, _P, _P, _I64,
+                            _P]),
+}
+
+
+class KvCacheStruct(ctypes.Structure):
+    """nm_kv_cache of include/nmattn.h."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("n_pages", _I64), ("page_size", _I),
+                ("heads", _I), ("D", _I), ("dtype", _I), ("format", _I)]
+
+
 _lib = None
+_attn_lib = None
 
 
 class NmError(RuntimeError):
@@ -63,6 +85,19 @@ def lib():
             fn.argtypes = args
         _lib = handle
     return _lib
+
+
+def attn_lib():
+    """lib() with the calls of include/nmattn.h bound as well."""
+    global _attn_lib
+    if _attn_lib is None:
+        handle = lib()
+        for name, (res, args) in ATTN_SIGNATURES.items():
+            fn = getattr(handle, name)
+            fn.restype = res
+            fn.argtypes = args
+        _attn_lib = handle
+    return _attn_lib
 
 
 def call(name, *args):

@@ -1,0 +1,142 @@
+// nm_attn.h -- shared by the entry points of include/nmattn.h and their
+// kernels: the cache's byte layout, the launch plan of nm_attn_decode, and the
+// kernel-side declarations.  Host-only C++ (no HIP types): the checks and the
+// plan also build with a plain compiler under sanitizers; the constexpr layout
+// functions are used by the device code too.
+#ifndef NM_ATTN_H
+#define NM_ATTN_H
+
+#include <cstdint>
+
+#include "nmattn.h"
+
+namespace nma {
+
+// ---- cache layout -----------------------------------------------------------
+//
+// [page][head][page_size / 16] tiles of 16 tokens x D columns.  A tile is cut
+// into `chunks` of 64 x cb bytes, cb (16, or 8 in the smallest case) bytes for
+// each lane of a wave, in lane order: lane = quarter * 16 + m.  A load of one
+// chunk by a wave is one contiguous read of full cache lines, and what it
+// brings is that lane's part of a matrix-core operand:
+//   keys    m = token, a lane's e = 8 cb / bits elements are consecutive columns,
+//           chunk c, quarter q: columns c * 4e + q * e ..
+//   values  m = column group (D / 16 columns), quarter q: tokens 4q .. 4q + 3;
+//           16-bit: a chunk is a column's four tokens (half an operand as it is);
+//           codes: a token's D / 16 columns side by side (one scale serves them).
+constexpr int kTile = 16;
+
+constexpr int format_bits(int format) { return format == NM_KV_16 ? 16 : format == NM_KV_MX8 ? 8 : 4; }
+constexpr int tile_bytes(int D, int bits) { return kTile * D * bits / 8; }
+constexpr int lane_bytes(int D, int bits) { return tile_bytes(D, bits) / 64; }              // 8 .. 128
+constexpr int k_chunk_bytes(int D, int bits) { return lane_bytes(D, bits) < 16 ? lane_bytes(D, bits) : 16; }
+constexpr int v_chunk_bytes(int D, int bits) { return bits == 16 ? 8 : k_chunk_bytes(D, bits); }
+
+// Byte of a tile at which key element (token, d) lies; d a multiple of 8 (8
+// columns always lie side by side, bits * 8 / 8 bytes).
+constexpr int k_offset(int D, int bits, int token, int d)
+{
+    const int cb = k_chunk_bytes(D, bits), e = cb * 8 / bits;
+    return d / (4 * e) * (64 * cb) + (d / e % 4 * 16 + token) * cb + d % e * bits / 8;
+}
+
+// Byte of a tile at which value element (token, d) lies (4-bit: d even, two
+// columns a byte, the lower one in the low nibble).
+constexpr int v_offset(int D, int bits, int token, int d)
+{
+    const int cb = v_chunk_bytes(D, bits), per = D / 16, j = d % per, r = token % 4;
+    const int at = (bits == 16 ? j * 4 + r : r * per + j) * bits / 8;
+    return at / cb * (64 * cb) + (token / 4 * 16 + d / per) * cb + at % cb;
+}
+
+// Scale bytes: one per 32 columns of a token's head; D / 2 per tile.  Keys:
+// [token][block] (a lane reads its token's), values: [block][token] (a lane
+// reads its four tokens' of one block).
+constexpr int kBlock = 32;
+constexpr int scale_tile_bytes(int D) { return kTile * D / kBlock; }
+constexpr int k_scale_offset(int D, int token, int block) { return token * (D / kBlock) + block; }
+constexpr int v_scale_offset(int token, int block) { return block * kTile + token; }
+
+// ---- the plan of nm_attn_decode ----------------------------------------------
+//
+// Work is cut into units of (row group, key head, range of tokens); a block of
+// kWaves waves takes one, its waves take the range's pairs of tiles in turn and
+// add their results up in LDS.  Prefix units: rows are the whole batch's query
+// heads of one key head, in groups of 16 mt; own-token units: one sequence's
+// query heads of one key head, in groups of 16.  Ranges of one row are added up
+// by a second launch (combine), through fp32 partial results in the workspace;
+// with a single range per row there is none and no workspace.
+constexpr int kWaves = 4;
+constexpr int kStep = 2 * kTile;            // tokens a wave takes at a time
+constexpr int kCus = 256;
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+constexpr int64_t kMaxRows = int64_t(1) << 26;      // B * Hq
+
+struct AttnPlan {
+    int G;                                        // query heads per key head
+    int mt;                                       // prefix units hold 16 mt rows
+    int64_t prefix_rows;                          // B * G
+    int64_t prefix_groups, prefix_splits, prefix_chunk;
+    int64_t own_groups, own_splits, own_chunk;
+    bool direct;                                  // no combine: units write o
+    int64_t prefix_parts, own_parts;              // partial rows of each kind
+};
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Cuts `tokens` into ranges of whole steps for every wave, so that `units` row
+// groups make about `blocks` blocks.
+inline void cut(int64_t tokens, int64_t units, int64_t blocks, int64_t* splits, int64_t* chunk)
+{
+    const int64_t grain = kWaves * kStep;
+    if (tokens == 0) {
+        *splits = 0;
+        *chunk = grain;
+        return;
+    }
+    int64_t want = ceil_div(blocks, units);
+    if (want > ceil_div(tokens, grain))
+        want = ceil_div(tokens, grain);
+    *chunk = ceil_div(ceil_div(tokens, want), grain) * grain;
+    *splits = ceil_div(tokens, *chunk);
+}
+
+inline AttnPlan attn_plan(int64_t B, int Hq, int heads, int D, int64_t prefix_len, int64_t max_len)
+{
+    AttnPlan p;
+    p.G = Hq / heads;
+    p.prefix_rows = B * p.G;
+    p.mt = p.prefix_rows <= 16 || D == 256 ? 1 : 2;
+    p.prefix_groups = ceil_div(p.prefix_rows, 16 * p.mt);
+    cut(prefix_len, heads * p.prefix_groups, kCus, &p.prefix_splits, &p.prefix_chunk);
+    p.own_groups = ceil_div(p.G, 16);
+    cut(max_len, B * heads * p.own_groups, 3 * kCus, &p.own_splits, &p.own_chunk);
+    p.direct = p.prefix_splits == 0 && p.own_splits <= 1;
+    p.prefix_parts = p.direct ? 0 : p.prefix_splits * heads * p.prefix_rows;
+    p.own_parts = p.direct ? 0 : p.own_splits * B * Hq;
+    return p;
+}
+
+// Workspace: every partial row's D sums, then every row's (maximum, sum).
+inline int64_t attn_workspace(const AttnPlan& p, int D) { return (p.prefix_parts + p.own_parts) * (D + 2) * 4; }
+
+}  // namespace nma
+
+namespace nmk {
+
+// The kernel side of the calls of the same names, on checked arguments with
+// work to do (rows > 0).
+int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t T, int Hq, int Hk, int D,
+                 int dtype, const void* wq, const void* wk, float eps, const int32_t* positions,
+                 const float* inv_freq, int rot, int interleaved, void* q_out, void* k_out, void* stream);
+int kv_write(const nm_kv_cache& cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t T,
+             const int64_t* slots, void* stream);
+int kv_read(const nm_kv_cache& cache, const int64_t* slots, int64_t T, void* k, void* v, void* stream);
+int attn_decode(const nma::AttnPlan& plan, const void* q, int64_t q_stride, int64_t B, int Hq,
+                const nm_kv_cache& cache, const int32_t* prefix_pages, int64_t prefix_len, const int32_t* page_table,
+                int64_t table_stride, const int32_t* lens, int64_t max_len, float scale, void* o, float* lse,
+                void* workspace, void* stream);
+
+}  // namespace nmk
+
+#endif  // NM_ATTN_H

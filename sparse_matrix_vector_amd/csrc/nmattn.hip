@@ -1,0 +1,675 @@
+// nmattn.hip -- nm_attn_decode: single-token attention over the paged cache.
+//
+// For the rows (query heads) q of a unit and its tokens t, with scores
+// s_t = scale * q . k_t, one pass keeps the running maximum m, the sum
+// l = sum exp(s_t - m) and the vector o = sum exp(s_t - m) v_t, multiplying l and
+// o by exp(m_old - m_new) where the maximum grows; units of one row are joined
+// by the same rule (combine_kernel).
+//
+// Everything runs on the matrix cores with the cache as the left operand, 16
+// tokens or 16 columns by 16 rows (v_mfma_f32_16x16x32):
+//   scores  S^T[token][row]  = sum over columns of K[token][d] q[row][d]
+//   output  O^T[d][row]     += sum over tokens of V[token][d] p[row][token]
+// In both a lane's column is its row of q (lane % 16), so the softmax statistics
+// and the rescaling of o are per lane.  The score tile's layout (lane quarter kg,
+// register r: token 4 kg + r) is the second product's right operand as it
+// stands when a step takes two 16-token tiles: its k index (kg, i) is token
+// 4 kg + i of the first tile for i < 4, of the second for i >= 4.  The values are
+// stored in that order, the keys in the order of the first product's left
+// operand (nm_attn.h), so nothing passes through LDS and every load is one
+// contiguous kilobyte for a wave.
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "nm_attn.h"
+#include "nm_device.h"
+
+namespace {
+
+using namespace nmd;
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+#define NM_NEG_INF (-__builtin_inff())
+
+int hip_status(hipError_t e) { return e == hipSuccess ? NM_OK : NM_ERR_HIP; }
+
+struct AttnArgs {
+    const uint16_t* q;
+    const uint8_t* k;
+    const uint8_t* v;
+    const uint8_t* k_scale;
+    const uint8_t* v_scale;
+    const int32_t* prefix_pages;
+    const int32_t* page_table;
+    const int32_t* lens;
+    uint16_t* o;
+    float* lse;
+    float* part_o;              // [rows][D] partial sums: prefix rows first, own rows behind them
+    f32x2* part_ml;             // [rows] (maximum, sum)
+    int64_t q_stride, table_stride, n_pages, own_base;   // own_base: first partial row of the own-token units
+    int B, Hq, heads, G, page_shift;
+    int prefix_len, max_len;
+    int prefix_rows, prefix_groups, prefix_splits, prefix_chunk;
+    int own_groups, own_splits, own_chunk;
+    float scale;                // scale * log2(e): scores are kept in base 2
+};
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
+{
+    if constexpr (DT == NM_FP16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                      0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+}
+
+// Maximum / sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48 (one row's quarters).
+__device__ __forceinline__ float quarters_max(float v)
+{
+    u32x2 p = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(f32_bits(v), f32_bits(v), false, false));
+    v = fmaxf(bits_f32(p.x), bits_f32(p.y));
+    p = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(f32_bits(v), f32_bits(v), false, false));
+    return fmaxf(bits_f32(p.x), bits_f32(p.y));
+}
+
+__device__ __forceinline__ float quarters_sum(float v)
+{
+    u32x2 p = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(f32_bits(v), f32_bits(v), false, false));
+    v = bits_f32(p.x) + bits_f32(p.y);
+    p = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(f32_bits(v), f32_bits(v), false, false));
+    return bits_f32(p.x) + bits_f32(p.y);
+}
+
+// One lane's part of a 16-token tile of keys or values as loaded, and how it
+// becomes operands.  BITS 16: as it is.  Codes: converted to bfloat16 with the
+// scale applied, which is exact (at most four significant bits).
+template <int BITS, int D>
+struct Cache {
+    static constexpr int kCb = nma::k_chunk_bytes(D, BITS);
+    static constexpr int kVb = nma::v_chunk_bytes(D, BITS);
+    static constexpr int kWords = nma::lane_bytes(D, BITS) / 4;
+    static constexpr int kE = kCb * 8 / BITS;          // elements of a chunk
+    static constexpr int kBlocks = D / nma::kBlock;    // scales of a token
+    static constexpr int kPer = D / 16;                // value columns of a lane
+
+    struct Raw {
+        uint32_t w[kWords];
+    };
+
+    template <int CB>
+    static __device__ __forceinline__ void load(Raw& raw, const uint8_t* tile, int lane)
+    {
+        typedef uint32_t chunk __attribute__((ext_vector_type(CB / 4)));
+#pragma unroll
+        for (int c = 0; c < kWords * 4 / CB; ++c) {
+            const chunk x = *reinterpret_cast<const chunk*>(tile + c * 64 * CB + lane * CB);
+#pragma unroll
+            for (int i = 0; i < CB / 4; ++i)
+                raw.w[CB / 4 * c + i] = x[i];
+        }
+    }
+
+    // The scale bytes of the lane's token (keys; kBlocks bytes, up to two words).
+    struct KScale {
+        uint32_t w[kBlocks > 4 ? 2 : 1];
+    };
+    static __device__ __forceinline__ void load_k_scale(KScale& s, const uint8_t* tile, int m)
+    {
+        if constexpr (BITS != 16) {
+            if constexpr (kBlocks == 2)
+                s.w[0] = *reinterpret_cast<const uint16_t*>(tile + m * 2);
+            else if constexpr (kBlocks == 4)
+                s.w[0] = *reinterpret_cast<const uint32_t*>(tile + m * 4);
+            else {
+                const u32x2 x = *reinterpret_cast<const u32x2*>(tile + m * 8);
+                s.w[0] = x.x;
+                s.w[1] = x.y;
+            }
+        }
+    }
+
+    // The scale bytes of the lane's four tokens in its column group's block (values).
+    static __device__ __forceinline__ void load_v_scale(uint32_t& s, const uint8_t* tile, int m, int kg)
+    {
+        if constexpr (BITS != 16)
+            s = *reinterpret_cast<const uint32_t*>(tile + nma::v_scale_offset(4 * kg, m * kPer / nma::kBlock));
+    }
+
+    // Key operand of k-step s: columns column(s, kg) .. + 7 of the lane's token.
+    static __device__ __forceinline__ int column(int s, int kg) { return s * 8 / kE * 4 * kE + kg * kE + s * 8 % kE; }
+
+    static __device__ __forceinline__ u32x4 k_operand(const Raw& raw, const KScale& sc, int s, int kg)
+    {
+        if constexpr (BITS == 16) {
+            return u32x4{raw.w[4 * s], raw.w[4 * s + 1], raw.w[4 * s + 2], raw.w[4 * s + 3]};
+        } else {
+            // the block of columns c 4E + kg E + ..: the first part is known here, the second by kg
+            const int block = s * 8 / kE * (4 * kE / nma::kBlock) + kg * kE / nma::kBlock;
+            const uint32_t word = kBlocks > 4 ? sc.w[s * 8 / kE * (4 * kE / nma::kBlock) / 4] : sc.w[0];
+            const float f = scale_value((word >> (8 * (block % 4))) & 255u);
+            u32x4 out;
+            if constexpr (BITS == 8) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    out[i] = __builtin_bit_cast(
+                        uint32_t, i % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw.w[2 * s + i / 2], f, true)
+                                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw.w[2 * s + i / 2], f, false));
+            } else {
+                out = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw.w[s], f, 0)),
+                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw.w[s], f, 1)),
+                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw.w[s], f, 2)),
+                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw.w[s], f, 3))};
+            }
+            return out;
+        }
+    }
+
+    // Value operands: out[2 j], out[2 j + 1] = column j of the lane's group, its
+    // four tokens.
+    static __device__ __forceinline__ void v_operands(uint32_t (&out)[2 * kPer], const Raw& raw, uint32_t sc)
+    {
+        if constexpr (BITS == 16) {
+#pragma unroll
+            for (int i = 0; i < 2 * kPer; ++i)
+                out[i] = raw.w[i];
+        } else {
+            uint32_t pair[4][kPer / 2];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float f = scale_value((sc >> (8 * r)) & 255u);
+#pragma unroll
+                for (int p = 0; p < kPer / 2; ++p) {
+                    const int at = (r * kPer + 2 * p) * BITS / 8;      // byte of the lane's part
+                    const uint32_t w = raw.w[at / 4];
+                    if constexpr (BITS == 8)
+                        pair[r][p] = __builtin_bit_cast(
+                            uint32_t, at % 4 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, f, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, f, false));
+                    else
+                        pair[r][p] = __builtin_bit_cast(
+                            uint32_t, at % 4 == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 0)
+                                      : at % 4 == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 1)
+                                      : at % 4 == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 2)
+                                                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 3));
+                }
+            }
+            // (column 2p, column 2p + 1) by token -> (token 2i, token 2i + 1) by column
+#pragma unroll
+            for (int p = 0; p < kPer / 2; ++p)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    out[2 * (2 * p) + i] = __builtin_amdgcn_perm(pair[2 * i + 1][p], pair[2 * i][p], 0x05040100u);
+                    out[2 * (2 * p + 1) + i] = __builtin_amdgcn_perm(pair[2 * i + 1][p], pair[2 * i][p], 0x07060302u);
+                }
+        }
+    }
+};
+
+// Everything one wave needs of a step's tile: where it lies and how many of its
+// 16 tokens count (a prefix of them).
+struct TileRef {
+    int64_t tile;
+    int n;
+};
+
+// Tile `a` (16-token index within its sequence or prefix) of the page list.
+__device__ __forceinline__ TileRef tile_ref(const AttnArgs& A, const int32_t* pages, int a, int end, int h)
+{
+    TileRef t;
+    const int t0 = a * nma::kTile;
+    t.n = min(max(end - t0, 0), nma::kTile);
+    int page = 0;
+    if (t.n > 0) {
+        page = pages[t0 >> A.page_shift];
+        if (page < 0 || page >= A.n_pages) {        // not followed: its tokens are absent
+            page = 0;
+            t.n = 0;
+        }
+    }
+    page = __builtin_amdgcn_readfirstlane(page);
+    t.n = __builtin_amdgcn_readfirstlane(t.n);
+    const int per = 1 << (A.page_shift - 4);
+    t.tile = ((int64_t)page * A.heads + h) * per + (a & (per - 1));
+    return t;
+}
+
+// One unit: 16 MT rows from row0 of the R rows of key head h, tokens
+// [start, end) of the page list.  Rows are query heads: row r is head h G + r of
+// sequence b0 + r / G (own-token units have R = G rows of one sequence).
+template <int DT, int BITS, int D, int MT>
+__device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, int h, int b0, int row0, int R,
+                                       int start, int end, bool direct, int64_t part_row, float* lds)
+{
+    using C = Cache<BITS, D>;
+    constexpr int kSteps = D / 32;                                   // k-steps of the score product
+    constexpr int kOp = BITS == 16 ? DT : NM_BF16;                   // operand type
+    constexpr bool kSplit = BITS != 16 && DT == NM_FP16;             // fp16 rows as two bfloat16 parts
+    constexpr int kPer = D / 16;
+    const int lane = threadIdx.x % 64, m = lane % 16, kg = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+
+    // The lane's row of each row tile, as right operands of the score product.
+    u32x4 q_hi[MT][kSteps], q_lo[kSplit ? MT : 1][kSplit ? kSteps : 1];
+#pragma unroll
+    for (int g = 0; g < MT; ++g) {
+        const int r = row0 + 16 * g + m;
+        const uint16_t* row =
+            A.q + (int64_t)(b0 + r / A.G) * A.q_stride + (int64_t)(h * A.G + r % A.G) * D;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            u32x4 x = {0u, 0u, 0u, 0u};
+            if (r < R)
+                x = *reinterpret_cast<const u32x4*>(row + C::column(s, kg));
+            if constexpr (kSplit) {
+                // fp16 = the nearest bfloat16 plus a remainder that bfloat16 holds exactly
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x2 p = unpack2<NM_FP16>(x[i]);
+                    const uint32_t hi = pack2<NM_BF16>(p.x, p.y);
+                    const f32x2 back = unpack2<NM_BF16>(hi);
+                    q_hi[g][s][i] = hi;
+                    q_lo[g][s][i] = pack2<NM_BF16>(p.x - back.x, p.y - back.y);
+                }
+            } else {
+                q_hi[g][s] = x;
+            }
+        }
+    }
+
+    f32x4 acc[MT][kPer];
+    float mx[MT], sum[MT];
+#pragma unroll
+    for (int g = 0; g < MT; ++g) {
+        mx[g] = NM_NEG_INF;
+        sum[g] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            acc[g][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    typename C::Raw kr[2], vr[2];
+    typename C::KScale ks[2];
+    uint32_t vs[2] = {0u, 0u};
+    TileRef cur[2], next[2];
+    const auto load_k = [&](const TileRef(&t)[2]) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            C::template load<C::kCb>(kr[u], A.k + t[u].tile * nma::tile_bytes(D, BITS), lane);
+            if constexpr (BITS != 16)
+                C::load_k_scale(ks[u], A.k_scale + t[u].tile * nma::scale_tile_bytes(D), m);
+        }
+    };
+    const auto load_v = [&](const TileRef(&t)[2]) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            C::template load<C::kVb>(vr[u], A.v + t[u].tile * nma::tile_bytes(D, BITS), lane);
+            if constexpr (BITS != 16)
+                C::load_v_scale(vs[u], A.v_scale + t[u].tile * nma::scale_tile_bytes(D), m, kg);
+        }
+    };
+
+    int at = start / nma::kTile + 2 * wave;             // the wave's next pair of tiles
+    const int last = (end + nma::kTile - 1) / nma::kTile;
+    if (at < last) {
+        cur[0] = tile_ref(A, pages, at, end, h);
+        cur[1] = tile_ref(A, pages, at + 1, end, h);
+        load_k(cur);
+        __builtin_amdgcn_sched_barrier(0);              // keys first: they are waited for first
+        load_v(cur);
+    }
+    // One step; with `more`, the loads of the wave's next one (pair `at`) start as
+    // soon as the registers they fill are free.
+    const auto step = [&](auto more) {
+        if constexpr (more()) {
+            next[0] = tile_ref(A, pages, at, end, h);
+            next[1] = tile_ref(A, pages, at + 1, end, h);
+        }
+        // scores
+        f32x4 sc[MT][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int g = 0; g < MT; ++g)
+                sc[g][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const u32x4 a = C::k_operand(kr[u], ks[u], s, kg);
+#pragma unroll
+                for (int g = 0; g < MT; ++g) {
+                    sc[g][u] = mfma<kOp>(a, q_hi[g][s], sc[g][u]);
+                    if constexpr (kSplit)
+                        sc[g][u] = mfma<kOp>(a, q_lo[g][s], sc[g][u]);
+                }
+            }
+        }
+        if constexpr (more())
+            load_k(next);
+        const bool whole = cur[0].n == nma::kTile && cur[1].n == nma::kTile;
+        // softmax weights of the step, as right operands of the second product
+        u32x4 p_hi[MT], p_lo[kSplit ? MT : 1];
+#pragma unroll
+        for (int g = 0; g < MT; ++g) {
+            float top = NM_NEG_INF;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float v = sc[g][u][r] * A.scale;
+                    if (!whole && 4 * kg + r >= cur[u].n)
+                        v = NM_NEG_INF;                 // whatever lies there, NaN included
+                    sc[g][u][r] = v;
+                    top = fmaxf(top, v);
+                }
+            top = fmaxf(mx[g], quarters_max(top));
+            const float base = top == NM_NEG_INF ? 0.0f : top;
+            if (__any(top > mx[g])) {
+                const float f = mx[g] == top ? 1.0f : __builtin_amdgcn_exp2f(mx[g] - base);
+                sum[g] *= f;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    acc[g][j] *= f;
+                mx[g] = top;
+            }
+            float p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[i] = __builtin_amdgcn_exp2f(sc[g][i / 4][i % 4] - base);
+                sum[g] += p[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                p_hi[g][i] = pack2<kOp>(p[2 * i], p[2 * i + 1]);
+                if constexpr (kSplit) {
+                    const f32x2 back = unpack2<NM_BF16>(p_hi[g][i]);
+                    p_lo[g][i] = pack2<NM_BF16>(p[2 * i] - back.x, p[2 * i + 1] - back.y);
+                }
+            }
+        }
+        // values
+        uint32_t vo[2][2 * kPer];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            C::v_operands(vo[u], vr[u], vs[u]);
+        if (!whole) {
+            // a token that does not count may hold anything: 0 * NaN must not reach o
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int left = cur[u].n - 4 * kg;
+                const uint32_t keep[2] = {left >= 2 ? 0xFFFFFFFFu : left == 1 ? 0xFFFFu : 0u,
+                                          left >= 4 ? 0xFFFFFFFFu : left == 3 ? 0xFFFFu : 0u};
+#pragma unroll
+                for (int i = 0; i < 2 * kPer; ++i)
+                    vo[u][i] &= keep[i % 2];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const u32x4 a = {vo[0][2 * j], vo[0][2 * j + 1], vo[1][2 * j], vo[1][2 * j + 1]};
+#pragma unroll
+            for (int g = 0; g < MT; ++g) {
+                acc[g][j] = mfma<kOp>(a, p_hi[g], acc[g][j]);
+                if constexpr (kSplit)
+                    acc[g][j] = mfma<kOp>(a, p_lo[g], acc[g][j]);
+            }
+        }
+        if constexpr (more()) {
+            load_v(next);
+            cur[0] = next[0];
+            cur[1] = next[1];
+        }
+    };
+    if (at < last) {
+        for (at += 2 * nma::kWaves; at < last; at += 2 * nma::kWaves)
+            step(std::true_type());
+        step(std::false_type());
+    }
+#pragma unroll
+    for (int g = 0; g < MT; ++g)
+        sum[g] = quarters_sum(sum[g]);
+
+    // The block's waves are joined two by two through LDS, lane to lane.
+    constexpr int kRegs = MT * (4 * kPer + 2);
+#pragma unroll
+    for (int half = nma::kWaves / 2; half >= 1; half /= 2) {
+        float* box = lds + (wave % half) * kRegs * 64 + lane;
+        if (half < nma::kWaves / 2)
+            __syncthreads();                            // the boxes' last readers are done
+        if (wave >= half && wave < 2 * half) {
+#pragma unroll
+            for (int g = 0; g < MT; ++g) {
+                box[(g * (4 * kPer + 2) + 4 * kPer) * 64] = mx[g];
+                box[(g * (4 * kPer + 2) + 4 * kPer + 1) * 64] = sum[g];
+#pragma unroll
+                for (int i = 0; i < 4 * kPer; ++i)
+                    box[(g * (4 * kPer + 2) + i) * 64] = acc[g][i / 4][i % 4];
+            }
+        }
+        __syncthreads();
+        if (wave < half) {
+#pragma unroll
+            for (int g = 0; g < MT; ++g) {
+                const float om = box[(g * (4 * kPer + 2) + 4 * kPer) * 64];
+                const float os = box[(g * (4 * kPer + 2) + 4 * kPer + 1) * 64];
+                const float top = fmaxf(mx[g], om), base = top == NM_NEG_INF ? 0.0f : top;
+                const float f0 = __builtin_amdgcn_exp2f(mx[g] - base), f1 = __builtin_amdgcn_exp2f(om - base);
+                sum[g] = sum[g] * f0 + os * f1;
+                mx[g] = top;
+#pragma unroll
+                for (int i = 0; i < 4 * kPer; ++i)
+                    acc[g][i / 4][i % 4] = acc[g][i / 4][i % 4] * f0 + box[(g * (4 * kPer + 2) + i) * 64] * f1;
+            }
+        }
+    }
+    if (wave != 0)
+        return;
+    // The lane holds columns kg D/4 + r D/16 + j of its row in acc[j][r].
+#pragma unroll
+    for (int g = 0; g < MT; ++g) {
+        const int r = row0 + 16 * g + m;
+        if (r >= R)
+            continue;
+        if (direct) {
+            const float f = sum[g] > 0.0f || sum[g] != sum[g] ? 1.0f / sum[g] : 0.0f;
+            const int64_t row = (int64_t)b0 * A.Hq + h * A.G + r;
+            uint16_t* o = A.o + row * D + kg * (D / 4);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int j = 0; j < kPer; j += 4)
+                    *reinterpret_cast<u32x2*>(o + c * kPer + j) =
+                        u32x2{pack2<DT>(acc[g][j][c] * f, acc[g][j + 1][c] * f),
+                              pack2<DT>(acc[g][j + 2][c] * f, acc[g][j + 3][c] * f)};
+            if (A.lse && kg == 0)
+                A.lse[row] = (mx[g] + __builtin_amdgcn_logf(sum[g])) * kLn2;
+        } else {
+            const int64_t row = part_row + r;
+            float* o = A.part_o + row * D + kg * (D / 4);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int j = 0; j < kPer; j += 4)
+                    *reinterpret_cast<f32x4*>(o + c * kPer + j) =
+                        f32x4{acc[g][j][c], acc[g][j + 1][c], acc[g][j + 2][c], acc[g][j + 3][c]};
+            if (kg == 0)
+                A.part_ml[row] = f32x2{mx[g], sum[g]};
+        }
+    }
+}
+
+constexpr int join_floats(int D, int mt) { return nma::kWaves / 2 * mt * (D / 4 + 2) * 64; }
+
+// Prefix units: block = (row group, range, key head).
+template <int DT, int BITS, int D, int MT>
+__global__ __launch_bounds__(nma::kWaves * 64, 2) void prefix_kernel(const AttnArgs A)
+{
+    __shared__ float lds[join_floats(D, MT)];
+    const int h = blockIdx.x % A.heads, split = blockIdx.x / A.heads % A.prefix_splits;
+    const int group = blockIdx.x / A.heads / A.prefix_splits;
+    const int start = split * A.prefix_chunk, end = min(start + A.prefix_chunk, A.prefix_len);
+    attend<DT, BITS, D, MT>(A, A.prefix_pages, h, 0, group * 16 * MT, A.prefix_rows, start, end, false,
+                            ((int64_t)split * A.heads + h) * A.prefix_rows, lds);
+}
+
+// Own-token units: block = (range, row group, key head, sequence).
+template <int DT, int BITS, int D>
+__global__ __launch_bounds__(nma::kWaves * 64, 2) void own_kernel(const AttnArgs A, int direct)
+{
+    __shared__ float lds[join_floats(D, 1)];
+    const int h = blockIdx.x % A.heads, b = blockIdx.x / A.heads % A.B;
+    const int group = blockIdx.x / A.heads / A.B % A.own_groups, split = blockIdx.x / A.heads / A.B / A.own_groups;
+    const int len = min(A.lens[b], A.max_len);
+    if (len < 0)
+        return;
+    const int start = split * A.own_chunk;
+    if (start >= len && !direct)                // combine looks at the ranges that hold tokens only
+        return;
+    const int end = min(start + A.own_chunk, len);
+    attend<DT, BITS, D, 1>(A, A.page_table + (int64_t)b * A.table_stride, h, b, group * 16, A.G, start, end, direct != 0,
+                           A.own_base + ((int64_t)split * A.B + b) * A.Hq + (int64_t)h * A.G, lds);
+}
+
+// Joins the partial results of each row: a wave takes one (sequence, head).
+template <int DT, int D>
+__global__ __launch_bounds__(256) void combine_kernel(const AttnArgs A)
+{
+    constexpr int kCols = D / 64;
+    const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    const int lane = threadIdx.x % 64;
+    if (row >= (int64_t)A.B * A.Hq)
+        return;
+    const int b = (int)(row / A.Hq), hq = (int)(row % A.Hq);
+    const int len = min(A.lens[b], A.max_len);
+    if (len < 0)
+        return;
+    const int own = (len + A.own_chunk - 1) / A.own_chunk, total = A.prefix_splits + own;
+    const auto part = [&](int i) -> int64_t {
+        return i < A.prefix_splits
+                   ? ((int64_t)i * A.heads + hq / A.G) * A.prefix_rows + (int64_t)b * A.G + hq % A.G
+                   : A.own_base + ((int64_t)(i - A.prefix_splits) * A.B + b) * A.Hq + hq;
+    };
+    float mx = NM_NEG_INF, sum = 0.0f, acc[kCols] = {};
+    for (int i = 0; i < total; ++i)
+        mx = fmaxf(mx, A.part_ml[part(i)].x);
+    const float base = mx == NM_NEG_INF ? 0.0f : mx;
+    for (int i = 0; i < total; ++i) {
+        const int64_t p = part(i);
+        const f32x2 ml = A.part_ml[p];
+        const float f = __builtin_amdgcn_exp2f(ml.x - base);
+        sum += ml.y * f;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+            acc[c] += A.part_o[p * D + lane * kCols + c] * f;
+    }
+    const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c)
+        acc[c] *= f;
+    uint16_t* o = A.o + row * D + lane * kCols;
+    if constexpr (kCols == 1)
+        *o = (uint16_t)pack2<DT>(acc[0], 0.0f);
+    else
+#pragma unroll
+        for (int c = 0; c < kCols; c += 2)
+            *reinterpret_cast<uint32_t*>(o + c) = pack2<DT>(acc[c], acc[c + 1]);
+    if (A.lse && lane == 0)
+        A.lse[row] = (mx + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+template <int DT, int BITS, int D>
+int launch(const nma::AttnPlan& P, const AttnArgs& A, hipStream_t s)
+{
+    (void)hipGetLastError();
+    const dim3 block(nma::kWaves * 64);
+    if (P.prefix_splits > 0) {
+        const int64_t blocks = P.prefix_groups * P.prefix_splits * A.heads;
+        if (blocks > INT32_MAX)
+            return NM_ERR_BAD_SHAPE;
+        const dim3 grid((unsigned)blocks);
+        if (P.mt == 1)
+            hipLaunchKernelGGL((prefix_kernel<DT, BITS, D, 1>), grid, block, 0, s, A);
+        else if constexpr (D != 256)
+            hipLaunchKernelGGL((prefix_kernel<DT, BITS, D, 2>), grid, block, 0, s, A);
+    }
+    const int64_t own_blocks = (P.direct ? 1 : P.own_splits) * P.own_groups * A.B * (int64_t)A.heads;
+    if (own_blocks > INT32_MAX)
+        return NM_ERR_BAD_SHAPE;
+    if (own_blocks > 0)
+        hipLaunchKernelGGL((own_kernel<DT, BITS, D>), dim3((unsigned)own_blocks), block, 0, s, A, P.direct ? 1 : 0);
+    if (!P.direct)
+        hipLaunchKernelGGL((combine_kernel<DT, D>), dim3((unsigned)nma::ceil_div((int64_t)A.B * A.Hq, 4)), dim3(256), 0,
+                           s, A);
+    return hip_status(hipGetLastError());
+}
+
+template <int DT, int BITS>
+int launch_width(const nma::AttnPlan& P, const AttnArgs& A, int D, hipStream_t s)
+{
+    switch (D) {
+    case 64: return launch<DT, BITS, 64>(P, A, s);
+    case 128: return launch<DT, BITS, 128>(P, A, s);
+    default: return launch<DT, BITS, 256>(P, A, s);
+    }
+}
+
+template <int DT>
+int launch_format(const nma::AttnPlan& P, const AttnArgs& A, int format, int D, hipStream_t s)
+{
+    switch (format) {
+    case NM_KV_16: return launch_width<DT, 16>(P, A, D, s);
+    case NM_KV_MX8: return launch_width<DT, 8>(P, A, D, s);
+    default: return launch_width<DT, 4>(P, A, D, s);
+    }
+}
+
+}  // namespace
+
+int nmk::attn_decode(const nma::AttnPlan& plan, const void* q, int64_t q_stride, int64_t B, int Hq,
+                     const nm_kv_cache& cache, const int32_t* prefix_pages, int64_t prefix_len,
+                     const int32_t* page_table, int64_t table_stride, const int32_t* lens, int64_t max_len, float scale,
+                     void* o, float* lse, void* workspace, void* stream)
+{
+    AttnArgs A;
+    A.q = static_cast<const uint16_t*>(q);
+    A.k = static_cast<const uint8_t*>(cache.k);
+    A.v = static_cast<const uint8_t*>(cache.v);
+    A.k_scale = cache.k_scale;
+    A.v_scale = cache.v_scale;
+    A.prefix_pages = prefix_pages;
+    A.page_table = page_table;
+    A.lens = lens;
+    A.o = static_cast<uint16_t*>(o);
+    A.lse = lse;
+    A.part_o = static_cast<float*>(workspace);
+    A.part_ml = reinterpret_cast<f32x2*>(A.part_o + (plan.prefix_parts + plan.own_parts) * cache.D);
+    A.q_stride = B > 1 ? q_stride : 0;
+    A.table_stride = B > 1 && max_len > 0 ? table_stride : 0;
+    A.n_pages = cache.n_pages;
+    A.own_base = plan.prefix_parts;
+    A.B = (int)B;
+    A.Hq = Hq;
+    A.heads = cache.heads;
+    A.G = plan.G;
+    A.page_shift = __builtin_ctz((unsigned)cache.page_size);
+    A.prefix_len = (int)prefix_len;
+    A.max_len = (int)max_len;
+    A.prefix_rows = (int)plan.prefix_rows;
+    A.prefix_groups = (int)plan.prefix_groups;
+    A.prefix_splits = (int)plan.prefix_splits;
+    A.prefix_chunk = (int)plan.prefix_chunk;
+    A.own_groups = (int)plan.own_groups;
+    A.own_splits = (int)plan.own_splits;
+    A.own_chunk = (int)plan.own_chunk;
+    A.scale = scale * kLog2e;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return cache.dtype == NM_FP16 ? launch_format<NM_FP16>(plan, A, cache.format, cache.D, s)
+                                  : launch_format<NM_BF16>(plan, A, cache.format, cache.D, s);
+}
