@@ -105,7 +105,7 @@ int64_t nm_kv_scale_bytes(int64_t n_pages, int page_size, int heads, int D, int 
  * into slot slots[t] (int64, 8-byte aligned).  A slot outside the cache (a
  * negative one: a padding row) is skipped.  Each slot at most once a call: one
  * that is listed twice ends with some mixture of its rows.  All other slots
- * keep their contents.  T below 2^31.
+ * keep their contents.  T below 2^31, T * heads * D below 2^40 (nm_kv_read too).
  */
 int nm_kv_write(const nm_kv_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t T,
                 const int64_t* slots, void* stream);

@@ -6,7 +6,6 @@ rows may be strided (views of a fused q+k+v buffer).  Work runs on ``stream``
 (default: the current stream of the tensors' device); results and workspaces
 that a call allocates belong to that stream.
 """
-import contextlib
 import ctypes
 import math
 
@@ -24,51 +23,70 @@ def _dtype(dtype):
     return _DT[dtype]
 
 
-def _check(t, name, device, dtype, shape=None, contiguous=True):
-    """t is a tensor on `device` with `dtype` (and `shape`, None entries free)."""
+def _refuse(t, name, device, dtype, shape, contiguous):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape))):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple('*' if s is None else s for s in shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _check(t, name, device, dtype, shape, contiguous=True):
+    """t is a tensor on the GPU `device` with `dtype` and `shape`."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and t.dtype == dtype and t.shape == shape and
+            (not contiguous or t.is_contiguous())):
+        _refuse(t, name, device, dtype, shape, contiguous)
+
+
+def _size(t, name, dims):
+    """The shape of a tensor of `dims` dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
+    return t.shape
 
 
 def _rows(t, name, device, dtype, shape):
-    """Row stride of strided rows [rows][heads][D]."""
+    """Row stride of strided rows [rows][heads][D] of that shape."""
     _check(t, name, device, dtype, shape, contiguous=False)
-    rows, heads, D = t.shape
+    rows, heads, D = shape
+    if t.is_contiguous():
+        return heads * D
     s0, s1, s2 = t.stride()
-    if rows and heads and ((D > 1 and s2 != 1) or (heads > 1 and s1 != D) or (rows > 1 and s0 < heads * D)):
+    if (D > 1 and s2 != 1) or (heads > 1 and s1 != D) or (rows > 1 and s0 < heads * D):
         raise ValueError(f"{name}: heads and columns must be contiguous, rows must not overlap")
-    return max(s0, heads * D) if rows <= 1 else s0
+    return s0 if rows > 1 else heads * D
 
 
 class _On:
-    """Makes `device` current and finds the stream to launch on; torch's
-    allocator hands out memory of that stream inside."""
+    """Makes `device` and the stream to launch on current (torch's allocator
+    then hands out memory of that stream); gives the stream's handle."""
+
+    __slots__ = ("guards", "handle")
 
     def __init__(self, device, stream):
-        self.device = device
-        self.stack = contextlib.ExitStack()
-        if device.index != torch.cuda.current_device():
-            self.stack.enter_context(torch.cuda.device(device))
+        self.guards = []
         if stream is not None:
             if stream.device != device:
                 raise ValueError(f"stream is on {stream.device}, not on {device}")
-            self.stack.enter_context(torch.cuda.stream(stream))
+            self.guards.append(torch.cuda.stream(stream))       # sets the device as well
+        elif device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        for g in self.guards:
+            g.__enter__()
         self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
     def __enter__(self):
         return self.handle
 
     def __exit__(self, *exc):
-        return self.stack.__exit__(*exc)
+        for g in self.guards:
+            g.__exit__(*exc)
 
 
 def _call(name, *args):
@@ -84,16 +102,15 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, interlea
     len(inv_freq), further columns are not turned.  positions int32 [T],
     inv_freq float32.  Returns (q, k), contiguous; ``out`` is such a pair, and
     may be (q, k) themselves."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
-        raise TypeError("q must be a CUDA (HIP) tensor [T][heads][D]")
+    T, hq, D = _size(q, "q", 3)
+    hk = _size(k, "k", 3)[1]
+    pairs, = _size(inv_freq, "inv_freq", 1)
     dev, dt = q.device, q.dtype
     code = _dtype(dt)
-    T, hq, D = q.shape
-    qs = _rows(q, "q", dev, dt, (T, None, D))
-    ks = _rows(k, "k", dev, dt, (T, None, D))
-    hk = k.shape[1]
+    qs = _rows(q, "q", dev, dt, (T, hq, D))
+    ks = _rows(k, "k", dev, dt, (T, hk, D))
     _check(positions, "positions", dev, torch.int32, (T,))
-    _check(inv_freq, "inv_freq", dev, torch.float32, (None,))
+    _check(inv_freq, "inv_freq", dev, torch.float32, (pairs,))
     for w, name in ((wq, "wq"), (wk, "wk")):
         if w is not None:
             _check(w, name, dev, dt, (D,))
@@ -105,7 +122,7 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, interlea
             out = (torch.empty((T, hq, D), dtype=dt, device=dev), torch.empty((T, hk, D), dtype=dt, device=dev))
         _call("nm_qk_norm_rope", q.data_ptr(), qs, k.data_ptr(), ks, T, hq, hk, D, code,
               None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), eps, positions.data_ptr(),
-              inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(bool(interleaved)), out[0].data_ptr(),
+              inv_freq.data_ptr(), 2 * pairs, int(bool(interleaved)), out[0].data_ptr(),
               out[1].data_ptr(), handle)
     return out[0], out[1]
 
@@ -169,26 +186,28 @@ def kv_write(cache, k, v, slots, stream=None):
     to the cache's format.  A negative slot, or one behind the last, is
     skipped; no slot twice in one call."""
     c = _cache(cache)
-    _check(slots, "slots", c.device, torch.int64, (None,))
-    shape = (slots.shape[0], c.heads, c.D)
+    T, = _size(slots, "slots", 1)
+    _check(slots, "slots", c.device, torch.int64, (T,))
+    shape = (T, c.heads, c.D)
     ks, vs = _rows(k, "k", c.device, c.dtype, shape), _rows(v, "v", c.device, c.dtype, shape)
     with _On(c.device, stream) as handle:
-        _call("nm_kv_write", c._ref, k.data_ptr(), ks, v.data_ptr(), vs, shape[0], slots.data_ptr(), handle)
+        _call("nm_kv_write", c._ref, k.data_ptr(), ks, v.data_ptr(), vs, T, slots.data_ptr(), handle)
 
 
 def kv_read(cache, slots, out=None, stream=None):
     """(k, v) [T][heads][D] in the cache's dtype from slots (int64 [T]); zeros
     for a slot outside the cache."""
     c = _cache(cache)
-    _check(slots, "slots", c.device, torch.int64, (None,))
-    shape = (slots.shape[0], c.heads, c.D)
+    T, = _size(slots, "slots", 1)
+    _check(slots, "slots", c.device, torch.int64, (T,))
+    shape = (T, c.heads, c.D)
     if out is not None:
         _check(out[0], "out[0]", c.device, c.dtype, shape)
         _check(out[1], "out[1]", c.device, c.dtype, shape)
     with _On(c.device, stream) as handle:
         if out is None:
             out = tuple(torch.empty(shape, dtype=c.dtype, device=c.device) for _ in range(2))
-        _call("nm_kv_read", c._ref, slots.data_ptr(), shape[0], out[0].data_ptr(), out[1].data_ptr(), handle)
+        _call("nm_kv_read", c._ref, slots.data_ptr(), T, out[0].data_ptr(), out[1].data_ptr(), handle)
     return out[0], out[1]
 
 
@@ -215,31 +234,33 @@ def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, pre
     sum.  ``ws``: an attn_workspace(), or None to allocate one."""
     c = _cache(cache)
     dev, dt = c.device, c.dtype
-    qs = _rows(q, "q", dev, dt, (None, None, c.D))
-    B, hq = q.shape[:2]
+    B, hq, _ = _size(q, "q", 3)
+    qs = _rows(q, "q", dev, dt, (B, hq, c.D))
     _check(lens, "lens", dev, torch.int32, (B,))
-    table, stride = None, 0
+    table, stride, width = None, 0, 0
     if page_table is not None:
-        _check(page_table, "page_table", dev, torch.int32, (B, None), contiguous=False)
-        stride = page_table.shape[1] if B <= 1 else page_table.stride(0)
-        if page_table.shape[1] > 1 and page_table.stride(1) != 1:
-            raise ValueError("page_table rows must be contiguous")
-        table, width = page_table.data_ptr(), page_table.shape[1] * c.page_size
-    else:
-        width = 0
+        width = _size(page_table, "page_table", 2)[1]
+        _check(page_table, "page_table", dev, torch.int32, (B, width), contiguous=False)
+        stride = width
+        if not page_table.is_contiguous():
+            if width > 1 and page_table.stride(1) != 1:
+                raise ValueError("page_table rows must be contiguous")
+            stride = page_table.stride(0)
+        table, width = page_table.data_ptr(), width * c.page_size
     max_len = width if max_len is None else max_len
     if max_len > width:
         raise ValueError(f"max_len {max_len} is more than page_table holds ({width} tokens)")
-    if prefix_pages is not None:
-        _check(prefix_pages, "prefix_pages", dev, torch.int32, (None,))
-    if prefix_len > (0 if prefix_pages is None else prefix_pages.shape[0] * c.page_size):
-        raise ValueError(f"prefix_len {prefix_len} is more than prefix_pages holds")
+    if prefix_len:
+        n, = _size(prefix_pages, "prefix_pages", 1)
+        _check(prefix_pages, "prefix_pages", dev, torch.int32, (n,))
+        if prefix_len > n * c.page_size:
+            raise ValueError(f"prefix_len {prefix_len} is more than prefix_pages holds ({n * c.page_size} tokens)")
     if out is not None:
         _check(out, "out", dev, dt, (B, hq, c.D))
     if lse is not None:
         _check(lse, "lse", dev, torch.float32, (B, hq))
     if ws is not None:
-        _check(ws, "ws", dev, torch.uint8, (None,))
+        _check(ws, "ws", dev, torch.uint8, _size(ws, "ws", 1))
     need = attn_lib().nm_attn_workspace_bytes(B, hq, c.heads, c.D, prefix_len, max_len)
     with _On(dev, stream) as handle:
         if out is None:

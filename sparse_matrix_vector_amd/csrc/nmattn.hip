@@ -537,42 +537,70 @@ __global__ __launch_bounds__(nma::kWaves * 64, 2) void own_kernel(const AttnArgs
                            A.own_base + ((int64_t)split * A.B + b) * A.Hq + (int64_t)h * A.G, lds);
 }
 
-// Joins the partial results of each row: a wave takes one (sequence, head).
+// Joins the partial results of each row: a block takes one (sequence, head).
+// The parts' weights are found by all threads at once and kept in LDS; then each
+// wave adds up a quarter of the parts, whose loads do not wait for each other.
+constexpr int kMaxParts = 2048;                 // of a row; the plan makes at most 4 kCus
+
 template <int DT, int D>
 __global__ __launch_bounds__(256) void combine_kernel(const AttnArgs A)
 {
     constexpr int kCols = D / 64;
-    const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
-    const int lane = threadIdx.x % 64;
-    if (row >= (int64_t)A.B * A.Hq)
-        return;
-    const int b = (int)(row / A.Hq), hq = (int)(row % A.Hq);
+    typedef float cols __attribute__((ext_vector_type(kCols)));
+    __shared__ float weight[kMaxParts], red[8], box[3 * D];
+    const int b = blockIdx.x / A.Hq, hq = blockIdx.x % A.Hq;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int len = min(A.lens[b], A.max_len);
     if (len < 0)
         return;
-    const int own = (len + A.own_chunk - 1) / A.own_chunk, total = A.prefix_splits + own;
-    const auto part = [&](int i) -> int64_t {
-        return i < A.prefix_splits
-                   ? ((int64_t)i * A.heads + hq / A.G) * A.prefix_rows + (int64_t)b * A.G + hq % A.G
-                   : A.own_base + ((int64_t)(i - A.prefix_splits) * A.B + b) * A.Hq + hq;
-    };
-    float mx = NM_NEG_INF, sum = 0.0f, acc[kCols] = {};
-    for (int i = 0; i < total; ++i)
-        mx = fmaxf(mx, A.part_ml[part(i)].x);
-    const float base = mx == NM_NEG_INF ? 0.0f : mx;
-    for (int i = 0; i < total; ++i) {
-        const int64_t p = part(i);
-        const f32x2 ml = A.part_ml[p];
-        const float f = __builtin_amdgcn_exp2f(ml.x - base);
-        sum += ml.y * f;
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-            acc[c] += A.part_o[p * D + lane * kCols + c] * f;
+    const int np = A.prefix_splits, total = np + (len + A.own_chunk - 1) / A.own_chunk;
+    const int64_t first_p = (int64_t)(hq / A.G) * A.prefix_rows + (int64_t)b * A.G + hq % A.G;
+    const int64_t step_p = (int64_t)A.heads * A.prefix_rows, step_o = (int64_t)A.B * A.Hq;
+    const int64_t first_o = A.own_base + (int64_t)b * A.Hq + hq - np * step_o;
+    const auto part = [&](int i) { return i < np ? first_p + i * step_p : first_o + i * step_o; };
+
+    float mx = NM_NEG_INF;
+    for (int i = threadIdx.x; i < total; i += 256) {
+        const float m = A.part_ml[part(i)].x;
+        weight[i] = m;
+        mx = fmaxf(mx, m);
     }
-    const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
 #pragma unroll
-    for (int c = 0; c < kCols; ++c)
-        acc[c] *= f;
+    for (int i = 1; i < 64; i *= 2)
+        mx = fmaxf(mx, __shfl_xor(mx, i));
+    if (lane == 0)
+        red[wave] = mx;
+    __syncthreads();
+    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float base = mx == NM_NEG_INF ? 0.0f : mx;
+    float sum = 0.0f;
+    for (int i = threadIdx.x; i < total; i += 256) {
+        const float f = __builtin_amdgcn_exp2f(weight[i] - base);
+        weight[i] = f;
+        sum += A.part_ml[part(i)].y * f;
+    }
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2)
+        sum += __shfl_xor(sum, i);
+    if (lane == 0)
+        red[4 + wave] = sum;
+    __syncthreads();
+    sum = (red[4] + red[5]) + (red[6] + red[7]);
+
+    cols acc = {};
+#pragma unroll 4
+    for (int i = wave; i < total; i += 4)
+        acc += *reinterpret_cast<const cols*>(A.part_o + part(i) * D + lane * kCols) * weight[i];
+    if (wave > 0)
+        *reinterpret_cast<cols*>(box + (wave - 1) * D + lane * kCols) = acc;
+    __syncthreads();
+    if (wave > 0)
+        return;
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+        acc += *reinterpret_cast<const cols*>(box + w * D + lane * kCols);
+    acc *= sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    const int64_t row = blockIdx.x;
     uint16_t* o = A.o + row * D + lane * kCols;
     if constexpr (kCols == 1)
         *o = (uint16_t)pack2<DT>(acc[0], 0.0f);
@@ -580,7 +608,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const AttnArgs A)
 #pragma unroll
         for (int c = 0; c < kCols; c += 2)
             *reinterpret_cast<uint32_t*>(o + c) = pack2<DT>(acc[c], acc[c + 1]);
-    if (A.lse && lane == 0)
+    if (A.lse && threadIdx.x == 0)
         A.lse[row] = (mx + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
@@ -605,8 +633,7 @@ int launch(const nma::AttnPlan& P, const AttnArgs& A, hipStream_t s)
     if (own_blocks > 0)
         hipLaunchKernelGGL((own_kernel<DT, BITS, D>), dim3((unsigned)own_blocks), block, 0, s, A, P.direct ? 1 : 0);
     if (!P.direct)
-        hipLaunchKernelGGL((combine_kernel<DT, D>), dim3((unsigned)nma::ceil_div((int64_t)A.B * A.Hq, 4)), dim3(256), 0,
-                           s, A);
+        hipLaunchKernelGGL((combine_kernel<DT, D>), dim3((unsigned)(A.B * A.Hq)), dim3(256), 0, s, A);
     return hip_status(hipGetLastError());
 }
 

@@ -2,9 +2,9 @@
 // the position rotation, and the paged cache's write and read.
 //
 // All three move each byte once and compute little on it; what bounds them is
-// HBM for long prompts and the launch for decode steps.  A thread holds eight
-// consecutive columns (one 16-byte load), so a head is D / 8 neighbouring lanes
-// and its reductions are lane exchanges within a wave.
+// HBM for long prompts and the launch for decode steps (about 3 us).  A thread
+// holds eight consecutive columns (one 16-byte load), so a head is D / 8
+// neighbouring lanes and its reductions are lane exchanges within a wave.
 
 #include <hip/hip_runtime.h>
 
@@ -38,7 +38,10 @@ struct QkArgs {
 
 // LPH lanes (a power of two, at least D / 8) hold one head; a block takes one
 // row's heads hb, hb + blocks_per_row, ... in groups of 256 / LPH.  The row's
-// sines and cosines are computed once per block and kept in LDS.
+// sines and cosines are computed once per block and kept in LDS; a thread's next
+// load is always in flight (16384 rows of 64 + 8 heads, 604 MB: 172 us with each
+// load waited for at once, 121 with the next one started first, 5.0 TB/s, which
+// is what the card copies at).
 //   y = n cos -+ n' sin  with n' the pair's other column: the same thread's for
 // neighbouring pairs, the one rot / 16 lanes away for pairs (i, i + rot / 2).
 template <int DT, int LPH, bool INTERLEAVED>
@@ -48,6 +51,20 @@ __global__ __launch_bounds__(kQkThreads) void qk_kernel(const QkArgs A)
     const int64_t t = blockIdx.x / A.blocks_per_row;
     const int part = blockIdx.x % A.blocks_per_row;
     const int half = A.rot / 2;
+    constexpr int kPerPass = kQkThreads / LPH;
+    const int lane = threadIdx.x % LPH, d0 = lane * 8;
+    const bool live = d0 < A.D;
+    const int total = A.heads[0] + A.heads[1], stride = A.blocks_per_row * kPerPass;
+    const auto load = [&](int hh) {
+        u32x4 raw = {0u, 0u, 0u, 0u};
+        if (live && hh < total) {
+            const int side = hh >= A.heads[0], h = side ? hh - A.heads[0] : hh;
+            raw = *reinterpret_cast<const u32x4*>(A.x[side] + t * A.stride[side] + (int64_t)h * A.D + d0);
+        }
+        return raw;
+    };
+    int hh = part * kPerPass + threadIdx.x / LPH;
+    u32x4 next = load(hh);          // in flight while the sines are computed
     if ((int)threadIdx.x < half) {
         // Turns in double: a position's product with its frequency keeps its phase
         // (fp32 would lose it from some thousand positions on).
@@ -58,26 +75,17 @@ __global__ __launch_bounds__(kQkThreads) void qk_kernel(const QkArgs A)
         cs[1][threadIdx.x] = s;
     }
     __syncthreads();
-    constexpr int kPerPass = kQkThreads / LPH;
-    const int lane = threadIdx.x % LPH, d0 = lane * 8;
-    const bool live = d0 < A.D;
-    const int total = A.heads[0] + A.heads[1];
-    for (int h0 = part * kPerPass; h0 < total; h0 += A.blocks_per_row * kPerPass) {
-        const int hh = h0 + threadIdx.x / LPH;
-        if (hh >= total)            // whole groups of LPH lanes leave together
-            continue;
+    for (; hh < total; hh += stride) {      // whole groups of LPH lanes leave together
+        const u32x4 raw = next;
+        next = load(hh + stride);
         const int side = hh >= A.heads[0];
         const int h = side ? hh - A.heads[0] : hh;
-        float n[8] = {};
-        if (live) {
-            const u32x4 raw =
-                *reinterpret_cast<const u32x4*>(A.x[side] + t * A.stride[side] + (int64_t)h * A.D + d0);
+        float n[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x2 p = unpack2<DT>(raw[i]);
-                n[2 * i] = p.x;
-                n[2 * i + 1] = p.y;
-            }
+        for (int i = 0; i < 4; ++i) {
+            const f32x2 p = unpack2<DT>(raw[i]);
+            n[2 * i] = p.x;
+            n[2 * i + 1] = p.y;
         }
         if (A.w[side]) {
             float ss = 0.0f;
@@ -200,27 +208,38 @@ __device__ __forceinline__ int scale_byte(float top)
     return min(max(e, 1), 254);
 }
 
-// Rows of k (blockIdx.y = 0) and v (1) into their slots: a thread takes eight
-// columns; the four neighbouring lanes that share a scale find it by two
-// exchanges.
-template <int DT, int BITS, int D>
-__global__ __launch_bounds__(kCacheThreads) void kv_write_kernel(const CacheArgs A, const uint16_t* __restrict__ k,
-                                                                 const uint16_t* __restrict__ v, int64_t k_stride,
-                                                                 int64_t v_stride)
+// The cache kernels' work: a wave takes kRows rows by kCols columns, a lane eight
+// columns of one row, of k and of v.  The four neighbouring lanes that share a
+// scale find it by two exchanges.  Eight rows by 64 columns: a row's piece is one
+// cache line on the rows' side, and on the cache's side eight tokens of a tile
+// make up whole lines.  32768 rows of 8 x 128 in MX8, write / read of 65536 back:
+// 4 rows x 128 columns 51 / 85 us, 8 x 64 48 / 81, 16 x 32 51 / 94 (a thread a
+// unit with 64-bit divisions, before: 63 / 128); the card copies at 4.9 TB/s,
+// which would take 41 / 82.
+constexpr int kRows = 8, kCols = 64;
+
+struct Lane {
+    int64_t t;          // row
+    int col;            // column of the row (heads D of them); h and d0 from it
+    bool live;
+};
+
+__device__ __forceinline__ Lane lane_of(int64_t T, int width)
 {
-    constexpr int kUnits = D / 8;
-    const int64_t i = (int64_t)blockIdx.x * kCacheThreads + threadIdx.x;
-    const int64_t row = i / kUnits, t = row / A.heads;
-    const int h = (int)(row % A.heads), d0 = (int)(i % kUnits) * 8;
-    if (t >= A.T)                   // whole heads leave together, and so do the lanes of a scale
-        return;
-    const int64_t slot = A.slots[t];
-    if (slot < 0 || slot >= A.n_slots)
-        return;
-    const int side = blockIdx.y;
-    const u32x4 raw = *reinterpret_cast<const u32x4*>((side ? v + t * v_stride : k + t * k_stride) + (int64_t)h * D + d0);
-    int token;
-    const int64_t tile = tile_of(A, slot, h, token);
+    const uint32_t lane = threadIdx.x % 64, per = (uint32_t)(width + kCols - 1) / kCols;
+    const uint32_t item = blockIdx.x * (kCacheThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const uint32_t group = item / per;          // uniform; cache_grid keeps items in 31 bits
+    Lane l;
+    l.t = (int64_t)group * kRows + lane / (kCols / 8);
+    l.col = (int)(item - group * per) * kCols + (int)(lane % (kCols / 8)) * 8;
+    l.live = l.t < T && l.col < width;
+    return l;
+}
+
+// Eight columns d0 .. d0 + 7 of a token into its tile.
+template <int DT, int BITS, int D>
+__device__ __forceinline__ void write_unit(const CacheArgs& A, int side, int64_t tile, int token, int d0, u32x4 raw)
+{
     uint8_t* dst = A.codes[side] + tile * nma::tile_bytes(D, BITS);
     if constexpr (BITS == 16) {
         if (side == 0) {
@@ -290,6 +309,25 @@ __global__ __launch_bounds__(kCacheThreads) void kv_write_kernel(const CacheArgs
     }
 }
 
+template <int DT, int BITS, int D>
+__global__ __launch_bounds__(kCacheThreads) void kv_write_kernel(const CacheArgs A, const uint16_t* __restrict__ k,
+                                                                 const uint16_t* __restrict__ v, int64_t k_stride,
+                                                                 int64_t v_stride)
+{
+    const Lane l = lane_of(A.T, A.heads * D);
+    if (!l.live)                    // rows and blocks of 32 columns leave whole, and with them the lanes of a scale
+        return;
+    const u32x4 kr = *reinterpret_cast<const u32x4*>(k + l.t * k_stride + l.col);
+    const u32x4 vr = *reinterpret_cast<const u32x4*>(v + l.t * v_stride + l.col);
+    const int64_t slot = A.slots[l.t];
+    if (slot < 0 || slot >= A.n_slots)
+        return;
+    int token;
+    const int64_t tile = tile_of(A, slot, l.col / D, token);
+    write_unit<DT, BITS, D>(A, 0, tile, token, l.col % D, kr);
+    write_unit<DT, BITS, D>(A, 1, tile, token, l.col % D, vr);
+}
+
 // Largest finite value of a 16-bit type, as fp32.
 template <int DT>
 __device__ __forceinline__ float finite_max()
@@ -304,68 +342,75 @@ __device__ __forceinline__ float saturate(float v)
     return v > m ? m : v < -m ? -m : v;         // a NaN stays one
 }
 
-// Slots back to rows: a thread gathers eight columns of k (blockIdx.y = 0) or v.
+// Eight columns of a token out of its tile.
+template <int DT, int BITS, int D>
+__device__ __forceinline__ u32x4 read_unit(const CacheArgs& A, int side, int64_t tile, int token, int d0)
+{
+    u32x4 out = {0u, 0u, 0u, 0u};
+    const uint8_t* src = A.codes[side] + tile * nma::tile_bytes(D, BITS);
+    if constexpr (BITS == 16) {
+        if (side == 0) {
+            out = *reinterpret_cast<const u32x4*>(src + nma::k_offset(D, BITS, token, d0));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                out[j / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(src + nma::v_offset(D, BITS, token, d0 + j))
+                              << (16 * (j % 2));
+        }
+    } else {
+        const int at = side ? nma::v_scale_offset(token, d0 / nma::kBlock) : nma::k_scale_offset(D, token, d0 / nma::kBlock);
+        const uint32_t byte = A.scales[side][tile * nma::scale_tile_bytes(D) + at];
+        float x[8];
+        const int p0 = side ? nma::v_offset(D, BITS, token, d0) : nma::k_offset(D, BITS, token, d0);
+        const int p1 = side ? nma::v_offset(D, BITS, token, d0 + 4) : p0 + 4 * BITS / 8;
+        if constexpr (BITS == 8) {
+            const uint32_t c[2] = {*reinterpret_cast<const uint32_t*>(src + p0),
+                                   *reinterpret_cast<const uint32_t*>(src + p1)};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j], false);
+                const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j], true);
+                x[4 * j] = lo.x, x[4 * j + 1] = lo.y, x[4 * j + 2] = hi.x, x[4 * j + 3] = hi.y;
+            }
+        } else {
+            const uint32_t c = (uint32_t)*reinterpret_cast<const uint16_t*>(src + p0) |
+                               (uint32_t)*reinterpret_cast<const uint16_t*>(src + p1) << 16;
+            const f32x2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0),
+                                __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1),
+                                __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2),
+                                __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x[2 * j] = p[j].x, x[2 * j + 1] = p[j].y;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = byte == 255u ? scale_value(byte) : saturate<DT>(ldexpf(x[j], (int)byte - 127));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            out[j] = pack2<DT>(x[2 * j], x[2 * j + 1]);
+    }
+    return out;
+}
+
 template <int DT, int BITS, int D>
 __global__ __launch_bounds__(kCacheThreads) void kv_read_kernel(const CacheArgs A, uint16_t* __restrict__ k,
                                                                 uint16_t* __restrict__ v)
 {
-    constexpr int kUnits = D / 8;
-    const int64_t i = (int64_t)blockIdx.x * kCacheThreads + threadIdx.x;
-    const int64_t row = i / kUnits, t = row / A.heads;
-    const int h = (int)(row % A.heads), d0 = (int)(i % kUnits) * 8;
-    if (t >= A.T)
+    const Lane l = lane_of(A.T, A.heads * D);
+    if (!l.live)
         return;
-    const int64_t slot = A.slots[t];
-    const int side = blockIdx.y;
-    u32x4 out = {0u, 0u, 0u, 0u};
+    const int64_t slot = A.slots[l.t];
+    u32x4 kr = {0u, 0u, 0u, 0u}, vr = {0u, 0u, 0u, 0u};
     if (slot >= 0 && slot < A.n_slots) {
         int token;
-        const int64_t tile = tile_of(A, slot, h, token);
-        const uint8_t* src = A.codes[side] + tile * nma::tile_bytes(D, BITS);
-        if constexpr (BITS == 16) {
-            if (side == 0) {
-                out = *reinterpret_cast<const u32x4*>(src + nma::k_offset(D, BITS, token, d0));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    out[j / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(src + nma::v_offset(D, BITS, token, d0 + j))
-                                  << (16 * (j % 2));
-            }
-        } else {
-            const int at = side ? nma::v_scale_offset(token, d0 / nma::kBlock) : nma::k_scale_offset(D, token, d0 / nma::kBlock);
-            const uint32_t byte = A.scales[side][tile * nma::scale_tile_bytes(D) + at];
-            float x[8];
-            const int p0 = side ? nma::v_offset(D, BITS, token, d0) : nma::k_offset(D, BITS, token, d0);
-            const int p1 = side ? nma::v_offset(D, BITS, token, d0 + 4) : p0 + 4 * BITS / 8;
-            if constexpr (BITS == 8) {
-                const uint32_t c[2] = {*reinterpret_cast<const uint32_t*>(src + p0),
-                                       *reinterpret_cast<const uint32_t*>(src + p1)};
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j], false);
-                    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j], true);
-                    x[4 * j] = lo.x, x[4 * j + 1] = lo.y, x[4 * j + 2] = hi.x, x[4 * j + 3] = hi.y;
-                }
-            } else {
-                const uint32_t c = (uint32_t)*reinterpret_cast<const uint16_t*>(src + p0) |
-                                   (uint32_t)*reinterpret_cast<const uint16_t*>(src + p1) << 16;
-                const f32x2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0),
-                                    __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1),
-                                    __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2),
-                                    __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3)};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x[2 * j] = p[j].x, x[2 * j + 1] = p[j].y;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[j] = byte == 255u ? scale_value(byte) : saturate<DT>(ldexpf(x[j], (int)byte - 127));
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                out[j] = pack2<DT>(x[2 * j], x[2 * j + 1]);
-        }
+        const int64_t tile = tile_of(A, slot, l.col / D, token);
+        kr = read_unit<DT, BITS, D>(A, 0, tile, token, l.col % D);
+        vr = read_unit<DT, BITS, D>(A, 1, tile, token, l.col % D);
     }
-    *reinterpret_cast<u32x4*>((side ? v : k) + row * D + d0) = out;
+    const int64_t at = l.t * A.heads * D + l.col;
+    *reinterpret_cast<u32x4*>(k + at) = kr;
+    *reinterpret_cast<u32x4*>(v + at) = vr;
 }
 
 CacheArgs cache_args(const nm_kv_cache& c, const int64_t* slots, int64_t T)
@@ -407,10 +452,10 @@ int by_cache(const nm_kv_cache& c, Fn fn)
 
 int cache_grid(const nm_kv_cache& c, int64_t T, dim3* grid)
 {
-    const int64_t blocks = nma::ceil_div(T * c.heads * (c.D / 8), kCacheThreads);
-    if (blocks > INT32_MAX)
+    const int64_t items = nma::ceil_div(T, kRows) * nma::ceil_div((int64_t)c.heads * c.D, kCols);
+    if (items > INT32_MAX)
         return NM_ERR_BAD_SHAPE;
-    *grid = dim3((unsigned)blocks, 2);
+    *grid = dim3((unsigned)nma::ceil_div(items, kCacheThreads / 64));
     return NM_OK;
 }
 
