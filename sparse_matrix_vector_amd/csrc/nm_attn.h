@@ -59,22 +59,27 @@ constexpr int v_scale_offset(int token, int block) { return block * kTile + toke
 
 // ---- the plan of nm_attn_decode ----------------------------------------------
 //
-// Work is cut into units of (row group, key head, range of tokens); a block of
-// kWaves waves takes one, its waves take the range's pairs of tiles in turn and
-// add their results up in LDS.  Prefix units: rows are the whole batch's query
-// heads of one key head, in groups of 16 mt; own-token units: one sequence's
-// query heads of one key head, in groups of 16.  Ranges of one row are added up
-// by a second launch (combine), through fp32 partial results in the workspace;
-// with a single range per row there is none and no workspace.
+// Work is cut into units of (row group, key head, range of tokens), one block
+// each.  Own-token units: one sequence's query heads of one key head, 16 rows;
+// the block's kWaves waves take pairs of tiles of the range in turn and add their
+// results up in LDS.  Prefix units: rows are the whole batch's query heads of one
+// key head.  Up to 32 rows they are worked like own-token units (16 mt rows);
+// beyond, a block of `waves` waves holds 16 mt rows in each wave, and all its
+// waves read the range's tiles from LDS, staged once for the block.
+// Ranges of one row are added up by a second launch (combine), through fp32
+// partial results in the workspace; with a single range per row there is none
+// and no workspace.
 constexpr int kWaves = 4;
 constexpr int kStep = 2 * kTile;            // tokens a wave takes at a time
+constexpr int kStaged = 4 * kTile;          // tokens staged at a time
 constexpr int kCus = 256;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxRows = int64_t(1) << 26;      // B * Hq
 
 struct AttnPlan {
     int G;                                        // query heads per key head
-    int mt;                                       // prefix units hold 16 mt rows
+    int mt;                                       // row tiles of a prefix unit's wave
+    int waves;                                    // of a staged prefix unit; 0: worked like own tokens
     int64_t prefix_rows;                          // B * G
     int64_t prefix_groups, prefix_splits, prefix_chunk;
     int64_t own_groups, own_splits, own_chunk;
@@ -107,8 +112,9 @@ inline AttnPlan attn_plan(int64_t B, int Hq, int heads, int D, int64_t prefix_le
     p.G = Hq / heads;
     p.prefix_rows = B * p.G;
     p.mt = p.prefix_rows <= 16 || D == 256 ? 1 : 2;
-    p.prefix_groups = ceil_div(p.prefix_rows, 16 * p.mt);
-    cut(prefix_len, heads * p.prefix_groups, kCus, &p.prefix_splits, &p.prefix_chunk);
+    p.waves = p.prefix_rows <= 16 * p.mt ? 0 : p.prefix_rows <= 64 * p.mt && D != 256 ? 4 : 8;
+    p.prefix_groups = ceil_div(p.prefix_rows, 16 * p.mt * (p.waves ? p.waves : 1));
+    cut(prefix_len, heads * p.prefix_groups, p.waves == 8 ? kCus : 2 * kCus, &p.prefix_splits, &p.prefix_chunk);
     p.own_groups = ceil_div(p.G, 16);
     cut(max_len, B * heads * p.own_groups, 3 * kCus, &p.own_splits, &p.own_chunk);
     p.direct = p.prefix_splits == 0 && p.own_splits <= 1;

@@ -21,6 +21,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <type_traits>
 
@@ -58,7 +59,10 @@ struct AttnArgs {
     int prefix_len, max_len;
     int prefix_rows, prefix_groups, prefix_splits, prefix_chunk;
     int own_groups, own_splits, own_chunk;
-    float scale;                // scale * log2(e): scores are kept in base 2
+    // Scores are kept in base 2: q . k times `scale` = |scale| log2(e) > 0, the sign
+    // (and a scale of zero) being put into q, which is exact.
+    float scale;
+    uint32_t q_and, q_xor;
 };
 
 template <int DT>
@@ -152,25 +156,33 @@ struct Cache {
         if constexpr (BITS == 16) {
             return u32x4{raw.w[4 * s], raw.w[4 * s + 1], raw.w[4 * s + 2], raw.w[4 * s + 3]};
         } else {
+            return k_codes(raw.w + s * BITS / 4, sc, s, kg);
+        }
+    }
+
+    // The same from k-step s's codes (BITS bytes).
+    static __device__ __forceinline__ u32x4 k_codes(const uint32_t* w, const KScale& sc, int s, int kg)
+    {
+        u32x4 out = {0u, 0u, 0u, 0u};
+        if constexpr (BITS != 16) {
             // the block of columns c 4E + kg E + ..: the first part is known here, the second by kg
             const int block = s * 8 / kE * (4 * kE / nma::kBlock) + kg * kE / nma::kBlock;
-            const uint32_t word = kBlocks > 4 ? sc.w[s * 8 / kE * (4 * kE / nma::kBlock) / 4] : sc.w[0];
+            const uint32_t word = kBlocks > 4 && block >= 4 ? sc.w[kBlocks > 4 ? 1 : 0] : sc.w[0];
             const float f = scale_value((word >> (8 * (block % 4))) & 255u);
-            u32x4 out;
             if constexpr (BITS == 8) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     out[i] = __builtin_bit_cast(
-                        uint32_t, i % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw.w[2 * s + i / 2], f, true)
-                                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw.w[2 * s + i / 2], f, false));
+                        uint32_t, i % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i / 2], f, true)
+                                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i / 2], f, false));
             } else {
-                out = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw.w[s], f, 0)),
-                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw.w[s], f, 1)),
-                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw.w[s], f, 2)),
-                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw.w[s], f, 3))};
+                out = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], f, 0)),
+                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], f, 1)),
+                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], f, 2)),
+                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], f, 3))};
             }
-            return out;
         }
+        return out;
     }
 
     // Value operands: out[2 j], out[2 j + 1] = column j of the lane's group, its
@@ -182,34 +194,46 @@ struct Cache {
             for (int i = 0; i < 2 * kPer; ++i)
                 out[i] = raw.w[i];
         } else {
-            uint32_t pair[4][kPer / 2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float f = scale_value((sc >> (8 * r)) & 255u);
+            for (int i = 0; i < 2; ++i) {
+                uint32_t half[kPer];
+                v_codes(half, raw.w + i * kPer * BITS / 16, sc >> (16 * i));
 #pragma unroll
-                for (int p = 0; p < kPer / 2; ++p) {
-                    const int at = (r * kPer + 2 * p) * BITS / 8;      // byte of the lane's part
-                    const uint32_t w = raw.w[at / 4];
-                    if constexpr (BITS == 8)
-                        pair[r][p] = __builtin_bit_cast(
-                            uint32_t, at % 4 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, f, true)
-                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, f, false));
-                    else
-                        pair[r][p] = __builtin_bit_cast(
-                            uint32_t, at % 4 == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 0)
-                                      : at % 4 == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 1)
-                                      : at % 4 == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 2)
-                                                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 3));
-                }
+                for (int j = 0; j < kPer; ++j)
+                    out[2 * j + i] = half[j];
             }
-            // (column 2p, column 2p + 1) by token -> (token 2i, token 2i + 1) by column
+        }
+    }
+
+    // out[j] = column j of the lane's group, tokens (2 i, 2 i + 1), from the pair's
+    // codes (kPer BITS / 4 bytes) and scale bytes (the low two of sc).
+    static __device__ __forceinline__ void v_codes(uint32_t (&out)[kPer], const uint32_t* w, uint32_t sc)
+    {
+        uint32_t pair[2][kPer / 2];
 #pragma unroll
-            for (int p = 0; p < kPer / 2; ++p)
+        for (int r = 0; r < 2; ++r) {
+            const float f = scale_value((sc >> (8 * r)) & 255u);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    out[2 * (2 * p) + i] = __builtin_amdgcn_perm(pair[2 * i + 1][p], pair[2 * i][p], 0x05040100u);
-                    out[2 * (2 * p + 1) + i] = __builtin_amdgcn_perm(pair[2 * i + 1][p], pair[2 * i][p], 0x07060302u);
-                }
+            for (int p = 0; p < kPer / 2; ++p) {
+                const int at = (r * kPer + 2 * p) * BITS / 8;
+                const uint32_t x = w[at / 4];
+                if constexpr (BITS == 8)
+                    pair[r][p] =
+                        __builtin_bit_cast(uint32_t, at % 4 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, f, true)
+                                                            : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, f, false));
+                else
+                    pair[r][p] = __builtin_bit_cast(
+                        uint32_t, at % 4 == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 0)
+                                  : at % 4 == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 1)
+                                  : at % 4 == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 2)
+                                                : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 3));
+            }
+        }
+        // (column 2p, column 2p + 1) by token -> (token 2i, token 2i + 1) by column
+#pragma unroll
+        for (int p = 0; p < kPer / 2; ++p) {
+            out[2 * p] = __builtin_amdgcn_perm(pair[1][p], pair[0][p], 0x05040100u);
+            out[2 * p + 1] = __builtin_amdgcn_perm(pair[1][p], pair[0][p], 0x07060302u);
         }
     }
 };
@@ -242,48 +266,153 @@ __device__ __forceinline__ TileRef tile_ref(const AttnArgs& A, const int32_t* pa
     return t;
 }
 
+// Operand type of both products; fp16 rows against a quantised cache (whose values
+// are bfloat16 operands) are taken as two bfloat16 parts.
+template <int DT, int BITS>
+constexpr int op_type()
+{
+    return BITS == 16 ? DT : NM_BF16;
+}
+template <int DT, int BITS>
+constexpr bool split_rows()
+{
+    return BITS != 16 && DT == NM_FP16;
+}
+
+// The lane's row of each of MT row tiles, as right operands of the score product.
+// Rows are query heads: row r is head h G + r % G of sequence b0 + r / G.
+template <int DT, int BITS, int D, int MT>
+struct Rows {
+    static constexpr int kSteps = D / 32;                            // k-steps of the score product
+    static constexpr bool kSplit = split_rows<DT, BITS>();
+    u32x4 hi[MT][kSteps], lo[kSplit ? MT : 1][kSplit ? kSteps : 1];
+
+    __device__ __forceinline__ void load(const AttnArgs& A, int h, int b0, int row0, int R, int m, int kg)
+    {
+#pragma unroll
+        for (int g = 0; g < MT; ++g) {
+            const int r = row0 + 16 * g + m;
+            const uint16_t* row = A.q + (int64_t)(b0 + r / A.G) * A.q_stride + (int64_t)(h * A.G + r % A.G) * D;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                u32x4 x = {0u, 0u, 0u, 0u};
+                if (r < R)
+                    x = (*reinterpret_cast<const u32x4*>(row + Cache<BITS, D>::column(s, kg)) & A.q_and) ^ A.q_xor;
+                if constexpr (kSplit) {
+                    // fp16 = the nearest bfloat16 plus a remainder that bfloat16 holds exactly
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const f32x2 p = unpack2<NM_FP16>(x[i]);
+                        const uint32_t top = pack2<NM_BF16>(p.x, p.y);
+                        const f32x2 back = unpack2<NM_BF16>(top);
+                        hi[g][s][i] = top;
+                        lo[g][s][i] = pack2<NM_BF16>(p.x - back.x, p.y - back.y);
+                    }
+                } else {
+                    hi[g][s] = x;
+                }
+            }
+        }
+    }
+};
+
+// Scores of tokens that do not count: n[u] of tile u's 16 do.
+template <int MT, int NT>
+__device__ __forceinline__ void mask_scores(f32x4 (&sc)[MT][NT], const int (&n)[NT], int kg)
+{
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (4 * kg + r >= n[u])
+#pragma unroll
+                for (int g = 0; g < MT; ++g)
+                    sc[g][u][r] = NM_NEG_INF;               // whatever lies there, NaN included
+}
+
+// The softmax weights of a step of NT tiles, as right operands of the second
+// product (one for each pair of tiles); updates the rows' maxima, sums and,
+// where a maximum grows, what has been added up so far.
+template <int DT, int BITS, int MT, int NT>
+struct Weights {
+    static constexpr bool kSplit = split_rows<DT, BITS>();
+    u32x4 hi[MT][NT / 2], lo[kSplit ? MT : 1][kSplit ? NT / 2 : 1];
+
+    template <int PER>
+    __device__ __forceinline__ void find(const f32x4 (&sc)[MT][NT], float (&mx)[MT], float (&sum)[MT],
+                                         f32x4 (&acc)[MT][PER], float scale)
+    {
+#pragma unroll
+        for (int g = 0; g < MT; ++g) {
+            float top = NM_NEG_INF;
+#pragma unroll
+            for (int u = 0; u < NT; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    top = fmaxf(top, sc[g][u][r]);
+            top = fmaxf(mx[g], quarters_max(top) * scale);
+            const float base = top == NM_NEG_INF ? 0.0f : top;
+            if (__any(top > mx[g])) {
+                const float f = mx[g] == top ? 1.0f : __builtin_amdgcn_exp2f(mx[g] - base);
+                sum[g] *= f;
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    acc[g][j] *= f;
+                mx[g] = top;
+            }
+#pragma unroll
+            for (int t = 0; t < NT / 2; ++t) {
+                float p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[g][2 * t + i / 4][i % 4], scale, -base));
+                    sum[g] += p[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    hi[g][t][i] = pack2<op_type<DT, BITS>()>(p[2 * i], p[2 * i + 1]);
+                    if constexpr (kSplit) {
+                        const f32x2 back = unpack2<NM_BF16>(hi[g][t][i]);
+                        lo[g][t][i] = pack2<NM_BF16>(p[2 * i] - back.x, p[2 * i + 1] - back.y);
+                    }
+                }
+            }
+        }
+    }
+};
+
+// A row's partial result: the lane holds columns kg D/4 + r D/16 + j in acc[j][r].
+template <int D>
+__device__ __forceinline__ void store_part(const AttnArgs& A, int64_t row, int kg, const f32x4 (&acc)[D / 16], float mx,
+                                           float sum)
+{
+    constexpr int kPer = D / 16;
+    float* o = A.part_o + row * D + kg * (D / 4);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < kPer; j += 4)
+            *reinterpret_cast<f32x4*>(o + c * kPer + j) = f32x4{acc[j][c], acc[j + 1][c], acc[j + 2][c], acc[j + 3][c]};
+    if (kg == 0)
+        A.part_ml[row] = f32x2{mx, sum};
+}
+
 // One unit: 16 MT rows from row0 of the R rows of key head h, tokens
-// [start, end) of the page list.  Rows are query heads: row r is head h G + r of
-// sequence b0 + r / G (own-token units have R = G rows of one sequence).
+// [start, end) of the page list.
 template <int DT, int BITS, int D, int MT>
 __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, int h, int b0, int row0, int R,
                                        int start, int end, bool direct, int64_t part_row, float* lds)
 {
     using C = Cache<BITS, D>;
     constexpr int kSteps = D / 32;                                   // k-steps of the score product
-    constexpr int kOp = BITS == 16 ? DT : NM_BF16;                   // operand type
-    constexpr bool kSplit = BITS != 16 && DT == NM_FP16;             // fp16 rows as two bfloat16 parts
+    constexpr int kOp = op_type<DT, BITS>();
+    constexpr bool kSplit = split_rows<DT, BITS>();
     constexpr int kPer = D / 16;
     const int lane = threadIdx.x % 64, m = lane % 16, kg = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
-    // The lane's row of each row tile, as right operands of the score product.
-    u32x4 q_hi[MT][kSteps], q_lo[kSplit ? MT : 1][kSplit ? kSteps : 1];
-#pragma unroll
-    for (int g = 0; g < MT; ++g) {
-        const int r = row0 + 16 * g + m;
-        const uint16_t* row =
-            A.q + (int64_t)(b0 + r / A.G) * A.q_stride + (int64_t)(h * A.G + r % A.G) * D;
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            u32x4 x = {0u, 0u, 0u, 0u};
-            if (r < R)
-                x = *reinterpret_cast<const u32x4*>(row + C::column(s, kg));
-            if constexpr (kSplit) {
-                // fp16 = the nearest bfloat16 plus a remainder that bfloat16 holds exactly
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x2 p = unpack2<NM_FP16>(x[i]);
-                    const uint32_t hi = pack2<NM_BF16>(p.x, p.y);
-                    const f32x2 back = unpack2<NM_BF16>(hi);
-                    q_hi[g][s][i] = hi;
-                    q_lo[g][s][i] = pack2<NM_BF16>(p.x - back.x, p.y - back.y);
-                }
-            } else {
-                q_hi[g][s] = x;
-            }
-        }
-    }
+    Rows<DT, BITS, D, MT> rows;
+    rows.load(A, h, b0, row0, R, m, kg);
 
     f32x4 acc[MT][kPer];
     float mx[MT], sum[MT];
@@ -345,55 +474,21 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
                 const u32x4 a = C::k_operand(kr[u], ks[u], s, kg);
 #pragma unroll
                 for (int g = 0; g < MT; ++g) {
-                    sc[g][u] = mfma<kOp>(a, q_hi[g][s], sc[g][u]);
+                    sc[g][u] = mfma<kOp>(a, rows.hi[g][s], sc[g][u]);
                     if constexpr (kSplit)
-                        sc[g][u] = mfma<kOp>(a, q_lo[g][s], sc[g][u]);
+                        sc[g][u] = mfma<kOp>(a, rows.lo[g][s], sc[g][u]);
                 }
             }
         }
         if constexpr (more())
             load_k(next);
         const bool whole = cur[0].n == nma::kTile && cur[1].n == nma::kTile;
-        // softmax weights of the step, as right operands of the second product
-        u32x4 p_hi[MT], p_lo[kSplit ? MT : 1];
-#pragma unroll
-        for (int g = 0; g < MT; ++g) {
-            float top = NM_NEG_INF;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float v = sc[g][u][r] * A.scale;
-                    if (!whole && 4 * kg + r >= cur[u].n)
-                        v = NM_NEG_INF;                 // whatever lies there, NaN included
-                    sc[g][u][r] = v;
-                    top = fmaxf(top, v);
-                }
-            top = fmaxf(mx[g], quarters_max(top));
-            const float base = top == NM_NEG_INF ? 0.0f : top;
-            if (__any(top > mx[g])) {
-                const float f = mx[g] == top ? 1.0f : __builtin_amdgcn_exp2f(mx[g] - base);
-                sum[g] *= f;
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    acc[g][j] *= f;
-                mx[g] = top;
-            }
-            float p[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(sc[g][i / 4][i % 4] - base);
-                sum[g] += p[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p_hi[g][i] = pack2<kOp>(p[2 * i], p[2 * i + 1]);
-                if constexpr (kSplit) {
-                    const f32x2 back = unpack2<NM_BF16>(p_hi[g][i]);
-                    p_lo[g][i] = pack2<NM_BF16>(p[2 * i] - back.x, p[2 * i + 1] - back.y);
-                }
-            }
+        if (!whole) {
+            const int n[2] = {cur[0].n, cur[1].n};
+            mask_scores(sc, n, kg);
         }
+        Weights<DT, BITS, MT, 2> w;
+        w.find(sc, mx, sum, acc, A.scale);
         // values
         uint32_t vo[2][2 * kPer];
 #pragma unroll
@@ -416,9 +511,9 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
             const u32x4 a = {vo[0][2 * j], vo[0][2 * j + 1], vo[1][2 * j], vo[1][2 * j + 1]};
 #pragma unroll
             for (int g = 0; g < MT; ++g) {
-                acc[g][j] = mfma<kOp>(a, p_hi[g], acc[g][j]);
+                acc[g][j] = mfma<kOp>(a, w.hi[g][0], acc[g][j]);
                 if constexpr (kSplit)
-                    acc[g][j] = mfma<kOp>(a, p_lo[g], acc[g][j]);
+                    acc[g][j] = mfma<kOp>(a, w.lo[g][0], acc[g][j]);
             }
         }
         if constexpr (more()) {
@@ -491,23 +586,266 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
             if (A.lse && kg == 0)
                 A.lse[row] = (mx[g] + __builtin_amdgcn_logf(sum[g])) * kLn2;
         } else {
-            const int64_t row = part_row + r;
-            float* o = A.part_o + row * D + kg * (D / 4);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int j = 0; j < kPer; j += 4)
-                    *reinterpret_cast<f32x4*>(o + c * kPer + j) =
-                        f32x4{acc[g][j][c], acc[g][j + 1][c], acc[g][j + 2][c], acc[g][j + 3][c]};
-            if (kg == 0)
-                A.part_ml[row] = f32x2{mx[g], sum[g]};
+            store_part<D>(A, part_row + r, kg, acc[g], mx[g], sum[g]);
         }
     }
 }
 
 constexpr int join_floats(int D, int mt) { return nma::kWaves / 2 * mt * (D / 4 + 2) * 64; }
 
-// Prefix units: block = (row group, range, key head).
+// ---- staged prefix units -----------------------------------------------------
+//
+// W waves with 16 MT rows each share every tile of the range: four tiles at a
+// time are loaded by the block (each wave a half or a whole of one tile's keys and
+// values), turned into operands once, and written to LDS in operand order, in two
+// buffers; the next four are on their way while the current ones are multiplied.
+//   keys    [tile][k-step][lane] 16 bytes
+//   values  [tile pair][column j][lane] 16 bytes, 8 of each tile
+template <int BITS, int D, int W>
+struct Stage {
+    using C = Cache<BITS, D>;
+    static constexpr int kTiles = nma::kStaged / nma::kTile;
+    static constexpr int kShare = W / kTiles;                // waves that load one tile
+    static constexpr int kSteps = D / 32, kPer = D / 16;
+    static constexpr int kTileBytes = 32 * D;                // a tile's keys (or values) as operands
+    static constexpr int kBytes = 2 * kTiles * kTileBytes;   // a buffer: all keys, then all values
+    static constexpr int kMine = kSteps / kShare;            // k-steps of keys (and equal parts of values) a wave loads
+    static_assert(kShare == 1 || kShare == 2, "a tile is loaded by one or two waves");
+
+    // Raw loads of one wave.  16-bit: whole 1 KB pieces of the tile.  Codes: keys by
+    // k-step (BITS bytes a lane), values by pairs of tokens.
+    static constexpr int kVPairs = 2 / kShare;               // token pairs (of a lane's two) a wave loads
+    static constexpr int kVBytes = kPer * BITS / 4;          // a lane's bytes of one pair
+    static constexpr int kVLoad = kVBytes < C::kCb ? kVBytes : C::kCb;
+    uint32_t k[BITS == 16 ? 4 * kMine : kMine * BITS / 4];
+    uint32_t v[BITS == 16 ? 4 * kMine : kVPairs * kVBytes / 4];
+    typename C::KScale ks;
+    uint32_t vs;
+    int n;
+
+    template <int BYTES>
+    static __device__ __forceinline__ void get(uint32_t* dst, const uint8_t* src)
+    {
+        typedef uint32_t piece __attribute__((ext_vector_type(BYTES / 4)));
+        if constexpr (BYTES == 4) {
+            dst[0] = *reinterpret_cast<const uint32_t*>(src);
+        } else {
+            const piece x = *reinterpret_cast<const piece*>(src);
+#pragma unroll
+            for (int i = 0; i < BYTES / 4; ++i)
+                dst[i] = x[i];
+        }
+    }
+
+    __device__ __forceinline__ void load(const AttnArgs& A, const TileRef& t, int part, int lane)
+    {
+        const uint8_t* kt = A.k + t.tile * nma::tile_bytes(D, BITS);
+        const uint8_t* vt = A.v + t.tile * nma::tile_bytes(D, BITS);
+        n = t.n;
+        if constexpr (BITS == 16) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                get<16>(k + 4 * i, kt + (part * kMine + i) * 1024 + lane * 16);
+                get<16>(v + 4 * i, vt + (part * kMine + i) * 1024 + lane * 16);
+            }
+        } else {
+            const int m = lane % 16, kg = lane / 16;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int at = (part * kMine + i) * BITS;
+                get<BITS>(k + i * BITS / 4, kt + at / C::kCb * 64 * C::kCb + lane * C::kCb + at % C::kCb);
+            }
+#pragma unroll
+            for (int i = 0; i < kVPairs * kVBytes; i += kVLoad) {
+                const int at = part * kVPairs * kVBytes + i;
+                get<kVLoad>(v + i / 4, vt + at / C::kVb * 64 * C::kVb + lane * C::kVb + at % C::kVb);
+            }
+            C::load_k_scale(ks, A.k_scale + t.tile * nma::scale_tile_bytes(D), m);
+            C::load_v_scale(vs, A.v_scale + t.tile * nma::scale_tile_bytes(D), m, kg);
+        }
+    }
+
+    // Operands of what was loaded into the tile's place in a buffer; values of
+    // tokens that do not count become zeros (0 * NaN must not reach o).
+    __device__ __forceinline__ void put(uint8_t* buf, int tile, int part, int lane) const
+    {
+        uint8_t* kd = buf + tile * kTileBytes;
+        uint8_t* vd = buf + (kTiles + tile / 2 * 2) * kTileBytes + tile % 2 * 8;
+        const int kg = lane / 16;
+        if constexpr (BITS == 16) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                *reinterpret_cast<u32x4*>(kd + (part * kMine + i) * 1024 + lane * 16) =
+                    u32x4{k[4 * i], k[4 * i + 1], k[4 * i + 2], k[4 * i + 3]};
+                u32x4 x = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+                if (n < nma::kTile) {
+                    // 16 bytes here are two lanes' halves of one column: quarter (lane % 32) / 8
+                    const int left = n - 4 * (lane % 32 / 8);
+                    x &= u32x4{keep(left, 0), keep(left, 1), keep(left, 0), keep(left, 1)};
+                }
+                uint8_t* to = vd + ((part * kMine + i) * 128 + lane * 2) * 16;
+                *reinterpret_cast<u32x2*>(to) = u32x2{x.x, x.y};
+                *reinterpret_cast<u32x2*>(to + 16) = u32x2{x.z, x.w};
+            }
+        } else {
+            const int left = n - 4 * kg;
+            // the operand functions take a lane's whole part; what this wave did not load is not used
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+                *reinterpret_cast<u32x4*>(kd + (part * kMine + i) * 1024 + lane * 16) =
+                    C::k_codes(k + i * BITS / 4, ks, part * kMine + i, kg);
+#pragma unroll
+            for (int i = 0; i < kVPairs; ++i) {
+                const int pair = part * kVPairs + i;
+                uint32_t out[kPer];
+                C::v_codes(out, v + i * kVBytes / 4, vs >> (16 * pair));
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    *reinterpret_cast<uint32_t*>(vd + j * 1024 + lane * 16 + pair * 4) = out[j] & keep(left, pair);
+            }
+        }
+    }
+
+    // Mask of the token pair (2 i, 2 i + 1) of a quarter of which `left` tokens count.
+    static __device__ __forceinline__ uint32_t keep(int left, int i)
+    {
+        return left >= 2 * i + 2 ? 0xFFFFFFFFu : left == 2 * i + 1 ? 0xFFFFu : 0u;
+    }
+};
+
+// Block = (row group, range, key head).
+template <int DT, int BITS, int D, int MT, int W>
+__global__ __launch_bounds__(W * 64, 2) void staged_kernel(const AttnArgs A)
+{
+    using S = Stage<BITS, D, W>;
+    constexpr int kOp = op_type<DT, BITS>(), NT = S::kTiles, kSteps = S::kSteps, kPer = S::kPer;
+    constexpr bool kSplit = split_rows<DT, BITS>();
+    constexpr int kGroup = 4;                                // value operands read at a time
+    __shared__ __align__(16) uint8_t buf[2][S::kBytes];
+    __shared__ int count[2][NT];
+    const int lane = threadIdx.x % 64, m = lane % 16, kg = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int h = blockIdx.x % A.heads, split = blockIdx.x / A.heads % A.prefix_splits;
+    const int row0 = ((int)(blockIdx.x / A.heads / A.prefix_splits) * W + wave) * 16 * MT;
+    const int start = split * A.prefix_chunk, end = min(start + A.prefix_chunk, A.prefix_len);
+    const int mine = wave % NT, part = wave / NT;            // the tile of each step that this wave loads
+    const bool busy = row0 < A.prefix_rows;
+
+    Rows<DT, BITS, D, MT> rows;
+    rows.load(A, h, 0, row0, A.prefix_rows, m, kg);
+    f32x4 acc[MT][kPer];
+    float mx[MT], sum[MT];
+#pragma unroll
+    for (int g = 0; g < MT; ++g) {
+        mx[g] = NM_NEG_INF;
+        sum[g] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            acc[g][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    S stage;
+    int at = start / nma::kTile + mine;
+    const int steps = (end - start + nma::kStaged - 1) / nma::kStaged;
+    const auto put = [&](int which) {
+        stage.put(buf[which], mine, part, lane);
+        if (part == 0 && lane == 0)
+            count[which][mine] = stage.n;
+    };
+    stage.load(A, tile_ref(A, A.prefix_pages, at, end, h), part, lane);
+    put(0);
+    TileRef next = tile_ref(A, A.prefix_pages, at + NT, end, h);
+    __syncthreads();
+    for (int i = 0; i < steps; ++i) {
+        const bool more = i + 1 < steps;
+        if (more) {
+            stage.load(A, next, part, lane);
+            at += NT;
+            next = tile_ref(A, A.prefix_pages, at + NT, end, h);
+        }
+        if (busy) {
+            const uint8_t* kb = buf[i & 1];
+            const uint8_t* vb = kb + NT * S::kTileBytes;
+            // Operands are read from LDS one tile (keys) or one group of columns (values)
+            // ahead of the products that use them; the barriers keep the compiler from
+            // moving the reads down to their uses.
+            u32x4 ka[2][kSteps], va[2][kGroup];
+            const auto read_k = [&](int u) {
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+                    ka[u % 2][s] = *reinterpret_cast<const u32x4*>(kb + u * S::kTileBytes + s * 1024 + lane * 16);
+            };
+            const auto read_v = [&](int x) {
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    va[x % 2][j] = *reinterpret_cast<const u32x4*>(vb + (x * kGroup + j) * 1024 + lane * 16);
+            };
+            f32x4 sc[MT][NT];
+            read_k(0);
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                if (u + 1 < NT)
+                    read_k(u + 1);
+                else
+                    read_v(0);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int g = 0; g < MT; ++g)
+                    sc[g][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                    for (int g = 0; g < MT; ++g) {
+                        sc[g][u] = mfma<kOp>(ka[u % 2][s], rows.hi[g][s], sc[g][u]);
+                        if constexpr (kSplit)
+                            sc[g][u] = mfma<kOp>(ka[u % 2][s], rows.lo[g][s], sc[g][u]);
+                    }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            int n[NT];
+            bool whole = true;
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                n[u] = __builtin_amdgcn_readfirstlane(count[i & 1][u]);
+                whole = whole && n[u] == nma::kTile;
+            }
+            if (!whole)
+                mask_scores(sc, n, kg);
+            Weights<DT, BITS, MT, NT> w;
+            w.find(sc, mx, sum, acc, A.scale);
+            constexpr int kGroups = NT / 2 * kPer / kGroup;
+#pragma unroll
+            for (int x = 0; x < kGroups; ++x) {
+                if (x + 1 < kGroups)
+                    read_v(x + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int c = 0; c < kGroup; ++c) {
+                    const int j = (x * kGroup + c) % kPer, t = (x * kGroup + c) / kPer;
+#pragma unroll
+                    for (int g = 0; g < MT; ++g) {
+                        acc[g][j] = mfma<kOp>(va[x % 2][c], w.hi[g][t], acc[g][j]);
+                        if constexpr (kSplit)
+                            acc[g][j] = mfma<kOp>(va[x % 2][c], w.lo[g][t], acc[g][j]);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if (more)
+            put((i + 1) & 1);           // that buffer's readers passed the barrier before this step
+        __syncthreads();
+    }
+#pragma unroll
+    for (int g = 0; g < MT; ++g) {
+        const int r = row0 + 16 * g + m;
+        const float total = quarters_sum(sum[g]);
+        if (r < A.prefix_rows)
+            store_part<D>(A, ((int64_t)split * A.heads + h) * A.prefix_rows + r, kg, acc[g], mx[g], total);
+    }
+}
+
+// Prefix units of few rows: block = (row group, range, key head).
 template <int DT, int BITS, int D, int MT>
 __global__ __launch_bounds__(nma::kWaves * 64, 2) void prefix_kernel(const AttnArgs A)
 {
@@ -622,7 +960,13 @@ int launch(const nma::AttnPlan& P, const AttnArgs& A, hipStream_t s)
         if (blocks > INT32_MAX)
             return NM_ERR_BAD_SHAPE;
         const dim3 grid((unsigned)blocks);
-        if (P.mt == 1)
+        constexpr int kMt = D == 256 ? 1 : 2;       // of the larger units (attn_plan)
+        if (P.waves == 8)
+            hipLaunchKernelGGL((staged_kernel<DT, BITS, D, kMt, 8>), grid, dim3(512), 0, s, A);
+        else if (P.waves == 4) {
+            if constexpr (D != 256)
+                hipLaunchKernelGGL((staged_kernel<DT, BITS, D, kMt, 4>), grid, dim3(256), 0, s, A);
+        } else if (P.mt == 1)
             hipLaunchKernelGGL((prefix_kernel<DT, BITS, D, 1>), grid, block, 0, s, A);
         else if constexpr (D != 256)
             hipLaunchKernelGGL((prefix_kernel<DT, BITS, D, 2>), grid, block, 0, s, A);
@@ -695,7 +1039,9 @@ int nmk::attn_decode(const nma::AttnPlan& plan, const void* q, int64_t q_stride,
     A.own_groups = (int)plan.own_groups;
     A.own_splits = (int)plan.own_splits;
     A.own_chunk = (int)plan.own_chunk;
-    A.scale = scale * kLog2e;
+    A.scale = scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e;
+    A.q_and = scale == 0.0f ? 0u : 0xFFFFFFFFu;
+    A.q_xor = scale < 0.0f ? 0x80008000u : 0u;
     hipStream_t s = static_cast<hipStream_t>(stream);
     return cache.dtype == NM_FP16 ? launch_format<NM_FP16>(plan, A, cache.format, cache.D, s)
                                   : launch_format<NM_BF16>(plan, A, cache.format, cache.D, s);

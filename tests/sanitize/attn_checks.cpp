@@ -202,7 +202,7 @@ long plans()
                             };
                             promise(covers(p.prefix_splits, p.prefix_chunk, P), "prefix ranges");
                             promise(covers(p.own_splits, p.own_chunk, ml), "own ranges");
-                            promise(p.prefix_groups * 16 * p.mt >= B * G && p.own_groups * 16 >= G, "row groups");
+                            promise(p.prefix_groups * 16 * p.mt * (p.waves ? p.waves : 1) >= B * G && p.own_groups * 16 >= G, "row groups");
                             promise(p.direct == (P == 0 && p.own_splits <= 1), "direct");
                             if (!p.direct) {
                                 promise(p.prefix_parts == p.prefix_splits * B * Hq, "prefix partial rows");
