@@ -7,7 +7,6 @@ rows may be strided (views of a fused q+k+v buffer).  Work runs on ``stream``
 that a call allocates belong to that stream.
 """
 import ctypes
-import math
 
 import torch
 
@@ -23,7 +22,7 @@ def _dtype(dtype):
     return _DT[dtype]
 
 
-def _refuse(t, name, device, dtype, shape, contiguous):
+def _refuse(t, name, device, dtype, shape):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.device != device:
@@ -35,32 +34,36 @@ def _refuse(t, name, device, dtype, shape, contiguous):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _check(t, name, device, dtype, shape, contiguous=True):
-    """t is a tensor on the GPU `device` with `dtype` and `shape`."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and t.dtype == dtype and t.shape == shape and
-            (not contiguous or t.is_contiguous())):
-        _refuse(t, name, device, dtype, shape, contiguous)
+def _check(t, name, device, dtype, shape):
+    """Address of t, which is a contiguous tensor on the GPU `device` with
+    `dtype` and `shape`."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and t.dtype == dtype and
+            t.shape == shape and t.is_contiguous()):
+        _refuse(t, name, device, dtype, shape)
+    return t.data_ptr()
 
 
 def _size(t, name, dims):
     """The shape of a tensor of `dims` dimensions."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, not {len(shape)}")
+    return shape
 
 
 def _rows(t, name, device, dtype, shape):
-    """Row stride of strided rows [rows][heads][D] of that shape."""
-    _check(t, name, device, dtype, shape, contiguous=False)
+    """Address and row stride of strided rows [rows][heads][D] of that shape."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and t.dtype == dtype and t.shape == shape):
+        _refuse(t, name, device, dtype, shape)
     rows, heads, D = shape
     if t.is_contiguous():
-        return heads * D
+        return t.data_ptr(), heads * D
     s0, s1, s2 = t.stride()
     if (D > 1 and s2 != 1) or (heads > 1 and s1 != D) or (rows > 1 and s0 < heads * D):
         raise ValueError(f"{name}: heads and columns must be contiguous, rows must not overlap")
-    return s0 if rows > 1 else heads * D
+    return t.data_ptr(), s0 if rows > 1 else heads * D
 
 
 class _On:
@@ -75,7 +78,7 @@ class _On:
             if stream.device != device:
                 raise ValueError(f"stream is on {stream.device}, not on {device}")
             self.guards.append(torch.cuda.stream(stream))       # sets the device as well
-        elif device.index != torch.cuda.current_device():
+        else:
             self.guards.append(torch.cuda.device(device))
         for g in self.guards:
             g.__enter__()
@@ -89,10 +92,39 @@ class _On:
             g.__exit__(*exc)
 
 
+class _Here:
+    """_On for the current stream of the current device, which needs no guards."""
+
+    def __enter__(self):
+        return _current_stream(torch.cuda.current_device())
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
+
+# torch's own shortcut to the current stream's handle where it has one (a stream
+# object costs about 2 us, which a decode step's calls would notice).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on(device, stream):
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE
+    return _On(device, stream)
+
+
 def _call(name, *args):
     st = getattr(attn_lib(), name)(*args)
     if st != NM_OK:
         raise NmError(name, st)
+
+
+def _empty(like, shape):
+    """A new contiguous tensor of that shape on like's device, in its dtype."""
+    return torch.empty_like(like) if like.shape == shape and like.is_contiguous() else like.new_empty(shape)
 
 
 def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, interleaved=False, out=None, stream=None):
@@ -107,23 +139,21 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, interlea
     pairs, = _size(inv_freq, "inv_freq", 1)
     dev, dt = q.device, q.dtype
     code = _dtype(dt)
-    qs = _rows(q, "q", dev, dt, (T, hq, D))
-    ks = _rows(k, "k", dev, dt, (T, hk, D))
-    _check(positions, "positions", dev, torch.int32, (T,))
-    _check(inv_freq, "inv_freq", dev, torch.float32, (pairs,))
-    for w, name in ((wq, "wq"), (wk, "wk")):
-        if w is not None:
-            _check(w, name, dev, dt, (D,))
-    if out is not None:
-        _check(out[0], "out[0]", dev, dt, (T, hq, D))
-        _check(out[1], "out[1]", dev, dt, (T, hk, D))
-    with _On(dev, stream) as handle:
+    qp, qs = _rows(q, "q", dev, dt, (T, hq, D))
+    kp, ks = _rows(k, "k", dev, dt, (T, hk, D))
+    pos = _check(positions, "positions", dev, torch.int32, (T,))
+    freq = _check(inv_freq, "inv_freq", dev, torch.float32, (pairs,))
+    wqp = None if wq is None else _check(wq, "wq", dev, dt, (D,))
+    wkp = None if wk is None else _check(wk, "wk", dev, dt, (D,))
+    with _on(dev, stream) as handle:
         if out is None:
-            out = (torch.empty((T, hq, D), dtype=dt, device=dev), torch.empty((T, hk, D), dtype=dt, device=dev))
-        _call("nm_qk_norm_rope", q.data_ptr(), qs, k.data_ptr(), ks, T, hq, hk, D, code,
-              None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), eps, positions.data_ptr(),
-              inv_freq.data_ptr(), 2 * pairs, int(bool(interleaved)), out[0].data_ptr(),
-              out[1].data_ptr(), handle)
+            out = _empty(q, (T, hq, D)), _empty(k, (T, hk, D))
+            oq, ok = out[0].data_ptr(), out[1].data_ptr()
+        else:
+            oq = _check(out[0], "out[0]", dev, dt, (T, hq, D))
+            ok = _check(out[1], "out[1]", dev, dt, (T, hk, D))
+        _call("nm_qk_norm_rope", qp, qs, kp, ks, T, hq, hk, D, code, wqp, wkp, eps, pos, freq, 2 * pairs,
+              1 if interleaved else 0, oq, ok, handle)
     return out[0], out[1]
 
 
@@ -187,11 +217,12 @@ def kv_write(cache, k, v, slots, stream=None):
     skipped; no slot twice in one call."""
     c = _cache(cache)
     T, = _size(slots, "slots", 1)
-    _check(slots, "slots", c.device, torch.int64, (T,))
+    sp = _check(slots, "slots", c.device, torch.int64, (T,))
     shape = (T, c.heads, c.D)
-    ks, vs = _rows(k, "k", c.device, c.dtype, shape), _rows(v, "v", c.device, c.dtype, shape)
-    with _On(c.device, stream) as handle:
-        _call("nm_kv_write", c._ref, k.data_ptr(), ks, v.data_ptr(), vs, T, slots.data_ptr(), handle)
+    kp, ks = _rows(k, "k", c.device, c.dtype, shape)
+    vp, vs = _rows(v, "v", c.device, c.dtype, shape)
+    with _on(c.device, stream) as handle:
+        _call("nm_kv_write", c._ref, kp, ks, vp, vs, T, sp, handle)
 
 
 def kv_read(cache, slots, out=None, stream=None):
@@ -199,15 +230,17 @@ def kv_read(cache, slots, out=None, stream=None):
     for a slot outside the cache."""
     c = _cache(cache)
     T, = _size(slots, "slots", 1)
-    _check(slots, "slots", c.device, torch.int64, (T,))
+    sp = _check(slots, "slots", c.device, torch.int64, (T,))
     shape = (T, c.heads, c.D)
-    if out is not None:
-        _check(out[0], "out[0]", c.device, c.dtype, shape)
-        _check(out[1], "out[1]", c.device, c.dtype, shape)
-    with _On(c.device, stream) as handle:
+    with _on(c.device, stream) as handle:
         if out is None:
-            out = tuple(torch.empty(shape, dtype=c.dtype, device=c.device) for _ in range(2))
-        _call("nm_kv_read", c._ref, slots.data_ptr(), T, out[0].data_ptr(), out[1].data_ptr(), handle)
+            k = slots.new_empty(shape, dtype=c.dtype)
+            out = k, torch.empty_like(k)
+            kp, vp = k.data_ptr(), out[1].data_ptr()
+        else:
+            kp = _check(out[0], "out[0]", c.device, c.dtype, shape)
+            vp = _check(out[1], "out[1]", c.device, c.dtype, shape)
+        _call("nm_kv_read", c._ref, sp, T, kp, vp, handle)
     return out[0], out[1]
 
 
@@ -235,40 +268,45 @@ def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, pre
     c = _cache(cache)
     dev, dt = c.device, c.dtype
     B, hq, _ = _size(q, "q", 3)
-    qs = _rows(q, "q", dev, dt, (B, hq, c.D))
-    _check(lens, "lens", dev, torch.int32, (B,))
+    shape = (B, hq, c.D)
+    qp, qs = _rows(q, "q", dev, dt, shape)
+    lp = _check(lens, "lens", dev, torch.int32, (B,))
     table, stride, width = None, 0, 0
     if page_table is not None:
         width = _size(page_table, "page_table", 2)[1]
-        _check(page_table, "page_table", dev, torch.int32, (B, width), contiguous=False)
-        stride = width
-        if not page_table.is_contiguous():
-            if width > 1 and page_table.stride(1) != 1:
-                raise ValueError("page_table rows must be contiguous")
-            stride = page_table.stride(0)
-        table, width = page_table.data_ptr(), width * c.page_size
+        if page_table.is_contiguous():
+            table, stride = _check(page_table, "page_table", dev, torch.int32, (B, width)), width
+        else:
+            if (width > 1 and page_table.stride(1) != 1) or not page_table.is_cuda or page_table.device != dev or \
+                    page_table.dtype != torch.int32 or page_table.shape[0] != B:
+                _refuse(page_table, "page_table (rows)", dev, torch.int32, (B, width))
+            table, stride = page_table.data_ptr(), page_table.stride(0)
+        width *= c.page_size
     max_len = width if max_len is None else max_len
     if max_len > width:
         raise ValueError(f"max_len {max_len} is more than page_table holds ({width} tokens)")
+    pp = None
     if prefix_len:
         n, = _size(prefix_pages, "prefix_pages", 1)
-        _check(prefix_pages, "prefix_pages", dev, torch.int32, (n,))
+        pp = _check(prefix_pages, "prefix_pages", dev, torch.int32, (n,))
         if prefix_len > n * c.page_size:
             raise ValueError(f"prefix_len {prefix_len} is more than prefix_pages holds ({n * c.page_size} tokens)")
-    if out is not None:
-        _check(out, "out", dev, dt, (B, hq, c.D))
-    if lse is not None:
-        _check(lse, "lse", dev, torch.float32, (B, hq))
+    lsep = None if lse is None else _check(lse, "lse", dev, torch.float32, (B, hq))
+    wsp, nbytes = None, 0
     if ws is not None:
-        _check(ws, "ws", dev, torch.uint8, _size(ws, "ws", 1))
-    need = attn_lib().nm_attn_workspace_bytes(B, hq, c.heads, c.D, prefix_len, max_len)
-    with _On(dev, stream) as handle:
+        nbytes, = _size(ws, "ws", 1)
+        wsp = _check(ws, "ws", dev, torch.uint8, (nbytes,))
+    with _on(dev, stream) as handle:
         if out is None:
-            out = torch.empty((B, hq, c.D), dtype=dt, device=dev)
-        if ws is None and need > 0:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        _call("nm_attn_decode", q.data_ptr(), qs, B, hq, c._ref, None if prefix_len == 0 else prefix_pages.data_ptr(),
-              prefix_len, table, stride, lens.data_ptr(), max_len, 1.0 / math.sqrt(c.D) if scale is None else scale,
-              out.data_ptr(), None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
-              0 if ws is None else ws.numel(), handle)
+            out = _empty(q, shape)
+            op = out.data_ptr()
+        else:
+            op = _check(out, "out", dev, dt, shape)
+        if ws is None:
+            nbytes = attn_lib().nm_attn_workspace_bytes(B, hq, c.heads, c.D, prefix_len, max_len)
+            if nbytes > 0:
+                ws = q.new_empty(nbytes, dtype=torch.uint8)
+                wsp = ws.data_ptr()
+        _call("nm_attn_decode", qp, qs, B, hq, c._ref, pp, prefix_len, table, stride, lp, max_len,
+              c.D ** -0.5 if scale is None else scale, op, lsep, wsp, max(nbytes, 0), handle)
     return out

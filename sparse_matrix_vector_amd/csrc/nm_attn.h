@@ -3,6 +3,7 @@
 // kernel-side declarations.  Host-only C++ (no HIP types): the checks and the
 // plan also build with a plain compiler under sanitizers; the constexpr layout
 // functions are used by the device code too.
+
 #ifndef NM_ATTN_H
 #define NM_ATTN_H
 

@@ -54,8 +54,8 @@ struct AttnArgs {
     float* lse;
     float* part_o;              // [rows][D] partial sums: prefix rows first, own rows behind them
     f32x2* part_ml;             // [rows] (maximum, sum)
-    int64_t q_stride, table_stride, n_pages, own_base;   // own_base: first partial row of the own-token units
-    int B, Hq, heads, G, page_shift;
+    int64_t q_stride, table_stride, own_base;            // own_base: first partial row of the own-token units
+    int n_pages, B, Hq, heads, G, page_shift;
     int prefix_len, max_len;
     int prefix_rows, prefix_groups, prefix_splits, prefix_chunk;
     int own_groups, own_splits, own_chunk;
@@ -115,7 +115,7 @@ struct Cache {
         typedef uint32_t chunk __attribute__((ext_vector_type(CB / 4)));
 #pragma unroll
         for (int c = 0; c < kWords * 4 / CB; ++c) {
-            const chunk x = *reinterpret_cast<const chunk*>(tile + c * 64 * CB + lane * CB);
+            const chunk x = __builtin_nontemporal_load(reinterpret_cast<const chunk*>(tile + c * 64 * CB + lane * CB));
 #pragma unroll
             for (int i = 0; i < CB / 4; ++i)
                 raw.w[CB / 4 * c + i] = x[i];
@@ -245,22 +245,24 @@ struct TileRef {
     int n;
 };
 
-// Tile `a` (16-token index within its sequence or prefix) of the page list.
-__device__ __forceinline__ TileRef tile_ref(const AttnArgs& A, const int32_t* pages, int a, int end, int h)
+// Page number of tile `a` (16-token index within its sequence or prefix, the same
+// for the whole wave) of a list that holds `limit` tokens: a scalar load, which
+// takes no part in the counts of vector loads outstanding.
+__device__ __forceinline__ int page_of(const AttnArgs& A, const int32_t* pages, int a, int limit)
 {
+    typedef __attribute__((address_space(4))) const int32_t constant_i32;
+    return a * nma::kTile < limit ? ((constant_i32*)pages)[a >> (A.page_shift - 4)] : -1;
+}
+
+// That tile of key head h, where tokens from `end` on do not count.  A page number
+// outside the cache is not followed: its tokens are absent.
+__device__ __forceinline__ TileRef tile_ref(const AttnArgs& A, int page, int a, int end, int h)
+{
+    const bool inside = (unsigned)page < (unsigned)A.n_pages;
     TileRef t;
-    const int t0 = a * nma::kTile;
-    t.n = min(max(end - t0, 0), nma::kTile);
-    int page = 0;
-    if (t.n > 0) {
-        page = pages[t0 >> A.page_shift];
-        if (page < 0 || page >= A.n_pages) {        // not followed: its tokens are absent
-            page = 0;
-            t.n = 0;
-        }
-    }
-    page = __builtin_amdgcn_readfirstlane(page);
+    t.n = inside ? min(max(end - a * nma::kTile, 0), nma::kTile) : 0;
     t.n = __builtin_amdgcn_readfirstlane(t.n);
+    page = __builtin_amdgcn_readfirstlane(inside ? page : 0);
     const int per = 1 << (A.page_shift - 4);
     t.tile = ((int64_t)page * A.heads + h) * per + (a & (per - 1));
     return t;
@@ -381,27 +383,38 @@ struct Weights {
     }
 };
 
-// A row's partial result: the lane holds columns kg D/4 + r D/16 + j in acc[j][r].
+// Partial results of a row tile, in the workspace: the lane (kg, m) holds columns
+// kg D/4 + r D/16 + j of row m in acc[j][r]; they are kept as
+//   [r D/64 + j / 4][kg][row of the tile's nr] 16 bytes,
+// so that a wave's store (and the load that joins them) is one contiguous piece.
+__device__ __forceinline__ int64_t part_at(int chunk, int kg, int nr, int m)
+{
+    return ((int64_t)(chunk * 4 + kg) * nr + m) * 4;
+}
+
 template <int D>
-__device__ __forceinline__ void store_part(const AttnArgs& A, int64_t row, int kg, const f32x4 (&acc)[D / 16], float mx,
-                                           float sum)
+__device__ __forceinline__ void store_part(const AttnArgs& A, int64_t row0, int nr, int m, int kg,
+                                           const f32x4 (&acc)[D / 16], float mx, float sum)
 {
     constexpr int kPer = D / 16;
-    float* o = A.part_o + row * D + kg * (D / 4);
+    float* o = A.part_o + row0 * D;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int j = 0; j < kPer; j += 4)
-            *reinterpret_cast<f32x4*>(o + c * kPer + j) = f32x4{acc[j][c], acc[j + 1][c], acc[j + 2][c], acc[j + 3][c]};
+            *reinterpret_cast<f32x4*>(o + part_at(c * (kPer / 4) + j / 4, kg, nr, m)) =
+                f32x4{acc[j][c], acc[j + 1][c], acc[j + 2][c], acc[j + 3][c]};
     if (kg == 0)
-        A.part_ml[row] = f32x2{mx, sum};
+        A.part_ml[row0 + m] = f32x2{mx, sum};
 }
 
 // One unit: 16 MT rows from row0 of the R rows of key head h, tokens
-// [start, end) of the page list.
+// [start, end) of a page list that holds `limit` tokens.  Page numbers are loaded
+// a step before the tiles they lead to; the wave's first two are page0 and page1.
 template <int DT, int BITS, int D, int MT>
 __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, int h, int b0, int row0, int R,
-                                       int start, int end, bool direct, int64_t part_row, float* lds)
+                                       int start, int end, int limit, int page0, int page1, bool direct,
+                                       int64_t part_row, float* lds)
 {
     using C = Cache<BITS, D>;
     constexpr int kSteps = D / 32;                                   // k-steps of the score product
@@ -411,6 +424,8 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
     const int lane = threadIdx.x % 64, m = lane % 16, kg = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
+    int at = start / nma::kTile + 2 * wave;             // the wave's next pair of tiles
+    int page[2] = {page0, page1};
     Rows<DT, BITS, D, MT> rows;
     rows.load(A, h, b0, row0, R, m, kg);
 
@@ -446,21 +461,22 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
         }
     };
 
-    int at = start / nma::kTile + 2 * wave;             // the wave's next pair of tiles
     const int last = (end + nma::kTile - 1) / nma::kTile;
-    if (at < last) {
-        cur[0] = tile_ref(A, pages, at, end, h);
-        cur[1] = tile_ref(A, pages, at + 1, end, h);
-        load_k(cur);
-        __builtin_amdgcn_sched_barrier(0);              // keys first: they are waited for first
-        load_v(cur);
-    }
-    // One step; with `more`, the loads of the wave's next one (pair `at`) start as
-    // soon as the registers they fill are free.
+    const auto fetch = [&]() {                          // the pages of pair `at`
+        page[0] = page_of(A, pages, at, limit);
+        page[1] = page_of(A, pages, at + 1, limit);
+    };
+    const auto refer = [&](TileRef(&t)[2]) {            // its tiles
+        t[0] = tile_ref(A, page[0], at, end, h);
+        t[1] = tile_ref(A, page[1], at + 1, end, h);
+        at += 2 * nma::kWaves;
+    };
+    // One step; with `more`, the loads of the wave's next one start as soon as the
+    // registers they fill are free.
     const auto step = [&](auto more) {
         if constexpr (more()) {
-            next[0] = tile_ref(A, pages, at, end, h);
-            next[1] = tile_ref(A, pages, at + 1, end, h);
+            refer(next);
+            fetch();
         }
         // scores
         f32x4 sc[MT][2];
@@ -523,7 +539,12 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
         }
     };
     if (at < last) {
-        for (at += 2 * nma::kWaves; at < last; at += 2 * nma::kWaves)
+        refer(cur);
+        load_k(cur);
+        __builtin_amdgcn_sched_barrier(0);              // keys first: they are waited for first
+        load_v(cur);
+        fetch();
+        while (at < last)
             step(std::true_type());
         step(std::false_type());
     }
@@ -586,7 +607,7 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
             if (A.lse && kg == 0)
                 A.lse[row] = (mx[g] + __builtin_amdgcn_logf(sum[g])) * kLn2;
         } else {
-            store_part<D>(A, part_row + r, kg, acc[g], mx[g], sum[g]);
+            store_part<D>(A, part_row + row0 + 16 * g, min(16, R - row0 - 16 * g), m, kg, acc[g], mx[g], sum[g]);
         }
     }
 }
@@ -752,16 +773,16 @@ __global__ __launch_bounds__(W * 64, 2) void staged_kernel(const AttnArgs A)
         if (part == 0 && lane == 0)
             count[which][mine] = stage.n;
     };
-    stage.load(A, tile_ref(A, A.prefix_pages, at, end, h), part, lane);
+    stage.load(A, tile_ref(A, page_of(A, A.prefix_pages, at, end), at, end, h), part, lane);
+    int page = page_of(A, A.prefix_pages, at + NT, end);
     put(0);
-    TileRef next = tile_ref(A, A.prefix_pages, at + NT, end, h);
     __syncthreads();
     for (int i = 0; i < steps; ++i) {
         const bool more = i + 1 < steps;
         if (more) {
-            stage.load(A, next, part, lane);
             at += NT;
-            next = tile_ref(A, A.prefix_pages, at + NT, end, h);
+            stage.load(A, tile_ref(A, page, at, end, h), part, lane);
+            page = page_of(A, A.prefix_pages, at + NT, end);
         }
         if (busy) {
             const uint8_t* kb = buf[i & 1];
@@ -838,10 +859,11 @@ __global__ __launch_bounds__(W * 64, 2) void staged_kernel(const AttnArgs A)
     }
 #pragma unroll
     for (int g = 0; g < MT; ++g) {
-        const int r = row0 + 16 * g + m;
+        const int r = row0 + 16 * g;
         const float total = quarters_sum(sum[g]);
-        if (r < A.prefix_rows)
-            store_part<D>(A, ((int64_t)split * A.heads + h) * A.prefix_rows + r, kg, acc[g], mx[g], total);
+        if (r + m < A.prefix_rows)
+            store_part<D>(A, ((int64_t)split * A.heads + h) * A.prefix_rows + r, min(16, A.prefix_rows - r), m, kg,
+                          acc[g], mx[g], total);
     }
 }
 
@@ -853,7 +875,9 @@ __global__ __launch_bounds__(nma::kWaves * 64, 2) void prefix_kernel(const AttnA
     const int h = blockIdx.x % A.heads, split = blockIdx.x / A.heads % A.prefix_splits;
     const int group = blockIdx.x / A.heads / A.prefix_splits;
     const int start = split * A.prefix_chunk, end = min(start + A.prefix_chunk, A.prefix_len);
-    attend<DT, BITS, D, MT>(A, A.prefix_pages, h, 0, group * 16 * MT, A.prefix_rows, start, end, false,
+    const int at = start / nma::kTile + 2 * __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    attend<DT, BITS, D, MT>(A, A.prefix_pages, h, 0, group * 16 * MT, A.prefix_rows, start, end, end,
+                            page_of(A, A.prefix_pages, at, end), page_of(A, A.prefix_pages, at + 1, end), false,
                             ((int64_t)split * A.heads + h) * A.prefix_rows, lds);
 }
 
@@ -864,89 +888,89 @@ __global__ __launch_bounds__(nma::kWaves * 64, 2) void own_kernel(const AttnArgs
     __shared__ float lds[join_floats(D, 1)];
     const int h = blockIdx.x % A.heads, b = blockIdx.x / A.heads % A.B;
     const int group = blockIdx.x / A.heads / A.B % A.own_groups, split = blockIdx.x / A.heads / A.B / A.own_groups;
-    const int len = min(A.lens[b], A.max_len);
-    if (len < 0)
+    const int start = split * A.own_chunk, at = start / nma::kTile + 2 * __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    // The length and the first page numbers come together: the table's entries behind
+    // the length may be read, they are only not followed.
+    const int32_t* pages = A.page_table + (int64_t)b * A.table_stride;
+    const int held = A.lens[b], page0 = page_of(A, pages, at, A.max_len), page1 = page_of(A, pages, at + 1, A.max_len);
+    asm volatile("" ::"s"(held), "s"(page0), "s"(page1));
+    const int len = min(held, A.max_len);
+    if (len < 0 || (start >= len && !direct))   // combine looks at the ranges that hold tokens only
         return;
-    const int start = split * A.own_chunk;
-    if (start >= len && !direct)                // combine looks at the ranges that hold tokens only
-        return;
-    const int end = min(start + A.own_chunk, len);
-    attend<DT, BITS, D, 1>(A, A.page_table + (int64_t)b * A.table_stride, h, b, group * 16, A.G, start, end, direct != 0,
-                           A.own_base + ((int64_t)split * A.B + b) * A.Hq + (int64_t)h * A.G, lds);
+    attend<DT, BITS, D, 1>(A, pages, h, b, group * 16, A.G, start, min(start + A.own_chunk, len), A.max_len, page0, page1,
+                           direct != 0, A.own_base + ((int64_t)split * A.B + b) * A.Hq + (int64_t)h * A.G, lds);
 }
 
-// Joins the partial results of each row: a block takes one (sequence, head).
-// The parts' weights are found by all threads at once and kept in LDS; then each
-// wave adds up a quarter of the parts, whose loads do not wait for each other.
-constexpr int kMaxParts = 2048;                 // of a row; the plan makes at most 4 kCus
-
-template <int DT, int D>
-__global__ __launch_bounds__(256) void combine_kernel(const AttnArgs A)
+// Joins the partial results: a block takes one chunk of a tile of 16 rows (r = b G
+// + g) of one key head, a lane (kg, m) row m as in the partial results.  NW waves
+// share the parts: first their maxima, then, with the row's maximum known, their
+// weighted sums, which meet in LDS.  No load waits for another part's: parts
+// behind a row's last are loaded from its first one and not added.
+template <int DT, int D, int NW>
+__global__ __launch_bounds__(NW * 64) void combine_kernel(const AttnArgs A)
 {
-    constexpr int kCols = D / 64;
-    typedef float cols __attribute__((ext_vector_type(kCols)));
-    __shared__ float weight[kMaxParts], red[8], box[3 * D];
-    const int b = blockIdx.x / A.Hq, hq = blockIdx.x % A.Hq;
-    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    __shared__ float tops[NW][64], sums[NW][64];
+    __shared__ f32x4 box[NW - 1][64];
+    const int lane = threadIdx.x % 64, m = lane % 16, kg = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int tiles = (A.prefix_rows + 15) / 16;
+    const int h = blockIdx.x % A.heads, tile = blockIdx.x / A.heads % tiles, chunk = blockIdx.x / A.heads / tiles;
+    const int r = tile * 16 + m, rr = min(r, A.prefix_rows - 1), b = rr / A.G, g = rr % A.G;
     const int len = min(A.lens[b], A.max_len);
-    if (len < 0)
-        return;
-    const int np = A.prefix_splits, total = np + (len + A.own_chunk - 1) / A.own_chunk;
-    const int64_t first_p = (int64_t)(hq / A.G) * A.prefix_rows + (int64_t)b * A.G + hq % A.G;
-    const int64_t step_p = (int64_t)A.heads * A.prefix_rows, step_o = (int64_t)A.B * A.Hq;
-    const int64_t first_o = A.own_base + (int64_t)b * A.Hq + hq - np * step_o;
-    const auto part = [&](int i) { return i < np ? first_p + i * step_p : first_o + i * step_o; };
+    const int np = A.prefix_splits, mine = np + (max(len, 0) + A.own_chunk - 1) / A.own_chunk;
+    // Part i of the lane's row: first row of its tile, rows of the tile, row in it.
+    const int p_rows = min(16, A.prefix_rows - tile * 16), o_rows = min(16, A.G - g / 16 * 16);
+    const int64_t p0 = (int64_t)h * A.prefix_rows + tile * 16, p_step = (int64_t)A.heads * A.prefix_rows;
+    const int64_t o_step = (int64_t)A.B * A.Hq;
+    const int64_t o0 = A.own_base + (int64_t)b * A.Hq + (int64_t)h * A.G + g / 16 * 16 - np * o_step;
+    const auto first = [&](int i) { return i < np ? p0 + i * p_step : o0 + i * o_step; };
+    int total = mine;                                   // of the tile's longest row
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2)
+        total = max(total, __shfl_xor(total, i));
+    total = __builtin_amdgcn_readfirstlane(total);
 
     float mx = NM_NEG_INF;
-    for (int i = threadIdx.x; i < total; i += 256) {
-        const float m = A.part_ml[part(i)].x;
-        weight[i] = m;
-        mx = fmaxf(mx, m);
-    }
-#pragma unroll
-    for (int i = 1; i < 64; i *= 2)
-        mx = fmaxf(mx, __shfl_xor(mx, i));
-    if (lane == 0)
-        red[wave] = mx;
+    for (int i = 4 * wave + kg; i < mine; i += 4 * NW)
+        mx = fmaxf(mx, A.part_ml[first(i) + (i < np ? rr : g) % 16].x);
+    tops[wave][lane] = quarters_max(mx);
     __syncthreads();
-    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        mx = fmaxf(mx, tops[w][lane]);
     const float base = mx == NM_NEG_INF ? 0.0f : mx;
+    f32x4 acc = {};
     float sum = 0.0f;
-    for (int i = threadIdx.x; i < total; i += 256) {
-        const float f = __builtin_amdgcn_exp2f(weight[i] - base);
-        weight[i] = f;
-        sum += A.part_ml[part(i)].y * f;
-    }
-#pragma unroll
-    for (int i = 1; i < 64; i *= 2)
-        sum += __shfl_xor(sum, i);
-    if (lane == 0)
-        red[4 + wave] = sum;
-    __syncthreads();
-    sum = (red[4] + red[5]) + (red[6] + red[7]);
-
-    cols acc = {};
 #pragma unroll 4
-    for (int i = wave; i < total; i += 4)
-        acc += *reinterpret_cast<const cols*>(A.part_o + part(i) * D + lane * kCols) * weight[i];
+    for (int i = wave; i < total; i += NW) {
+        const bool live = i < mine;
+        const int at = live ? i : 0;
+        const int64_t row0 = first(at);
+        const int in = (at < np ? rr : g) % 16;
+        const f32x2 x = A.part_ml[row0 + in];
+        const f32x4 o = *reinterpret_cast<const f32x4*>(A.part_o + row0 * D + part_at(chunk, kg, at < np ? p_rows : o_rows, in));
+        const float f = __builtin_amdgcn_exp2f(x.x - base);
+        sum += live ? x.y * f : 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            acc[c] += live ? o[c] * f : 0.0f;
+    }
+    sums[wave][lane] = sum;
     if (wave > 0)
-        *reinterpret_cast<cols*>(box + (wave - 1) * D + lane * kCols) = acc;
+        box[wave - 1][lane] = acc;
     __syncthreads();
-    if (wave > 0)
+    if (wave > 0 || r >= A.prefix_rows || len < 0)      // a padding row stays as it was
         return;
 #pragma unroll
-    for (int w = 0; w < 3; ++w)
-        acc += *reinterpret_cast<const cols*>(box + w * D + lane * kCols);
+    for (int w = 1; w < NW; ++w) {
+        sum += sums[w][lane];
+        acc += box[w - 1][lane];
+    }
     acc *= sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    const int64_t row = blockIdx.x;
-    uint16_t* o = A.o + row * D + lane * kCols;
-    if constexpr (kCols == 1)
-        *o = (uint16_t)pack2<DT>(acc[0], 0.0f);
-    else
-#pragma unroll
-        for (int c = 0; c < kCols; c += 2)
-            *reinterpret_cast<uint32_t*>(o + c) = pack2<DT>(acc[c], acc[c + 1]);
-    if (A.lse && threadIdx.x == 0)
+    const int64_t row = (int64_t)b * A.Hq + (int64_t)h * A.G + g;
+    *reinterpret_cast<u32x2*>(A.o + row * D + kg * (D / 4) + chunk * 4) =
+        u32x2{pack2<DT>(acc[0], acc[1]), pack2<DT>(acc[2], acc[3])};
+    if (A.lse && kg == 0 && chunk == 0)
         A.lse[row] = (mx + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
@@ -976,8 +1000,16 @@ int launch(const nma::AttnPlan& P, const AttnArgs& A, hipStream_t s)
         return NM_ERR_BAD_SHAPE;
     if (own_blocks > 0)
         hipLaunchKernelGGL((own_kernel<DT, BITS, D>), dim3((unsigned)own_blocks), block, 0, s, A, P.direct ? 1 : 0);
-    if (!P.direct)
-        hipLaunchKernelGGL((combine_kernel<DT, D>), dim3((unsigned)(A.B * A.Hq)), dim3(256), 0, s, A);
+    if (!P.direct) {
+        const int64_t blocks = nma::ceil_div(P.prefix_rows, 16) * A.heads * (D / 16);
+        if (blocks > INT32_MAX)
+            return NM_ERR_BAD_SHAPE;
+        // Few tiles of rows have many parts each: more waves share them then.
+        if (blocks < 2 * nma::kCus && P.prefix_splits + P.own_splits > 16)
+            hipLaunchKernelGGL((combine_kernel<DT, D, 16>), dim3((unsigned)blocks), dim3(1024), 0, s, A);
+        else
+            hipLaunchKernelGGL((combine_kernel<DT, D, 4>), dim3((unsigned)blocks), dim3(256), 0, s, A);
+    }
     return hip_status(hipGetLastError());
 }
 
@@ -1023,7 +1055,7 @@ int nmk::attn_decode(const nma::AttnPlan& plan, const void* q, int64_t q_stride,
     A.part_ml = reinterpret_cast<f32x2*>(A.part_o + (plan.prefix_parts + plan.own_parts) * cache.D);
     A.q_stride = B > 1 ? q_stride : 0;
     A.table_stride = B > 1 && max_len > 0 ? table_stride : 0;
-    A.n_pages = cache.n_pages;
+    A.n_pages = (int)cache.n_pages;
     A.own_base = plan.prefix_parts;
     A.B = (int)B;
     A.Hq = Hq;
