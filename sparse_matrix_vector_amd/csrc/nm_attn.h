@@ -91,8 +91,12 @@ struct AttnPlan {
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Cuts `tokens` into ranges of whole steps for every wave, so that `units` row
-// groups make about `blocks` blocks.
-inline void cut(int64_t tokens, int64_t units, int64_t blocks, int64_t* splits, int64_t* chunk)
+// groups make about `blocks` blocks, and into ranges of at most `longest` where
+// that takes no more than 64 (a batch of very different lengths would otherwise
+// wait for its longest sequence's block).
+constexpr int64_t kMaxRanges = 64, kMaxBlocks = int64_t(1) << 24;
+
+inline void cut(int64_t tokens, int64_t units, int64_t blocks, int64_t longest, int64_t* splits, int64_t* chunk)
 {
     const int64_t grain = kWaves * kStep;
     if (tokens == 0) {
@@ -101,6 +105,13 @@ inline void cut(int64_t tokens, int64_t units, int64_t blocks, int64_t* splits, 
         return;
     }
     int64_t want = ceil_div(blocks, units);
+    int64_t even = ceil_div(tokens, longest);
+    if (even > kMaxRanges)
+        even = kMaxRanges;
+    if (even > kMaxBlocks / units)
+        even = kMaxBlocks / units;
+    if (want < even)
+        want = even;
     if (want > ceil_div(tokens, grain))
         want = ceil_div(tokens, grain);
     *chunk = ceil_div(ceil_div(tokens, want), grain) * grain;
@@ -115,9 +126,16 @@ inline AttnPlan attn_plan(int64_t B, int Hq, int heads, int D, int64_t prefix_le
     p.mt = p.prefix_rows <= 16 || D == 256 ? 1 : 2;
     p.waves = p.prefix_rows <= 16 * p.mt ? 0 : p.prefix_rows <= 64 * p.mt && D != 256 ? 4 : 8;
     p.prefix_groups = ceil_div(p.prefix_rows, 16 * p.mt * (p.waves ? p.waves : 1));
-    cut(prefix_len, heads * p.prefix_groups, p.waves == 8 ? kCus : 2 * kCus, &p.prefix_splits, &p.prefix_chunk);
+    cut(prefix_len, heads * p.prefix_groups, p.waves == 8 ? kCus : 2 * kCus, kMaxTokens, &p.prefix_splits,
+        &p.prefix_chunk);
     p.own_groups = ceil_div(p.G, 16);
-    cut(max_len, B * heads * p.own_groups, 3 * kCus, &p.own_splits, &p.own_chunk);
+    // Own tokens (us; 8 key heads, MX8, x blocks for each CU): 32 sequences of up to
+    // 1024 tokens, one unit per CU: 1 block 12.3, 2 blocks 14.2, 3 blocks 14.8; 16 of up
+    // to 8192: 38.3 / 34.2 / 35.8; 8 of up to 32768: 69.8 / 58.1 / 61.8.  Longest range
+    // for 32 sequences of up to 16384: 2048 tokens 95.7, 4096 97.2, 8192 110.3; of
+    // 4096 each: 49.8 / 45.7 / 45.7.
+    const int64_t units = B * heads * p.own_groups;
+    cut(max_len, units, units >= kCus ? kCus : 2 * kCus, 4096, &p.own_splits, &p.own_chunk);
     p.direct = p.prefix_splits == 0 && p.own_splits <= 1;
     p.prefix_parts = p.direct ? 0 : p.prefix_splits * heads * p.prefix_rows;
     p.own_parts = p.direct ? 0 : p.own_splits * B * Hq;

@@ -363,9 +363,14 @@ __device__ __forceinline__ u32x4 read_unit(const CacheArgs& A, int side, int64_t
         float x[8];
         const int p0 = side ? nma::v_offset(D, BITS, token, d0) : nma::k_offset(D, BITS, token, d0);
         const int p1 = side ? nma::v_offset(D, BITS, token, d0 + 4) : p0 + 4 * BITS / 8;
+        // the eight columns lie side by side but for values of D = 64 (four and four)
+        const bool whole = side == 0 || D >= 128;
         if constexpr (BITS == 8) {
-            const uint32_t c[2] = {*reinterpret_cast<const uint32_t*>(src + p0),
-                                   *reinterpret_cast<const uint32_t*>(src + p1)};
+            u32x2 c;
+            if (whole)
+                c = *reinterpret_cast<const u32x2*>(src + p0);
+            else
+                c = u32x2{*reinterpret_cast<const uint32_t*>(src + p0), *reinterpret_cast<const uint32_t*>(src + p1)};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j], false);
@@ -373,8 +378,9 @@ __device__ __forceinline__ u32x4 read_unit(const CacheArgs& A, int side, int64_t
                 x[4 * j] = lo.x, x[4 * j + 1] = lo.y, x[4 * j + 2] = hi.x, x[4 * j + 3] = hi.y;
             }
         } else {
-            const uint32_t c = (uint32_t)*reinterpret_cast<const uint16_t*>(src + p0) |
-                               (uint32_t)*reinterpret_cast<const uint16_t*>(src + p1) << 16;
+            const uint32_t c = whole ? *reinterpret_cast<const uint32_t*>(src + p0)
+                                     : (uint32_t)*reinterpret_cast<const uint16_t*>(src + p0) |
+                                           (uint32_t)*reinterpret_cast<const uint16_t*>(src + p1) << 16;
             const f32x2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0),
                                 __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1),
                                 __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2),
