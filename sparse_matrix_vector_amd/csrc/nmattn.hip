@@ -411,7 +411,7 @@ __device__ __forceinline__ void store_part(const AttnArgs& A, int64_t row0, int 
 // One unit: 16 MT rows from row0 of the R rows of key head h, tokens
 // [start, end) of a page list that holds `limit` tokens.  Page numbers are loaded
 // a step before the tiles they lead to; the wave's first two are page0 and page1.
-template <int DT, int BITS, int D, int MT>
+template <int DT, int BITS, int D, int MT, int NW>
 __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, int h, int b0, int row0, int R,
                                        int start, int end, int limit, int page0, int page1, bool direct,
                                        int64_t part_row, float* lds)
@@ -469,7 +469,7 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
     const auto refer = [&](TileRef(&t)[2]) {            // its tiles
         t[0] = tile_ref(A, page[0], at, end, h);
         t[1] = tile_ref(A, page[1], at + 1, end, h);
-        at += 2 * nma::kWaves;
+        at += 2 * NW;
     };
     // One step; with `more`, the loads of the wave's next one start as soon as the
     // registers they fill are free.
@@ -555,9 +555,9 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
     // The block's waves are joined two by two through LDS, lane to lane.
     constexpr int kRegs = MT * (4 * kPer + 2);
 #pragma unroll
-    for (int half = nma::kWaves / 2; half >= 1; half /= 2) {
+    for (int half = NW / 2; half >= 1; half /= 2) {
         float* box = lds + (wave % half) * kRegs * 64 + lane;
-        if (half < nma::kWaves / 2)
+        if (half < NW / 2)
             __syncthreads();                            // the boxes' last readers are done
         if (wave >= half && wave < 2 * half) {
 #pragma unroll
@@ -612,7 +612,7 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
     }
 }
 
-constexpr int join_floats(int D, int mt) { return nma::kWaves / 2 * mt * (D / 4 + 2) * 64; }
+constexpr int join_bytes(int D, int mt, int waves) { return waves / 2 * mt * (D / 4 + 2) * 64 * 4; }
 
 // ---- staged prefix units -----------------------------------------------------
 //
@@ -734,20 +734,26 @@ struct Stage {
     }
 };
 
-// Block = (row group, range, key head).
+// Unit `unit` = (row group, range, key head); lds: two buffers and two counts of
+// each tile's tokens (staged_bytes).
+template <int BITS, int D, int W>
+constexpr int staged_bytes()
+{
+    return 2 * Stage<BITS, D, W>::kBytes + 2 * Stage<BITS, D, W>::kTiles * 4;
+}
+
 template <int DT, int BITS, int D, int MT, int W>
-__global__ __launch_bounds__(W * 64, 2) void staged_kernel(const AttnArgs A)
+__device__ __forceinline__ void attend_staged(const AttnArgs& A, int unit, uint8_t* lds)
 {
     using S = Stage<BITS, D, W>;
     constexpr int kOp = op_type<DT, BITS>(), NT = S::kTiles, kSteps = S::kSteps, kPer = S::kPer;
     constexpr bool kSplit = split_rows<DT, BITS>();
     constexpr int kGroup = 4;                                // value operands read at a time
-    __shared__ __align__(16) uint8_t buf[2][S::kBytes];
-    __shared__ int count[2][NT];
+    int(*const count)[NT] = reinterpret_cast<int(*)[NT]>(lds + 2 * S::kBytes);
     const int lane = threadIdx.x % 64, m = lane % 16, kg = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int h = blockIdx.x % A.heads, split = blockIdx.x / A.heads % A.prefix_splits;
-    const int row0 = ((int)(blockIdx.x / A.heads / A.prefix_splits) * W + wave) * 16 * MT;
+    const int h = unit % A.heads, split = unit / A.heads % A.prefix_splits;
+    const int row0 = (unit / A.heads / A.prefix_splits * W + wave) * 16 * MT;
     const int start = split * A.prefix_chunk, end = min(start + A.prefix_chunk, A.prefix_len);
     const int mine = wave % NT, part = wave / NT;            // the tile of each step that this wave loads
     const bool busy = row0 < A.prefix_rows;
@@ -769,7 +775,7 @@ __global__ __launch_bounds__(W * 64, 2) void staged_kernel(const AttnArgs A)
     int at = start / nma::kTile + mine;
     const int steps = (end - start + nma::kStaged - 1) / nma::kStaged;
     const auto put = [&](int which) {
-        stage.put(buf[which], mine, part, lane);
+        stage.put(lds + which * S::kBytes, mine, part, lane);
         if (part == 0 && lane == 0)
             count[which][mine] = stage.n;
     };
@@ -785,7 +791,7 @@ __global__ __launch_bounds__(W * 64, 2) void staged_kernel(const AttnArgs A)
             page = page_of(A, A.prefix_pages, at + NT, end);
         }
         if (busy) {
-            const uint8_t* kb = buf[i & 1];
+            const uint8_t* kb = lds + (i & 1) * S::kBytes;
             const uint8_t* vb = kb + NT * S::kTileBytes;
             // Operands are read from LDS one tile (keys) or one group of columns (values)
             // ahead of the products that use them; the barriers keep the compiler from
@@ -867,28 +873,38 @@ __global__ __launch_bounds__(W * 64, 2) void staged_kernel(const AttnArgs A)
     }
 }
 
-// Prefix units of few rows: block = (row group, range, key head).
-template <int DT, int BITS, int D, int MT>
-__global__ __launch_bounds__(nma::kWaves * 64, 2) void prefix_kernel(const AttnArgs A)
+// One launch for all units: the first prefix_blocks blocks take prefix units, staged
+// with W waves or (W = 0) like own tokens, the others own-token units = (range, row
+// group, sequence, key head).  Two waves a SIMD: with more than 256 registers to
+// spend the compiler keeps sums in accumulation registers and moves them to and fro
+// (and was seen to reuse a register of an operand too early doing so).
+template <int DT, int BITS, int D, int MT, int W>
+__global__ __launch_bounds__((W ? W : nma::kWaves) * 64, 2) void units_kernel(const AttnArgs A, int prefix_blocks, int direct)
 {
-    __shared__ float lds[join_floats(D, MT)];
-    const int h = blockIdx.x % A.heads, split = blockIdx.x / A.heads % A.prefix_splits;
-    const int group = blockIdx.x / A.heads / A.prefix_splits;
-    const int start = split * A.prefix_chunk, end = min(start + A.prefix_chunk, A.prefix_len);
-    const int at = start / nma::kTile + 2 * __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    attend<DT, BITS, D, MT>(A, A.prefix_pages, h, 0, group * 16 * MT, A.prefix_rows, start, end, end,
-                            page_of(A, A.prefix_pages, at, end), page_of(A, A.prefix_pages, at + 1, end), false,
-                            ((int64_t)split * A.heads + h) * A.prefix_rows, lds);
-}
-
-// Own-token units: block = (range, row group, key head, sequence).
-template <int DT, int BITS, int D>
-__global__ __launch_bounds__(nma::kWaves * 64, 2) void own_kernel(const AttnArgs A, int direct)
-{
-    __shared__ float lds[join_floats(D, 1)];
-    const int h = blockIdx.x % A.heads, b = blockIdx.x / A.heads % A.B;
-    const int group = blockIdx.x / A.heads / A.B % A.own_groups, split = blockIdx.x / A.heads / A.B / A.own_groups;
-    const int start = split * A.own_chunk, at = start / nma::kTile + 2 * __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    constexpr int NW = W ? W : nma::kWaves;
+    constexpr int kJoin = join_bytes(D, W ? 1 : MT, NW), kLds = W && staged_bytes<BITS, D, W ? W : 4>() > kJoin
+                                                                    ? staged_bytes<BITS, D, W ? W : 4>() : kJoin;
+    __shared__ __align__(16) uint8_t lds[kLds];
+    float* const join = reinterpret_cast<float*>(lds);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    if ((int)blockIdx.x < prefix_blocks) {
+        const int unit = blockIdx.x;
+        if constexpr (W > 0) {
+            attend_staged<DT, BITS, D, MT, W>(A, unit, lds);
+        } else {
+            const int h = unit % A.heads, split = unit / A.heads % A.prefix_splits, group = unit / A.heads / A.prefix_splits;
+            const int start = split * A.prefix_chunk, end = min(start + A.prefix_chunk, A.prefix_len);
+            const int at = start / nma::kTile + 2 * wave;
+            attend<DT, BITS, D, MT, NW>(A, A.prefix_pages, h, 0, group * 16 * MT, A.prefix_rows, start, end, end,
+                                        page_of(A, A.prefix_pages, at, end), page_of(A, A.prefix_pages, at + 1, end),
+                                        false, ((int64_t)split * A.heads + h) * A.prefix_rows, join);
+        }
+        return;
+    }
+    const unsigned unit = blockIdx.x - prefix_blocks;
+    const int h = unit % A.heads, b = unit / A.heads % A.B;
+    const int group = unit / A.heads / A.B % A.own_groups, split = unit / A.heads / A.B / A.own_groups;
+    const int start = split * A.own_chunk, at = start / nma::kTile + 2 * wave;
     // The length and the first page numbers come together: the table's entries behind
     // the length may be read, they are only not followed.
     const int32_t* pages = A.page_table + (int64_t)b * A.table_stride;
@@ -897,8 +913,9 @@ __global__ __launch_bounds__(nma::kWaves * 64, 2) void own_kernel(const AttnArgs
     const int len = min(held, A.max_len);
     if (len < 0 || (start >= len && !direct))   // combine looks at the ranges that hold tokens only
         return;
-    attend<DT, BITS, D, 1>(A, pages, h, b, group * 16, A.G, start, min(start + A.own_chunk, len), A.max_len, page0, page1,
-                           direct != 0, A.own_base + ((int64_t)split * A.B + b) * A.Hq + (int64_t)h * A.G, lds);
+    attend<DT, BITS, D, 1, NW>(A, pages, h, b, group * 16, A.G, start, min(start + A.own_chunk, len), A.max_len, page0,
+                               page1, direct != 0,
+                               A.own_base + ((int64_t)split * A.B + b) * A.Hq + (int64_t)h * A.G, join);
 }
 
 // Joins the partial results: a block takes one chunk of a tile of 16 rows (r = b G
@@ -974,32 +991,32 @@ __global__ __launch_bounds__(NW * 64) void combine_kernel(const AttnArgs A)
         A.lse[row] = (mx + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
+template <int DT, int BITS, int D, int MT, int W>
+void launch_units(const AttnArgs& A, int64_t prefix_blocks, int64_t blocks, bool direct, hipStream_t s)
+{
+    hipLaunchKernelGGL((units_kernel<DT, BITS, D, MT, W>), dim3((unsigned)blocks), dim3((W ? W : nma::kWaves) * 64), 0, s,
+                       A, (int)prefix_blocks, direct ? 1 : 0);
+}
+
 template <int DT, int BITS, int D>
 int launch(const nma::AttnPlan& P, const AttnArgs& A, hipStream_t s)
 {
     (void)hipGetLastError();
-    const dim3 block(nma::kWaves * 64);
-    if (P.prefix_splits > 0) {
-        const int64_t blocks = P.prefix_groups * P.prefix_splits * A.heads;
-        if (blocks > INT32_MAX)
-            return NM_ERR_BAD_SHAPE;
-        const dim3 grid((unsigned)blocks);
-        constexpr int kMt = D == 256 ? 1 : 2;       // of the larger units (attn_plan)
-        if (P.waves == 8)
-            hipLaunchKernelGGL((staged_kernel<DT, BITS, D, kMt, 8>), grid, dim3(512), 0, s, A);
-        else if (P.waves == 4) {
-            if constexpr (D != 256)
-                hipLaunchKernelGGL((staged_kernel<DT, BITS, D, kMt, 4>), grid, dim3(256), 0, s, A);
-        } else if (P.mt == 1)
-            hipLaunchKernelGGL((prefix_kernel<DT, BITS, D, 1>), grid, block, 0, s, A);
-        else if constexpr (D != 256)
-            hipLaunchKernelGGL((prefix_kernel<DT, BITS, D, 2>), grid, block, 0, s, A);
-    }
-    const int64_t own_blocks = (P.direct ? 1 : P.own_splits) * P.own_groups * A.B * (int64_t)A.heads;
-    if (own_blocks > INT32_MAX)
+    const int64_t prefix_blocks = P.prefix_groups * P.prefix_splits * A.heads;
+    const int64_t all = prefix_blocks + (P.direct ? 1 : P.own_splits) * P.own_groups * A.B * (int64_t)A.heads;
+    if (all > INT32_MAX)
         return NM_ERR_BAD_SHAPE;
-    if (own_blocks > 0)
-        hipLaunchKernelGGL((own_kernel<DT, BITS, D>), dim3((unsigned)own_blocks), block, 0, s, A, P.direct ? 1 : 0);
+    constexpr int kMt = D == 256 ? 1 : 2;           // of the larger prefix units (attn_plan)
+    if (prefix_blocks == 0 || (P.waves == 0 && P.mt == 1))
+        launch_units<DT, BITS, D, 1, 0>(A, prefix_blocks, all, P.direct, s);
+    else if (P.waves == 8)
+        launch_units<DT, BITS, D, kMt, 8>(A, prefix_blocks, all, false, s);
+    else if constexpr (D != 256) {
+        if (P.waves == 4)
+            launch_units<DT, BITS, D, 2, 4>(A, prefix_blocks, all, false, s);
+        else
+            launch_units<DT, BITS, D, 2, 0>(A, prefix_blocks, all, false, s);
+    }
     if (!P.direct) {
         const int64_t blocks = nma::ceil_div(P.prefix_rows, 16) * A.heads * (D / 16);
         if (blocks > INT32_MAX)
