@@ -148,7 +148,7 @@ int nm_kv_read(const nm_kv_cache* cache, const int64_t* slots, int64_t T, void* 
  * B and Hq 1..65535, B * Hq below 2^26, prefix_len and max_len 0..2^30, scale finite.  o, lse
  * and workspace must not overlap anything else.
  */
-int64_t nm_attn_workspace_bytes(int64_t B, int Hq, int heads, int D, int64_t prefix_len, int64_t max_len);
+int64_t nm_attn_workspace_bytes(int64_t B, int Hq, int heads, int D, int format, int64_t prefix_len, int64_t max_len);
 int nm_attn_decode(const void* q, int64_t q_stride, int64_t B, int Hq, const nm_kv_cache* cache,
                    const int32_t* prefix_pages, int64_t prefix_len, const int32_t* page_table, int64_t table_stride,
                    const int32_t* lens, int64_t max_len, float scale, void* o, float* lse, void* workspace,

@@ -46,7 +46,7 @@ ATTN_SIGNATURES = {
     "nm_kv_scale_bytes": (_I64, [_I64, _I, _I, _I, _I]),
     "nm_kv_write": (_I, [_P, _P, _I64, _P, _I64, _I64, _P, _P]),
     "nm_kv_read": (_I, [_P, _P, _I64, _P, _P, _P]),
-    "nm_attn_workspace_bytes": (_I64, [_I64, _I, _I, _I, _I64, _I64]),
+    "nm_attn_workspace_bytes": (_I64, [_I64, _I, _I, _I, _I, _I64, _I64]),
     "nm_attn_decode": (_I, [_P, _I64, _I64, _I, _P, _P, _I64, _P, _I64, _P, _I64, ctypes.c_float, _P, _P, _P, _I64,
                             _P]),
 }

@@ -248,7 +248,7 @@ def attn_workspace(B, heads_q, cache, max_len, prefix_len=0):
     """A workspace for attn_decode calls of this shape on the cache's device
     (any contents; calls that may run at the same time need one each)."""
     c = _cache(cache)
-    nbytes = attn_lib().nm_attn_workspace_bytes(B, heads_q, c.heads, c.D, prefix_len, max_len)
+    nbytes = attn_lib().nm_attn_workspace_bytes(B, heads_q, c.heads, c.D, _FORMATS[c.format], prefix_len, max_len)
     if nbytes < 0:
         raise ValueError(f"no such attention: {B} sequences, {heads_q} query heads on {c.heads}, {prefix_len} + "
                          f"{max_len} tokens")
@@ -303,7 +303,7 @@ def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, pre
         else:
             op = _check(out, "out", dev, dt, shape)
         if ws is None:
-            nbytes = attn_lib().nm_attn_workspace_bytes(B, hq, c.heads, c.D, prefix_len, max_len)
+            nbytes = attn_lib().nm_attn_workspace_bytes(B, hq, c.heads, c.D, _FORMATS[c.format], prefix_len, max_len)
             if nbytes > 0:
                 ws = q.new_empty(nbytes, dtype=torch.uint8)
                 wsp = ws.data_ptr()

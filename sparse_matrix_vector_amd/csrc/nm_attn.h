@@ -104,7 +104,7 @@ inline void cut(int64_t tokens, int64_t units, int64_t blocks, int64_t longest, 
         *chunk = grain;
         return;
     }
-    int64_t want = ceil_div(blocks, units);
+    int64_t want = blocks > units ? ceil_div(blocks, units) : 1;
     int64_t even = ceil_div(tokens, longest);
     if (even > kMaxRanges)
         even = kMaxRanges;
@@ -118,7 +118,7 @@ inline void cut(int64_t tokens, int64_t units, int64_t blocks, int64_t longest, 
     *splits = ceil_div(tokens, *chunk);
 }
 
-inline AttnPlan attn_plan(int64_t B, int Hq, int heads, int D, int64_t prefix_len, int64_t max_len)
+inline AttnPlan attn_plan(int64_t B, int Hq, int heads, int D, int format, int64_t prefix_len, int64_t max_len)
 {
     AttnPlan p;
     p.G = Hq / heads;
@@ -126,9 +126,20 @@ inline AttnPlan attn_plan(int64_t B, int Hq, int heads, int D, int64_t prefix_le
     p.mt = p.prefix_rows <= 16 || D == 256 ? 1 : 2;
     p.waves = p.prefix_rows <= 16 * p.mt ? 0 : p.prefix_rows <= 64 * p.mt && D != 256 ? 4 : 8;
     p.prefix_groups = ceil_div(p.prefix_rows, 16 * p.mt * (p.waves ? p.waves : 1));
-    cut(prefix_len, heads * p.prefix_groups, p.waves == 8 ? kCus : 2 * kCus, kMaxTokens, &p.prefix_splits,
-        &p.prefix_chunk);
     p.own_groups = ceil_div(p.G, 16);
+    // Prefix units of eight waves have a CU to themselves, and the matrix cores limit
+    // them; own-token units are limited by HBM.  So they share the GPU side by side,
+    // the prefix taking as many CUs as its share of the work: a token of a key head
+    // takes a staged block 52 units of time (at D = 128), an own-token block 22 (16-bit;
+    // by its bytes), of which two thirds, since the batch is rarely full to max_len.
+    // 32 sequences of 64 heads, 16-bit, 32741 tokens + up to 1024: 256 blocks 81.5 us, 192
+    // 78.0, 160 79.2; 8192 + up to 1024: 47.9 / 45.0 / 39.8; MX8, 32768 + up to 4096: 96.0 /
+    // 94.7 / 83.1; 32768 alone: 68.4 / 71.7 / 77.4.
+    const double staged = 52.0 * (double)(prefix_len * heads * p.prefix_groups);
+    const double own = 22.0 * 2 / 3 * format_bits(format) / 16 * (double)(B * heads * p.own_groups) * (double)max_len;
+    const int64_t cus = max_len == 0 ? kCus : (int64_t)(kCus * (staged / (staged + own)));
+    cut(prefix_len, heads * p.prefix_groups, p.waves == 8 ? cus : 2 * kCus, kMaxTokens, &p.prefix_splits,
+        &p.prefix_chunk);
     // Own tokens (us; 8 key heads, MX8, x blocks for each CU): 32 sequences of up to
     // 1024 tokens, one unit per CU: 1 block 12.3, 2 blocks 14.2, 3 blocks 14.8; 16 of up
     // to 8192: 38.3 / 34.2 / 35.8; 8 of up to 32768: 69.8 / 58.1 / 61.8.  Longest range

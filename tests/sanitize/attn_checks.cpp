@@ -195,7 +195,7 @@ long plans()
                             const int64_t Hq = (int64_t)heads * G;
                             if (Hq > 65535 || B * Hq >= nma::kMaxRows)
                                 continue;
-                            const nma::AttnPlan p = nma::attn_plan(B, (int)Hq, heads, D, P, ml);
+                            const nma::AttnPlan p = nma::attn_plan(B, (int)Hq, heads, D, (int)(n % 3), P, ml);
                             const auto covers = [](int64_t splits, int64_t chunk, int64_t tokens) {
                                 return chunk > 0 && chunk % nma::kStep == 0 && splits * chunk >= tokens &&
                                        (splits == 0 || (splits - 1) * chunk < tokens) && splits * chunk <= (int64_t(1) << 31);

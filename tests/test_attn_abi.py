@@ -136,9 +136,10 @@ def test_attention_refusals(kw, want):
 
 def test_attention_workspace_bytes():
     f = L.attn_lib().nm_attn_workspace_bytes
-    assert f(1, 32, 8, 128, 0, 40) == 0 and f(4, 8, 8, 64, 0, 0) == 0
-    assert f(32, 64, 8, 128, 32768, 1024) > 0
-    for bad in ((0, 8, 8, 64, 0, 1), (1, 7, 2, 64, 0, 1), (1, 8, 8, 80, 0, 1), (1, 8, 8, 64, -1, 1), (1, 8, 8, 64, 0, 2 ** 31)):
+    assert f(1, 32, 8, 128, 0, 0, 40) == 0 and f(4, 8, 8, 64, 1, 0, 0) == 0
+    assert f(32, 64, 8, 128, 2, 32768, 1024) > 0
+    for bad in ((0, 8, 8, 64, 0, 0, 1), (1, 7, 2, 64, 0, 0, 1), (1, 8, 8, 80, 0, 0, 1), (1, 8, 8, 64, 0, -1, 1),
+                (1, 8, 8, 64, 0, 0, 2 ** 31), (1, 8, 8, 64, 3, 0, 1), (1, 8, 8, 64, -1, 0, 1)):
         assert f(*bad) == -1
 
 
