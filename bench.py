@@ -73,6 +73,10 @@ def parse():
     p.add_argument("--crossover", action="store_true",
                    help="batch crossover study instead of the step: Qwen3-32B MLP shapes (2:4 bf16) at B = 1..32, "
                         "sparse vs the dense kernel vs torch's matmul; prints one JSON line")
+    p.add_argument("--decode-layers", action="store_true",
+                   help="decode layers with their attention instead of the step: Llama-3.1-8B shapes (2:4 fp16) with an "
+                        "8192-token context in each cache format, at batch 1, 8 and 32, the last behind a shared prefix "
+                        "too; prints one JSON line")
     p.add_argument("--no-configs", action="store_true",
                    help="leave out the other workloads' step figures (extras.configs) from the default run")
     p.add_argument("--no-glu", action="store_true",
@@ -585,6 +589,71 @@ def crossover(torch, nm, I, batches=(1, 2, 4, 8, 16, 32)):
     return out
 
 
+def decode_layers(torch, nm, I, layers=4, context=8192, page=64, reps=10):
+    """Whole decode layers but for the residual path: q+k+v in one launch, the
+    rotation, the cache write, attention over `context` tokens a sequence, o,
+    gate+up with SwiGLU and down, every layer on weights and a cache of its
+    own, captured into one graph; beside it the same graph without the three
+    calls between q+k+v and o.  "shared" puts all but 512 of the tokens into a
+    prefix that the batch has in common."""
+    dt, hq, hk, D = torch.float16, 32, 8, 128
+    shapes = I.LLAMA31_8B
+    packs = [{nme: nm.pack(I.weight(*shapes[nme], dt, I.seed_of("layers", l, nme), device="cuda"), None, 2, 4)
+              for nme in I.LAYER_ORDER} for l in range(layers)]
+    freq = torch.pow(500000.0, -torch.arange(0, D, 2, dtype=torch.float64) / D).float().cuda()
+    ws = nm.workspace()
+    out = []
+    for B, fmt, shared in ((1, "16", 0), (1, "mx8", 0), (8, "mx8", 0), (32, "16", 0), (32, "mx8", 0), (32, "mx4", 0),
+                           (32, "16", 1), (32, "mx8", 1)):
+        prefix, own = (context - 512, 512) if shared else (0, context)
+        n_pages = (prefix + B * own) // page
+        caches = [nm.KVCache(n_pages, page, hk, D, dt, fmt) for _ in range(layers)]
+        for c in caches:
+            for t in range(0, n_pages * page, 16384):
+                n = min(16384, n_pages * page - t)
+                k, v = (torch.randn((n, hk, D), device="cuda").to(dt) for _ in range(2))
+                nm.kv_write(c, k, v, torch.arange(t, t + n, device="cuda"))
+        order = torch.randperm(n_pages, device="cuda").int()
+        pp, table = order[:prefix // page].contiguous(), order[prefix // page:].view(B, own // page).contiguous()
+        lens = torch.full((B,), own, dtype=torch.int32, device="cuda")
+        pos = torch.full((B,), context - 1, dtype=torch.int32, device="cuda")
+        slots = table[:, -1].long() * page + page - 1
+        x = I.activation_normal(B, 4096, dt, I.seed_of("layers", "x", B), device="cuda")
+        aws = nm.attn_workspace(B, hq, caches[0], own, prefix)
+
+        def step(attention):
+            for w, c in zip(packs, caches):
+                q, k, v = nm.spmv_multi([w["q"], w["k"], w["v"]], x, ws=ws)
+                if attention:
+                    qr, kr = nm.qk_norm_rope(q.view(B, hq, D), k.view(B, hk, D), pos, freq)
+                    nm.kv_write(c, kr, v.view(B, hk, D), slots)
+                    q = nm.attn_decode(qr, c, table, lens, max_len=own, prefix_pages=pp, prefix_len=prefix, ws=aws)
+                nm.spmv_multi([w["o"]], q.view(B, hq * D), ws=ws)
+                nm.spmv_multi([w["down"]], nm.spmv_swiglu(w["gate"], w["up"], x), ws=ws)
+
+        us = []
+        for attention in (True, False):
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.stream(s):
+                step(attention)
+                torch.cuda.synchronize()
+                with torch.cuda.graph(g, stream=s):
+                    step(attention)
+            torch.cuda.synchronize()
+            us.append(trials_us(torch, g.replay, reps, layers)[1])
+            del g
+        row = D * {"16": 16, "mx8": 8, "mx4": 4}[fmt] // 8 + (0 if fmt == "16" else D // 32)
+        cache_bytes = 2 * hk * row * (prefix + B * own)
+        out.append({"B": B, "cache": fmt, "prefix": prefix, "own": own, "layer_us": round(us[0], 2),
+                    "products_us": round(us[1], 2), "attention_us": round(us[0] - us[1], 2), "cache_bytes": cache_bytes,
+                    "cache_gbs": round(cache_bytes / (us[0] - us[1]) / 1e3, 1)})
+        del caches, aws
+        torch.cuda.empty_cache()
+    return out
+
+
 def main():
     a = parse()
     if a.gpus != 1:
@@ -603,6 +672,11 @@ def main():
         torch.cuda.set_device(0)
         print(json.dumps({"crossover": crossover(torch, nm, I), "workload": "Qwen3-32B MLP, 2:4 sparse, bf16"}),
               flush=True)
+        return
+    if a.decode_layers:
+        torch.cuda.set_device(0)
+        print(json.dumps({"decode_layers": decode_layers(torch, nm, I),
+                          "workload": "Llama-3.1-8B decode layers with attention, 2:4 sparse, fp16"}), flush=True)
         return
     spec = specs[a.workload]
     desc, _, layers, dts, n, m, B = spec[:7]

@@ -296,6 +296,44 @@ def test_attention_unseen_tokens(nm, fmt, garbage):
     assert same(dirty.run(), clean.run())
 
 
+# Rows of a key head that see the prefix: 48 and 160 of 128 columns, 48 of 256, 40 of 64.
+SHARED = ((128, 4, 1, 12), (128, 10, 2, 32), (256, 8, 1, 6), (64, 20, 4, 8))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", (F16, BF16))
+@pytest.mark.parametrize("D,hq,heads,B", SHARED)
+def test_attention_shared_prefix(nm, dtype, fmt, D, hq, heads, B):
+    """Prefixes of one token, around the 64 that are staged at a time, and of several ranges, own tokens beside them;
+    with garbage wherever no sequence looks; a page of the prefix and one of a sequence outside the cache."""
+    for i, P in enumerate((1, 63, 65, 200, 1500)):
+        lens = [(7 * b + i) % 40 for b in range(B)]
+        lens[1] = -1
+        b = Batch(nm, dtype, fmt, D, hq, heads, 16, P, lens, tag=i)
+        lse = torch.empty((B, hq), device="cuda")
+        o = b.run(lse=lse)
+        b.check(o, lse)
+        dirty = Batch(nm, dtype, fmt, D, hq, heads, 16, P, lens, tag=i, garbage=(float("nan"), float("inf"))[i % 2])
+        seen = [k for k, n in enumerate(lens) if n >= 0]
+        assert same(dirty.run()[seen], o[seen])
+    drop = set(range(32, 48)) | set(b.tokens(0)[1500:1516])
+    dirty.prefix_pages[2] = -1
+    dirty.table[0, 0] = dirty.cache.n_pages
+    dirty.check(dirty.run(lse=lse), lse, drop=drop)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_shared_prefix_peaked(nm, fmt):
+    """Scores of which few count, the largest ones late: the running maximum grows from step to step."""
+    b = Batch(nm, BF16, fmt, 128, 16, 2, 32, 700, [50] * 20, scale=1.0)
+    ramp = torch.linspace(0.2, 6, b.k.shape[0]).view(-1, 1, 1).cuda()
+    b.k = (b.k.float() * ramp).to(BF16)
+    nm.kv_write(b.cache, b.k, b.v, b.slots.cuda())
+    b.qk = ref.quantised(ref.f64(b.k), fmt)
+    lse = torch.empty((20, 16), device="cuda")
+    b.check(b.run(lse=lse), lse)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_attention_seen_nan_stays_in_its_rows(nm, fmt):
     b = Batch(nm, BF16, fmt, 128, 4, 2, 16, 0, [40, 40])
@@ -442,6 +480,29 @@ def test_graph_replays_with_new_inputs(nm):
         eager = step(e)
         assert same(captured[:2], eager[:2]), rep
         assert torch.equal(a.cache.k, e.cache.k) and torch.equal(a.cache.v, e.cache.v)
+        del junk
+
+
+def test_graph_of_a_shared_prefix(nm):
+    """A captured call with staged prefix units, replayed with other queries and lengths."""
+    b = Batch(nm, BF16, "mx8", 128, 16, 2, 32, 1000, [60] * 24, tag=6)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        b.run()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            captured = b.run()
+    torch.cuda.synchronize()
+    for rep in range(4):
+        b.q.copy_(rnd(b.q.shape, BF16, "gq", rep))
+        b.t_lens.copy_(ints(24, 0, 61, "gl", rep))
+        junk = torch.randn(1 << 20, device="cuda").sum()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(captured, b.run()), rep
         del junk
 
 
