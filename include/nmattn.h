@@ -67,10 +67,10 @@ int nm_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_st
  *              power-of-two scale 2^e per 32 consecutive columns of a token's head.
  *   NM_KV_MX4  4-bit codes (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and sign), scales
  *              as for MX8.
- * e is the least integer in -126..127 with max|x| <= M 2^e over the 32 columns,
- * M = 448 (e4m3) or 6 (e2m1); a code is x / 2^e rounded to nearest, ties to the
- * even code.  32 columns that hold a NaN or an infinity read back as NaN, all
- * of them.
+ * e is the least integer with max|x| <= M 2^e over the 32 columns, M = 448 (e4m3)
+ * or 6 (e2m1), but at least -126 in a bfloat16 cache, -14 (MX8) or -22 (MX4) in an
+ * fp16 one; a code is x / 2^e rounded to nearest, ties to the even code.  32
+ * columns that hold a NaN or an infinity read back as NaN, all of them.
  *
  * k, v       nm_kv_bytes(...) bytes each, 16-byte aligned.
  * k_scale, v_scale   nm_kv_scale_bytes(...) bytes each, 16-byte aligned (NULL for
@@ -139,13 +139,12 @@ int nm_kv_read(const nm_kv_cache* cache, const int64_t* slots, int64_t T, void* 
  *                      256-byte aligned, any contents; may be NULL when that is 0.
  * A page number outside the cache is not followed: its tokens count as absent.
  * Scores, softmax statistics and sums are fp32; the weights of the sum are
- * rounded to the operand type of the matrix cores (dtype for NM_KV_16; bfloat16
- * for a quantised cache of bfloat16, two bfloat16 parts for one of fp16), o once
- * to dtype.  Results do not depend on other calls and repeat bit for bit.
+ * rounded to dtype, the operand type of the matrix cores, and o once to dtype.
+ * Results do not depend on other calls and repeat bit for bit.
  * Infinities or NaN in a token that is seen give infinities or NaN in the rows
- * that see it; in a token that is not seen they have no effect.  (A quantised
- * cache holds magnitudes up to 2^127.)
- * B and Hq 1..65535, B * Hq below 2^26, prefix_len and max_len 0..2^30, scale finite.  o, lse
+ * that see it; in a token that is not seen they have no effect.  (In a quantised
+ * bfloat16 cache magnitudes of 2^127 and more count as infinities here.)
+ * B and Hq 1..65535, B * Hq below 2^26, prefix_len and max_len 0..2^30, |scale| <= 1e30.  o, lse
  * and workspace must not overlap anything else.
  */
 int64_t nm_attn_workspace_bytes(int64_t B, int Hq, int heads, int D, int format, int64_t prefix_len, int64_t max_len);

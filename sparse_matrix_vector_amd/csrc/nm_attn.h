@@ -58,6 +58,16 @@ constexpr int scale_tile_bytes(int D) { return kTile * D / kBlock; }
 constexpr int k_scale_offset(int D, int token, int block) { return token * (D / kBlock) + block; }
 constexpr int v_scale_offset(int token, int block) { return block * kTile + token; }
 
+// A scale byte b stands for codes times 2^(b - bias).  Attention turns codes into
+// operands of the cache's dtype times 2^(b - 127), and that has to be exact.  It is
+// in bfloat16, whose range is fp32's; fp16 ends at 65504, below the 65536 to which a
+// large value may be rounded, and at multiples of 2^-24.  So an fp16 cache's operands
+// are half its values (bias 126, made good in the scores' scale and in the output),
+// and its e stays where the smallest codes, 2^-9 (e4m3) and 2^-1 (e2m1), do not fall
+// below 2^-23.  255 marks a block that held a NaN or an infinity.
+constexpr int scale_bias(int dtype) { return dtype == NM_FP16 ? 126 : 127; }
+constexpr int least_exponent(int dtype, int bits) { return dtype == NM_BF16 ? -126 : bits == 8 ? -14 : -22; }
+
 // ---- the plan of nm_attn_decode ----------------------------------------------
 //
 // Work is cut into units of (row group, key head, range of tokens), one block

@@ -63,6 +63,7 @@ struct AttnArgs {
     // (and a scale of zero) being put into q, which is exact.
     float scale;
     uint32_t q_and, q_xor;
+    float o_scale;              // 2 where the operands are half the cached values, else 1
 };
 
 template <int DT>
@@ -93,10 +94,29 @@ __device__ __forceinline__ float quarters_sum(float v)
     return bits_f32(p.x) + bits_f32(p.y);
 }
 
+// Two neighbouring codes of a word times a power of two, as two 16-bit floats.
+template <int DT, bool HIGH>
+__device__ __forceinline__ uint32_t from_fp8(uint32_t w, float f)
+{
+    if constexpr (DT == NM_FP16)
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, f, HIGH));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, f, HIGH));
+}
+
+template <int DT, int BYTE>
+__device__ __forceinline__ uint32_t from_fp4(uint32_t w, float f)
+{
+    if constexpr (DT == NM_FP16)
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, f, BYTE));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, BYTE));
+}
+
 // One lane's part of a 16-token tile of keys or values as loaded, and how it
-// becomes operands.  BITS 16: as it is.  Codes: converted to bfloat16 with the
-// scale applied, which is exact (at most four significant bits).
-template <int BITS, int D>
+// becomes operands of the cache's dtype.  BITS 16: as it is.  Codes: converted with
+// the scale applied, which is exact (nm_attn.h: scale bytes).
+template <int DT, int BITS, int D>
 struct Cache {
     static constexpr int kCb = nma::k_chunk_bytes(D, BITS);
     static constexpr int kVb = nma::v_chunk_bytes(D, BITS);
@@ -169,18 +189,12 @@ struct Cache {
             const int block = s * 8 / kE * (4 * kE / nma::kBlock) + kg * kE / nma::kBlock;
             const uint32_t word = kBlocks > 4 && block >= 4 ? sc.w[kBlocks > 4 ? 1 : 0] : sc.w[0];
             const float f = scale_value((word >> (8 * (block % 4))) & 255u);
-            if constexpr (BITS == 8) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    out[i] = __builtin_bit_cast(
-                        uint32_t, i % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i / 2], f, true)
-                                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i / 2], f, false));
-            } else {
-                out = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], f, 0)),
-                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], f, 1)),
-                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], f, 2)),
-                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], f, 3))};
-            }
+            if constexpr (BITS == 8)
+                out = u32x4{from_fp8<DT, false>(w[0], f), from_fp8<DT, true>(w[0], f), from_fp8<DT, false>(w[1], f),
+                            from_fp8<DT, true>(w[1], f)};
+            else
+                out = u32x4{from_fp4<DT, 0>(w[0], f), from_fp4<DT, 1>(w[0], f), from_fp4<DT, 2>(w[0], f),
+                            from_fp4<DT, 3>(w[0], f)};
         }
         return out;
     }
@@ -218,15 +232,12 @@ struct Cache {
                 const int at = (r * kPer + 2 * p) * BITS / 8;
                 const uint32_t x = w[at / 4];
                 if constexpr (BITS == 8)
-                    pair[r][p] =
-                        __builtin_bit_cast(uint32_t, at % 4 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, f, true)
-                                                            : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, f, false));
+                    pair[r][p] = at % 4 ? from_fp8<DT, true>(x, f) : from_fp8<DT, false>(x, f);
                 else
-                    pair[r][p] = __builtin_bit_cast(
-                        uint32_t, at % 4 == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 0)
-                                  : at % 4 == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 1)
-                                  : at % 4 == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 2)
-                                                : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, f, 3));
+                    pair[r][p] = at % 4 == 0   ? from_fp4<DT, 0>(x, f)
+                                 : at % 4 == 1 ? from_fp4<DT, 1>(x, f)
+                                 : at % 4 == 2 ? from_fp4<DT, 2>(x, f)
+                                               : from_fp4<DT, 3>(x, f);
             }
         }
         // (column 2p, column 2p + 1) by token -> (token 2i, token 2i + 1) by column
@@ -268,26 +279,12 @@ __device__ __forceinline__ TileRef tile_ref(const AttnArgs& A, int page, int a, 
     return t;
 }
 
-// Operand type of both products; fp16 rows against a quantised cache (whose values
-// are bfloat16 operands) are taken as two bfloat16 parts.
-template <int DT, int BITS>
-constexpr int op_type()
-{
-    return BITS == 16 ? DT : NM_BF16;
-}
-template <int DT, int BITS>
-constexpr bool split_rows()
-{
-    return BITS != 16 && DT == NM_FP16;
-}
-
 // The lane's row of each of MT row tiles, as right operands of the score product.
 // Rows are query heads: row r is head h G + r % G of sequence b0 + r / G.
 template <int DT, int BITS, int D, int MT>
 struct Rows {
     static constexpr int kSteps = D / 32;                            // k-steps of the score product
-    static constexpr bool kSplit = split_rows<DT, BITS>();
-    u32x4 hi[MT][kSteps], lo[kSplit ? MT : 1][kSplit ? kSteps : 1];
+    u32x4 op[MT][kSteps];
 
     __device__ __forceinline__ void load(const AttnArgs& A, int h, int b0, int row0, int R, int m, int kg)
     {
@@ -297,22 +294,10 @@ struct Rows {
             const uint16_t* row = A.q + (int64_t)(b0 + r / A.G) * A.q_stride + (int64_t)(h * A.G + r % A.G) * D;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                u32x4 x = {0u, 0u, 0u, 0u};
+                op[g][s] = u32x4{0u, 0u, 0u, 0u};
                 if (r < R)
-                    x = (*reinterpret_cast<const u32x4*>(row + Cache<BITS, D>::column(s, kg)) & A.q_and) ^ A.q_xor;
-                if constexpr (kSplit) {
-                    // fp16 = the nearest bfloat16 plus a remainder that bfloat16 holds exactly
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const f32x2 p = unpack2<NM_FP16>(x[i]);
-                        const uint32_t top = pack2<NM_BF16>(p.x, p.y);
-                        const f32x2 back = unpack2<NM_BF16>(top);
-                        hi[g][s][i] = top;
-                        lo[g][s][i] = pack2<NM_BF16>(p.x - back.x, p.y - back.y);
-                    }
-                } else {
-                    hi[g][s] = x;
-                }
+                    op[g][s] =
+                        (*reinterpret_cast<const u32x4*>(row + Cache<DT, BITS, D>::column(s, kg)) & A.q_and) ^ A.q_xor;
             }
         }
     }
@@ -335,10 +320,9 @@ __device__ __forceinline__ void mask_scores(f32x4 (&sc)[MT][NT], const int (&n)[
 // The softmax weights of a step of NT tiles, as right operands of the second
 // product (one for each pair of tiles); updates the rows' maxima, sums and,
 // where a maximum grows, what has been added up so far.
-template <int DT, int BITS, int MT, int NT>
+template <int DT, int MT, int NT>
 struct Weights {
-    static constexpr bool kSplit = split_rows<DT, BITS>();
-    u32x4 hi[MT][NT / 2], lo[kSplit ? MT : 1][kSplit ? NT / 2 : 1];
+    u32x4 op[MT][NT / 2];
 
     template <int PER>
     __device__ __forceinline__ void find(const f32x4 (&sc)[MT][NT], float (&mx)[MT], float (&sum)[MT],
@@ -371,13 +355,8 @@ struct Weights {
                     sum[g] += p[i];
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    hi[g][t][i] = pack2<op_type<DT, BITS>()>(p[2 * i], p[2 * i + 1]);
-                    if constexpr (kSplit) {
-                        const f32x2 back = unpack2<NM_BF16>(hi[g][t][i]);
-                        lo[g][t][i] = pack2<NM_BF16>(p[2 * i] - back.x, p[2 * i + 1] - back.y);
-                    }
-                }
+                for (int i = 0; i < 4; ++i)
+                    op[g][t][i] = pack2<DT>(p[2 * i], p[2 * i + 1]);
             }
         }
     }
@@ -416,10 +395,8 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
                                        int start, int end, int limit, int page0, int page1, bool direct,
                                        int64_t part_row, float* lds)
 {
-    using C = Cache<BITS, D>;
+    using C = Cache<DT, BITS, D>;
     constexpr int kSteps = D / 32;                                   // k-steps of the score product
-    constexpr int kOp = op_type<DT, BITS>();
-    constexpr bool kSplit = split_rows<DT, BITS>();
     constexpr int kPer = D / 16;
     const int lane = threadIdx.x % 64, m = lane % 16, kg = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -490,9 +467,7 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
                 const u32x4 a = C::k_operand(kr[u], ks[u], s, kg);
 #pragma unroll
                 for (int g = 0; g < MT; ++g) {
-                    sc[g][u] = mfma<kOp>(a, rows.hi[g][s], sc[g][u]);
-                    if constexpr (kSplit)
-                        sc[g][u] = mfma<kOp>(a, rows.lo[g][s], sc[g][u]);
+                    sc[g][u] = mfma<DT>(a, rows.op[g][s], sc[g][u]);
                 }
             }
         }
@@ -503,7 +478,7 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
             const int n[2] = {cur[0].n, cur[1].n};
             mask_scores(sc, n, kg);
         }
-        Weights<DT, BITS, MT, 2> w;
+        Weights<DT, MT, 2> w;
         w.find(sc, mx, sum, acc, A.scale);
         // values
         uint32_t vo[2][2 * kPer];
@@ -527,9 +502,7 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
             const u32x4 a = {vo[0][2 * j], vo[0][2 * j + 1], vo[1][2 * j], vo[1][2 * j + 1]};
 #pragma unroll
             for (int g = 0; g < MT; ++g) {
-                acc[g][j] = mfma<kOp>(a, w.hi[g][0], acc[g][j]);
-                if constexpr (kSplit)
-                    acc[g][j] = mfma<kOp>(a, w.lo[g][0], acc[g][j]);
+                acc[g][j] = mfma<DT>(a, w.op[g][0], acc[g][j]);
             }
         }
         if constexpr (more()) {
@@ -594,7 +567,7 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
         if (r >= R)
             continue;
         if (direct) {
-            const float f = sum[g] > 0.0f || sum[g] != sum[g] ? 1.0f / sum[g] : 0.0f;
+            const float f = sum[g] > 0.0f || sum[g] != sum[g] ? A.o_scale / sum[g] : 0.0f;
             const int64_t row = (int64_t)b0 * A.Hq + h * A.G + r;
             uint16_t* o = A.o + row * D + kg * (D / 4);
 #pragma unroll
@@ -622,9 +595,9 @@ constexpr int join_bytes(int D, int mt, int waves) { return waves / 2 * mt * (D 
 // buffers; the next four are on their way while the current ones are multiplied.
 //   keys    [tile][k-step][lane] 16 bytes
 //   values  [tile pair][column j][lane] 16 bytes, 8 of each tile
-template <int BITS, int D, int W>
+template <int DT, int BITS, int D, int W>
 struct Stage {
-    using C = Cache<BITS, D>;
+    using C = Cache<DT, BITS, D>;
     static constexpr int kTiles = nma::kStaged / nma::kTile;
     static constexpr int kShare = W / kTiles;                // waves that load one tile
     static constexpr int kSteps = D / 32, kPer = D / 16;
@@ -739,15 +712,14 @@ struct Stage {
 template <int BITS, int D, int W>
 constexpr int staged_bytes()
 {
-    return 2 * Stage<BITS, D, W>::kBytes + 2 * Stage<BITS, D, W>::kTiles * 4;
+    return 2 * Stage<NM_FP16, BITS, D, W>::kBytes + 2 * Stage<NM_FP16, BITS, D, W>::kTiles * 4;
 }
 
 template <int DT, int BITS, int D, int MT, int W>
 __device__ __forceinline__ void attend_staged(const AttnArgs& A, int unit, uint8_t* lds)
 {
-    using S = Stage<BITS, D, W>;
-    constexpr int kOp = op_type<DT, BITS>(), NT = S::kTiles, kSteps = S::kSteps, kPer = S::kPer;
-    constexpr bool kSplit = split_rows<DT, BITS>();
+    using S = Stage<DT, BITS, D, W>;
+    constexpr int NT = S::kTiles, kSteps = S::kSteps, kPer = S::kPer;
     constexpr int kGroup = 4;                                // value operands read at a time
     int(*const count)[NT] = reinterpret_cast<int(*)[NT]>(lds + 2 * S::kBytes);
     const int lane = threadIdx.x % 64, m = lane % 16, kg = lane / 16;
@@ -823,9 +795,7 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, int unit, uint8
                 for (int s = 0; s < kSteps; ++s)
 #pragma unroll
                     for (int g = 0; g < MT; ++g) {
-                        sc[g][u] = mfma<kOp>(ka[u % 2][s], rows.hi[g][s], sc[g][u]);
-                        if constexpr (kSplit)
-                            sc[g][u] = mfma<kOp>(ka[u % 2][s], rows.lo[g][s], sc[g][u]);
+                        sc[g][u] = mfma<DT>(ka[u % 2][s], rows.op[g][s], sc[g][u]);
                     }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -838,7 +808,7 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, int unit, uint8
             }
             if (!whole)
                 mask_scores(sc, n, kg);
-            Weights<DT, BITS, MT, NT> w;
+            Weights<DT, MT, NT> w;
             w.find(sc, mx, sum, acc, A.scale);
             constexpr int kGroups = NT / 2 * kPer / kGroup;
 #pragma unroll
@@ -851,9 +821,7 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, int unit, uint8
                     const int j = (x * kGroup + c) % kPer, t = (x * kGroup + c) / kPer;
 #pragma unroll
                     for (int g = 0; g < MT; ++g) {
-                        acc[g][j] = mfma<kOp>(va[x % 2][c], w.hi[g][t], acc[g][j]);
-                        if constexpr (kSplit)
-                            acc[g][j] = mfma<kOp>(va[x % 2][c], w.lo[g][t], acc[g][j]);
+                        acc[g][j] = mfma<DT>(va[x % 2][c], w.op[g][t], acc[g][j]);
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -983,7 +951,7 @@ __global__ __launch_bounds__(NW * 64) void combine_kernel(const AttnArgs A)
         sum += sums[w][lane];
         acc += box[w - 1][lane];
     }
-    acc *= sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    acc *= sum > 0.0f || sum != sum ? A.o_scale / sum : 0.0f;
     const int64_t row = (int64_t)b * A.Hq + (int64_t)h * A.G + g;
     *reinterpret_cast<u32x2*>(A.o + row * D + kg * (D / 4) + chunk * 4) =
         u32x2{pack2<DT>(acc[0], acc[1]), pack2<DT>(acc[2], acc[3])};
@@ -1088,7 +1056,9 @@ int nmk::attn_decode(const nma::AttnPlan& plan, const void* q, int64_t q_stride,
     A.own_groups = (int)plan.own_groups;
     A.own_splits = (int)plan.own_splits;
     A.own_chunk = (int)plan.own_chunk;
-    A.scale = scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e;
+    // Codes of an fp16 cache become halves of their values (nm_attn.h: scale bytes).
+    A.o_scale = cache.format != NM_KV_16 && cache.dtype == NM_FP16 ? 2.0f : 1.0f;
+    A.scale = scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e * A.o_scale;
     A.q_and = scale == 0.0f ? 0u : 0xFFFFFFFFu;
     A.q_xor = scale < 0.0f ? 0x80008000u : 0u;
     hipStream_t s = static_cast<hipStream_t>(stream);

@@ -193,7 +193,7 @@ int nm_attn_decode(const void* q, int64_t q_stride, int64_t B, int Hq, const nm_
         return st;
     const int64_t need = attn_shape(B, Hq, cache->heads, cache->D, cache->format, prefix_len, max_len);
     const int64_t width = (int64_t)Hq * cache->D;
-    if (need < 0 || !stride_ok(B, q_stride, width) || !std::isfinite(scale))
+    if (need < 0 || !stride_ok(B, q_stride, width) || !(std::fabs(scale) <= 1e30f))
         return NM_ERR_BAD_SHAPE;
     const int64_t own_pages = nma::ceil_div(max_len, cache->page_size);
     if (max_len > 0 && B > 1 && (table_stride < own_pages || table_stride > kMaxStride))

@@ -197,15 +197,16 @@ __device__ __forceinline__ int64_t tile_of(const CacheArgs& A, int64_t slot, int
     return (page * A.heads + h) * ((1 << A.page_shift) / nma::kTile) + place / nma::kTile;
 }
 
-// Exponent e (biased by 127) of the 32 columns whose largest magnitude is
-// `top`: the least with top <= M 2^e, M = 1.75 * 2^8 or 1.5 * 2^2, so one less or
-// equal to top's own exponent minus 8 (2), by a compare of the fractions.
-template <int BITS>
+// Scale byte of the 32 columns whose largest magnitude is `top`: the least e with
+// top <= M 2^e, M = 1.75 * 2^8 or 1.5 * 2^2, so top's own exponent minus 8 (2), and one
+// more if its fraction is above M's.
+template <int DT, int BITS>
 __device__ __forceinline__ int scale_byte(float top)
 {
     const uint32_t b = f32_bits(top);
-    const int e = (int)(b >> 23) - (BITS == 8 ? 8 : 2) + ((b & 0x7FFFFFu) > (BITS == 8 ? 0x600000u : 0x400000u) ? 1 : 0);
-    return min(max(e, 1), 254);
+    const int e = (int)(b >> 23) - 127 - (BITS == 8 ? 8 : 2) +
+                  ((b & 0x7FFFFFu) > (BITS == 8 ? 0x600000u : 0x400000u) ? 1 : 0);
+    return max(e, nma::least_exponent(DT, BITS)) + nma::scale_bias(DT);
 }
 
 // The cache kernels' work: a wave takes kRows rows by kCols columns, a lane eight
@@ -269,11 +270,11 @@ __device__ __forceinline__ void write_unit(const CacheArgs& A, int side, int64_t
         top = fmaxf(top, __shfl_xor(top, 1));
         top = fmaxf(top, __shfl_xor(top, 2));
         bad = f32_bits(top) == 0x7F800000u;
-        const int byte = bad ? 255 : scale_byte<BITS>(top);
+        const int byte = bad ? 255 : scale_byte<DT, BITS>(top);
         // x 2^-e is exact (a code's subnormals lie far above fp32's), so one rounding
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            x[j] = bad ? 0.0f : ldexpf(x[j], 127 - byte);
+            x[j] = bad ? 0.0f : ldexpf(x[j], nma::scale_bias(DT) - byte);
         if constexpr (BITS == 8) {
             u32x2 c = {0u, 0u};
 #pragma unroll
@@ -391,7 +392,7 @@ __device__ __forceinline__ u32x4 read_unit(const CacheArgs& A, int side, int64_t
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            x[j] = byte == 255u ? scale_value(byte) : saturate<DT>(ldexpf(x[j], (int)byte - 127));
+            x[j] = byte == 255u ? scale_value(byte) : saturate<DT>(ldexpf(x[j], (int)byte - nma::scale_bias(DT)));
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             out[j] = pack2<DT>(x[2 * j], x[2 * j + 1]);

@@ -29,9 +29,13 @@ GRID = {"mx8": _e4m3(), "mx4": np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
 TOP = {"mx8": 448.0, "mx4": 6.0}
 
 
-def quantised(x, fmt, dtype=None):
-    """The values a cache of format fmt holds for x [..., D]; with dtype, as
-    they are read back into it (saturating)."""
+LEAST = {(torch.bfloat16, "mx8"): -126, (torch.bfloat16, "mx4"): -126,       # least exponent of a scale
+         (torch.float16, "mx8"): -14, (torch.float16, "mx4"): -22}
+
+
+def quantised(x, fmt, dtype, read=False):
+    """The values a cache of format fmt holds for x [..., D] of dtype; with
+    read, as they are read back into it (saturating)."""
     x = np.asarray(x, dtype=np.float64)
     if fmt == "16":
         return x
@@ -42,15 +46,15 @@ def quantised(x, fmt, dtype=None):
         if not np.isfinite(b).all():
             out[i] = np.nan
             continue
-        top, e = np.abs(b).max(), -126
-        while top > TOP[fmt] * 2.0 ** e and e < 127:
+        top, e = np.abs(b).max(), LEAST[dtype, fmt]
+        while top > TOP[fmt] * 2.0 ** e:
             e += 1
         a = np.abs(b) * 2.0 ** -e
         below, upto = np.searchsorted(mid, a, side="left"), np.searchsorted(mid, a, side="right")
         code = np.where(below % 2 == 0, below, upto)
         out[i] = np.copysign(grid[code] * 2.0 ** e, b)
     out = out.reshape(x.shape)
-    return out if dtype is None else np.clip(out, -LARGEST[dtype], LARGEST[dtype])
+    return out if not read else np.clip(out, -LARGEST[dtype], LARGEST[dtype])
 
 
 # ---- norm and rotation --------------------------------------------------------
@@ -85,17 +89,16 @@ def qk_close(got, x, w, eps, positions, inv_freq, interleaved):
 
 # ---- attention ------------------------------------------------------------------
 
-def attend(q, keys, values, scale, dtype, fmt):
+def attend(q, keys, values, scale, dtype):
     """One sequence: q [Hq][D], keys and values [tokens][heads][D] (the cache's
     values, float64).  Returns (o, lse, tolerance of o, tolerance of lse).
 
     Tolerance: a score's fp32 error is at most (D + 8) 2^-24 of sum |q k| scale
-    (twice as many terms where q has two parts) plus 2^-22 of its size for the
+    plus 2^-22 of its size for the
     base-2 factor and the exponential; it moves a weight by that much,
-    relative.  Each weight is rounded once to the operand type (half a step;
-    2^-16 for two bfloat16 parts); weights below fp16's normal range lose at
-    most 2^-25 of the largest one, each.  fp32 sums over the tokens add
-    (tokens + 32) 2^-24.  Then one rounding of o."""
+    relative.  Each weight is rounded once to dtype (half a step); weights below
+    fp16's normal range lose at most 2^-25 of the largest one, each.  fp32 sums
+    over the tokens add (tokens + 32) 2^-24.  Then one rounding of o."""
     Hq, D = q.shape
     n, heads, _ = keys.shape
     G = Hq // heads
@@ -103,8 +106,7 @@ def attend(q, keys, values, scale, dtype, fmt):
     tol, ltol = np.full((Hq, D), TINY[dtype]), np.zeros(Hq)
     if n == 0:
         return o, lse, tol, ltol
-    split = fmt != "16" and dtype == torch.float16
-    unit = 2.0 ** -16 if split else UNIT[dtype]
+    unit = UNIT[dtype]
     for h in range(Hq):
         k, v = keys[:, h // G], values[:, h // G]
         s = k @ q[h] * scale
@@ -114,9 +116,9 @@ def attend(q, keys, values, scale, dtype, fmt):
         o[h] = w @ v
         lse[h] = s.max() + np.log(l)
         size = np.abs(k) @ np.abs(q[h]) * abs(scale)
-        err = 2 * (((2 if split else 1) * D + 8) * 2.0 ** -24 * size.max() + 2.0 ** -22 * np.abs(s).max() + 2.0 ** -22)
+        err = 2 * ((D + 8) * 2.0 ** -24 * size.max() + 2.0 ** -22 * np.abs(s).max() + 2.0 ** -22)
         rel = 2 * err + unit + (n + 32) * 2.0 ** -24
-        floor = 2.0 ** -25 if dtype == torch.float16 and not split else 0.0
+        floor = 2.0 ** -25 if dtype == torch.float16 else 0.0
         t = rel * (w @ np.abs(v)) + floor * np.abs(v).sum(0) / l
         tol[h] = t + UNIT[dtype] * (np.abs(o[h]) + t) + TINY[dtype]
         ltol[h] = err + (n + 32) * 2.0 ** -24 + 2.0 ** -22 * (1 + abs(lse[h]))

@@ -125,7 +125,7 @@ def test_read_refusals(kw, want):
 @pytest.mark.parametrize("kw,want", [
     (dict(B=0), 2), (dict(B=65536), 2), (dict(Hq=0), 2), (dict(Hq=5), 2), (dict(P=-1), 2), (dict(ml=-1), 2),
     (dict(P=2 ** 30 + 1), 2), (dict(ml=2 ** 30 + 1), 2), (dict(qs=504), 2), (dict(qs=516), 2), (dict(scale=math.nan), 2),
-    (dict(scale=math.inf), 2), (dict(stride=3), 2), (dict(B=65535, Hq=1026, qs=1026 * 128), 2),
+    (dict(scale=math.inf), 2), (dict(scale=-1.1e30), 2), (dict(stride=3), 2), (dict(B=65535, Hq=1026, qs=1026 * 128), 2),
     (dict(q=None), 1), (dict(o=None), 1), (dict(lens=None), 1), (dict(table=None), 1), (dict(P=5), 1), (dict(q=ADDR[0] + 2), 1),
     (dict(o=ADDR[3] + 8), 1), (dict(lens=ADDR[2] + 2), 1), (dict(ws=ADDR[4] + 16), 1), (dict(o=ADDR[0]), 1),
     (dict(lse=ADDR[3] + 64), 1), (dict(o=ADDR[8]), 1), (dict(ws=ADDR[10]), 1), (dict(lse=ADDR[2]), 1), (dict(nb=-1), 1),

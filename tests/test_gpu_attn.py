@@ -56,8 +56,8 @@ def test_cache_round_trip(nm, fmt, dtype, D, heads, page, T):
     slots = torch.randperm(pages * page, generator=torch.Generator().manual_seed(5))[:T].cuda()
     nm.kv_write(cache, k, v, slots)
     gk, gv = nm.kv_read(cache, slots)
-    assert equal_values(gk, ref.quantised(ref.f64(k), fmt, dtype))
-    assert equal_values(gv, ref.quantised(ref.f64(v), fmt, dtype))
+    assert equal_values(gk, ref.quantised(ref.f64(k), fmt, dtype, read=True))
+    assert equal_values(gv, ref.quantised(ref.f64(v), fmt, dtype, read=True))
     # every other slot is as it was: zero
     rest = torch.tensor(sorted(set(range(pages * page)) - set(slots.tolist())), device="cuda")
     for t in nm.kv_read(cache, rest):
@@ -81,7 +81,7 @@ def test_cache_every_word(nm, fmt, dtype):
         if fmt == "16":
             assert same(gk, rows) and same(gv, rows.flip(0))
         else:
-            want = ref.quantised(ref.f64(rows), fmt, dtype)
+            want = ref.quantised(ref.f64(rows), fmt, dtype, read=True)
             assert equal_values(gk, want)
             assert equal_values(gv, want[::-1])
 
@@ -221,7 +221,7 @@ class Batch:
         self.k, self.v = rnd((n, heads, D), dtype, "ak", tag, D, scale=scale), rnd((n, heads, D), dtype, "av", tag, D)
         self.q = rnd((len(lens), hq, D), dtype, "aq", tag, D)
         nm.kv_write(self.cache, self.k, self.v, self.slots.cuda())
-        self.qk, self.qv = (ref.quantised(ref.f64(t), fmt) for t in (self.k, self.v))
+        self.qk, self.qv = (ref.quantised(ref.f64(t), fmt, dtype) for t in (self.k, self.v))
 
     def run(self, **kw):
         return self.nm.attn_decode(self.q, self.cache, self.table, self.t_lens, prefix_pages=self.prefix_pages,
@@ -237,7 +237,7 @@ class Batch:
             if n < 0:
                 continue
             t = [i for i in self.tokens(b) if drop is None or i not in drop]
-            want, wl, tol, ltol = ref.attend(ref.f64(self.q[b]), self.qk[t], self.qv[t], scale, self.dtype, self.fmt)
+            want, wl, tol, ltol = ref.attend(ref.f64(self.q[b]), self.qk[t], self.qv[t], scale, self.dtype)
             err = np.abs(ref.f64(o[b]) - want)
             assert (err <= tol).all(), (b, n, float((err / tol).max()))
             if lse is not None:
@@ -329,19 +329,42 @@ def test_attention_shared_prefix_peaked(nm, fmt):
     ramp = torch.linspace(0.2, 6, b.k.shape[0]).view(-1, 1, 1).cuda()
     b.k = (b.k.float() * ramp).to(BF16)
     nm.kv_write(b.cache, b.k, b.v, b.slots.cuda())
-    b.qk = ref.quantised(ref.f64(b.k), fmt)
+    b.qk = ref.quantised(ref.f64(b.k), fmt, BF16)
     lse = torch.empty((20, 16), device="cuda")
     b.check(b.run(lse=lse), lse)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_attention_seen_nan_stays_in_its_rows(nm, fmt):
-    b = Batch(nm, BF16, fmt, 128, 4, 2, 16, 0, [40, 40])
+@pytest.mark.parametrize("dtype", (F16, BF16))
+def test_attention_seen_nan_stays_in_its_rows(nm, dtype, fmt):
+    b = Batch(nm, dtype, fmt, 128, 4, 2, 16, 0, [40, 40])
     k, v = b.k[3:4].clone(), b.v[3:4].clone()
     v[0, 1, 5] = float("nan")                         # token 3 of sequence 0, key head 1
     b.nm.kv_write(b.cache, k, v, b.slots[3:4].cuda())
     o = b.run()
     assert torch.isnan(o[0, 2:, 5]).all() and torch.isfinite(o[0, :2]).all() and torch.isfinite(o[1]).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype,size", ((F16, 65504.0), (F16, 2.0 ** -13), (F16, 2.0 ** -20), (BF16, 2.0 ** 60),
+                                        (BF16, 2.0 ** -60)))
+@pytest.mark.parametrize("P,B", ((0, 2), (90, 12)))
+def test_attention_large_and_small_values(nm, dtype, fmt, size, P, B):
+    """Values at the ends of the type's range (fp16: up to its largest, whose codes stand for 65536), and keys as
+    small; the operands of quantised caches hold all of them exactly."""
+    b = Batch(nm, dtype, fmt, 128, 4, 1, 16, P, [20 + 3 * i for i in range(B)])
+    b.v = (b.v.float().clamp(-1, 1) * size).to(dtype)
+    if size < 1:
+        b.k = (b.k.float() * size).to(dtype)
+        b.q = (b.q.float() * (min(1 / size, 2.0 ** 12))).to(dtype)
+    nm.kv_write(b.cache, b.k, b.v, b.slots.cuda())
+    b.qk, b.qv = (ref.quantised(ref.f64(t), fmt, dtype) for t in (b.k, b.v))
+    o = b.run()
+    if size == 65504.0 and fmt != "16":                # a mean of 65536s is past fp16
+        big = torch.isinf(o).cpu().numpy()
+        o = o.clamp(-65504, 65504)
+        assert big.mean() < 0.05
+    b.check(o)
 
 
 def test_attention_bad_pages(nm):
@@ -406,12 +429,12 @@ def test_attention_offsets_past_32_bits(nm, fmt):
     k, v = rnd((n, heads, D), BF16, "bigk"), rnd((n, heads, D), BF16, "bigv")
     nm.kv_write(cache, k, v, slots)
     gk, gv = nm.kv_read(cache, slots)
-    wk, wv = ref.quantised(ref.f64(k), fmt), ref.quantised(ref.f64(v), fmt)
+    wk, wv = ref.quantised(ref.f64(k), fmt, BF16), ref.quantised(ref.f64(v), fmt, BF16)
     assert equal_values(gk, wk) and equal_values(gv, wv)
     q = rnd((1, heads, D), BF16, "bigq")
     lens = torch.tensor([n], dtype=torch.int32, device="cuda")
     o = nm.attn_decode(q, cache, pages[None].cuda(), lens)
-    want, _, tol, _ = ref.attend(ref.f64(q[0]), wk, wv, 1 / 16, BF16, fmt)
+    want, _, tol, _ = ref.attend(ref.f64(q[0]), wk, wv, 1 / 16, BF16)
     assert (np.abs(ref.f64(o[0]) - want) <= tol).all()
 
 
@@ -552,7 +575,7 @@ def test_decode_layer(nm, dtype, fmt, norm):
     def write(k, v, slots):
         nm.kv_write(cache, k, v, slots)
         for s, a, b in zip(slots.tolist(), ref.f64(k), ref.f64(v)):
-            held[s] = (ref.quantised(a, fmt), ref.quantised(b, fmt))
+            held[s] = (ref.quantised(a, fmt, dtype), ref.quantised(b, fmt, dtype))
 
     i = torch.arange(P)
     prefix_slots = (order[i // page] * page + i % page)
@@ -579,7 +602,7 @@ def test_decode_layer(nm, dtype, fmt, norm):
                 own = [int(table[b, t // page]) * page + t % page for t in range(step + 1)]
                 seen = [held[s] for s in prefix_slots.tolist() + own]
                 want, _, tol, _ = ref.attend(ref.f64(qr[b]), np.stack([s[0] for s in seen]),
-                                             np.stack([s[1] for s in seen]), 1 / np.sqrt(D), dtype, fmt)
+                                             np.stack([s[1] for s in seen]), 1 / np.sqrt(D), dtype)
                 assert (np.abs(ref.f64(o[b]) - want) <= tol).all(), (step, b)
         y = nm.spmv(*o_pack, o.view(B, hq * D))
         assert y.shape == (B, hidden) and torch.isfinite(y).all()
