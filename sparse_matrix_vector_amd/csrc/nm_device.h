@@ -49,4 +49,17 @@ __device__ __forceinline__ float scale_value(uint32_t byte)
     return bits_f32(byte == 255u ? 0x7FC00000u : byte << 23);
 }
 
+// A grid of `blocks` blocks.  A grid dimension holds less than 2^32 threads, so many
+// blocks are laid out in rows of kGridRow; flat_block() is the block's number, which
+// may be `blocks` or more in the last row.
+constexpr int64_t kGridRow = int64_t(1) << 22;
+
+inline dim3 flat_grid(int64_t blocks)
+{
+    return blocks <= kGridRow ? dim3((unsigned)blocks)
+                              : dim3((unsigned)kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
+}
+
+__device__ __forceinline__ uint32_t flat_block() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 }  // namespace nmd

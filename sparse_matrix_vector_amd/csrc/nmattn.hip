@@ -16,8 +16,15 @@
 // stands when a step takes two 16-token tiles: its k index (kg, i) is token
 // 4 kg + i of the first tile for i < 4, of the second for i >= 4.  The values are
 // stored in that order, the keys in the order of the first product's left
-// operand (nm_attn.h), so nothing passes through LDS and every load is one
-// contiguous kilobyte for a wave.
+// operand (nm_attn.h), so nothing passes through LDS and a wave's loads are
+// contiguous pieces of 512 or 1024 bytes.
+//
+// Own tokens are bound by HBM: 32 sequences of 4096 tokens, 8 key heads of 128
+// columns, MX8, take 45.5 us, 6.1 TB/s; with few or very different sequences the
+// start of the blocks and the joining of ranges show (16 of 0 .. 8192: 29 + 4 us, 5.1
+// TB/s; one of 131071, MX4: 27 + 5, 5.3).  A shared prefix is bound by the matrix
+// cores' and vector units' power at 256 rows (131072 tokens: 185 us, 740 TFLOP/s on
+// random values, 37% less time on zeros) and by HBM below.
 
 #include <hip/hip_runtime.h>
 
@@ -847,7 +854,7 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, int unit, uint8
 // spend the compiler keeps sums in accumulation registers and moves them to and fro
 // (and was seen to reuse a register of an operand too early doing so).
 template <int DT, int BITS, int D, int MT, int W>
-__global__ __launch_bounds__((W ? W : nma::kWaves) * 64, 2) void units_kernel(const AttnArgs A, int prefix_blocks, int direct)
+__global__ __launch_bounds__((W ? W : nma::kWaves) * 64, 2) void units_kernel(const AttnArgs A, int prefix_blocks, int blocks, int direct)
 {
     constexpr int NW = W ? W : nma::kWaves;
     constexpr int kJoin = join_bytes(D, W ? 1 : MT, NW), kLds = W && staged_bytes<BITS, D, W ? W : 4>() > kJoin
@@ -855,8 +862,11 @@ __global__ __launch_bounds__((W ? W : nma::kWaves) * 64, 2) void units_kernel(co
     __shared__ __align__(16) uint8_t lds[kLds];
     float* const join = reinterpret_cast<float*>(lds);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    if ((int)blockIdx.x < prefix_blocks) {
-        const int unit = blockIdx.x;
+    const int block = (int)flat_block();
+    if (block >= blocks)
+        return;
+    if (block < prefix_blocks) {
+        const int unit = block;
         if constexpr (W > 0) {
             attend_staged<DT, BITS, D, MT, W>(A, unit, lds);
         } else {
@@ -869,7 +879,7 @@ __global__ __launch_bounds__((W ? W : nma::kWaves) * 64, 2) void units_kernel(co
         }
         return;
     }
-    const unsigned unit = blockIdx.x - prefix_blocks;
+    const unsigned unit = block - prefix_blocks;
     const int h = unit % A.heads, b = unit / A.heads % A.B;
     const int group = unit / A.heads / A.B % A.own_groups, split = unit / A.heads / A.B / A.own_groups;
     const int start = split * A.own_chunk, at = start / nma::kTile + 2 * wave;
@@ -899,7 +909,10 @@ __global__ __launch_bounds__(NW * 64) void combine_kernel(const AttnArgs A)
     const int lane = threadIdx.x % 64, m = lane % 16, kg = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int tiles = (A.prefix_rows + 15) / 16;
-    const int h = blockIdx.x % A.heads, tile = blockIdx.x / A.heads % tiles, chunk = blockIdx.x / A.heads / tiles;
+    const uint32_t block = flat_block();
+    const int h = block % A.heads, tile = block / A.heads % tiles, chunk = block / A.heads / tiles;
+    if (chunk >= D / 16)
+        return;
     const int r = tile * 16 + m, rr = min(r, A.prefix_rows - 1), b = rr / A.G, g = rr % A.G;
     const int len = min(A.lens[b], A.max_len);
     const int np = A.prefix_splits, mine = np + (max(len, 0) + A.own_chunk - 1) / A.own_chunk;
@@ -962,8 +975,8 @@ __global__ __launch_bounds__(NW * 64) void combine_kernel(const AttnArgs A)
 template <int DT, int BITS, int D, int MT, int W>
 void launch_units(const AttnArgs& A, int64_t prefix_blocks, int64_t blocks, bool direct, hipStream_t s)
 {
-    hipLaunchKernelGGL((units_kernel<DT, BITS, D, MT, W>), dim3((unsigned)blocks), dim3((W ? W : nma::kWaves) * 64), 0, s,
-                       A, (int)prefix_blocks, direct ? 1 : 0);
+    hipLaunchKernelGGL((units_kernel<DT, BITS, D, MT, W>), flat_grid(blocks), dim3((W ? W : nma::kWaves) * 64), 0, s, A,
+                       (int)prefix_blocks, (int)blocks, direct ? 1 : 0);
 }
 
 template <int DT, int BITS, int D>
@@ -991,9 +1004,9 @@ int launch(const nma::AttnPlan& P, const AttnArgs& A, hipStream_t s)
             return NM_ERR_BAD_SHAPE;
         // Few tiles of rows have many parts each: more waves share them then.
         if (blocks < 2 * nma::kCus && P.prefix_splits + P.own_splits > 16)
-            hipLaunchKernelGGL((combine_kernel<DT, D, 16>), dim3((unsigned)blocks), dim3(1024), 0, s, A);
+            hipLaunchKernelGGL((combine_kernel<DT, D, 16>), flat_grid(blocks), dim3(1024), 0, s, A);
         else
-            hipLaunchKernelGGL((combine_kernel<DT, D, 4>), dim3((unsigned)blocks), dim3(256), 0, s, A);
+            hipLaunchKernelGGL((combine_kernel<DT, D, 4>), flat_grid(blocks), dim3(256), 0, s, A);
     }
     return hip_status(hipGetLastError());
 }

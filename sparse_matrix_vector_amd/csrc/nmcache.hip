@@ -30,6 +30,7 @@ struct QkArgs {
     const uint16_t* w[2];       // norm weights or NULL
     int64_t stride[2];          // of x, elements
     int heads[2];
+    int64_t T;
     int D, rot, blocks_per_row;
     float eps;
     const int32_t* positions;
@@ -48,8 +49,11 @@ template <int DT, int LPH, bool INTERLEAVED>
 __global__ __launch_bounds__(kQkThreads) void qk_kernel(const QkArgs A)
 {
     __shared__ float cs[2][256];
-    const int64_t t = blockIdx.x / A.blocks_per_row;
-    const int part = blockIdx.x % A.blocks_per_row;
+    const uint32_t block = flat_block();
+    const int64_t t = block / A.blocks_per_row;
+    const int part = block % A.blocks_per_row;
+    if (t >= A.T)
+        return;
     const int half = A.rot / 2;
     constexpr int kPerPass = kQkThreads / LPH;
     const int lane = threadIdx.x % LPH, d0 = lane * 8;
@@ -147,9 +151,9 @@ int launch_qk(const QkArgs& A, bool interleaved, int64_t blocks, hipStream_t s)
 {
     (void)hipGetLastError();
     if (interleaved)
-        hipLaunchKernelGGL((qk_kernel<DT, LPH, true>), dim3((unsigned)blocks), dim3(kQkThreads), 0, s, A);
+        hipLaunchKernelGGL((qk_kernel<DT, LPH, true>), flat_grid(blocks), dim3(kQkThreads), 0, s, A);
     else
-        hipLaunchKernelGGL((qk_kernel<DT, LPH, false>), dim3((unsigned)blocks), dim3(kQkThreads), 0, s, A);
+        hipLaunchKernelGGL((qk_kernel<DT, LPH, false>), flat_grid(blocks), dim3(kQkThreads), 0, s, A);
     return hip_status(hipGetLastError());
 }
 
@@ -228,7 +232,7 @@ struct Lane {
 __device__ __forceinline__ Lane lane_of(int64_t T, int width)
 {
     const uint32_t lane = threadIdx.x % 64, per = (uint32_t)(width + kCols - 1) / kCols;
-    const uint32_t item = blockIdx.x * (kCacheThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const uint32_t item = flat_block() * (kCacheThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t group = item / per;          // uniform; cache_grid keeps items in 31 bits
     Lane l;
     l.t = (int64_t)group * kRows + lane / (kCols / 8);
@@ -462,7 +466,7 @@ int cache_grid(const nm_kv_cache& c, int64_t T, dim3* grid)
     const int64_t items = nma::ceil_div(T, kRows) * nma::ceil_div((int64_t)c.heads * c.D, kCols);
     if (items > INT32_MAX)
         return NM_ERR_BAD_SHAPE;
-    *grid = dim3((unsigned)nma::ceil_div(items, kCacheThreads / 64));
+    *grid = flat_grid(nma::ceil_div(items, kCacheThreads / 64));
     return NM_OK;
 }
 
@@ -483,6 +487,7 @@ int nmk::qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_
     A.stride[1] = T > 1 ? k_stride : 0;
     A.heads[0] = Hq;
     A.heads[1] = Hk;
+    A.T = T;
     A.D = D;
     A.rot = rot;
     A.eps = eps;

@@ -190,6 +190,22 @@ def test_qk_no_rows_no_heads(nm):
     assert gq.shape == (0, 2, 64)
 
 
+def test_qk_more_rows_than_a_grid_dimension_holds(nm):
+    """2^22 + 5 rows, a block each: the grid has a second row.  All rows alike but the first and the last ones."""
+    T, D = (1 << 22) + 5, 16
+    q = rnd((1, 1, D), F16, "many").expand(T, 1, D).contiguous()
+    ends = torch.tensor([0, 1, (1 << 22) - 1, 1 << 22, T - 1], device="cuda")
+    q[ends] = rnd((5, 1, D), F16, "ends")
+    pos, f, w = torch.full((T,), 7, dtype=torch.int32, device="cuda"), frequencies(16), rnd((D,), F16, "w")
+    pos[ends] = torch.tensor([3, 4, 5, 6, 8], dtype=torch.int32, device="cuda")
+    gq, _ = nm.qk_norm_rope(q, q[:, :0], pos, f, w)
+    eps = float(np.float32(1e-6))
+    ref.qk_close(gq[ends], q[ends], w, eps, pos[ends], f, False)
+    ref.qk_close(gq[2:3], q[2:3], w, eps, pos[2:3], f, False)
+    gq[ends] = gq[2].clone()
+    assert (gq == gq[2]).all()
+
+
 # ---- attention ------------------------------------------------------------------
 
 class Batch:
@@ -436,6 +452,26 @@ def test_attention_offsets_past_32_bits(nm, fmt):
     o = nm.attn_decode(q, cache, pages[None].cuda(), lens)
     want, _, tol, _ = ref.attend(ref.f64(q[0]), wk, wv, 1 / 16, BF16)
     assert (np.abs(ref.f64(o[0]) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("P", (0, 17))
+def test_attention_more_units_than_a_grid_dimension_holds(nm, P):
+    """65535 sequences on 66 heads, 2^22 + 2^17 units, every sequence on the same page."""
+    B, heads, D = 65535, 66, 64
+    cache = nm.KVCache(4, 16, heads, D, F16, "mx8")
+    k, v = rnd((40, heads, D), F16, "uk"), rnd((40, heads, D), F16, "uv")
+    nm.kv_write(cache, k, v, torch.arange(40, device="cuda"))
+    q = rnd((64, heads, D), F16, "uq")[torch.arange(B, device="cuda") % 64]
+    lens = (torch.arange(B, device="cuda") % 5).int()
+    table = torch.full((B, 1), 2, dtype=torch.int32, device="cuda")
+    pages = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    o = nm.attn_decode(q, cache, table, lens, prefix_pages=pages, prefix_len=P)
+    kk, vv = (ref.quantised(ref.f64(t), "mx8", F16) for t in (k, v))
+    for b in (0, 1, 63549, 63550, 63551, 65534):          # around unit 2^22 and both ends
+        t = list(range(P)) + list(range(32, 32 + int(lens[b])))
+        want, _, tol, _ = ref.attend(ref.f64(q[b]), kk[t], vv[t], 0.125, F16)
+        assert (np.abs(ref.f64(o[b]) - want) <= tol).all(), b
+    assert same(o[:320], o[64960:65280])                  # the same queries and lengths come back every 320
 
 
 # ---- streams, graphs, workspaces -----------------------------------------------------
