@@ -37,8 +37,8 @@ def _refuse(t, name, device, dtype, shape):
 def _check(t, name, device, dtype, shape):
     """Address of t, which is a contiguous tensor on the GPU `device` with
     `dtype` and `shape`."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and t.dtype == dtype and
-            t.shape == shape and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype is dtype and t.shape == shape and
+            t.is_contiguous()):
         _refuse(t, name, device, dtype, shape)
     return t.data_ptr()
 
@@ -55,7 +55,7 @@ def _size(t, name, dims):
 
 def _rows(t, name, device, dtype, shape):
     """Address and row stride of strided rows [rows][heads][D] of that shape."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and t.dtype == dtype and t.shape == shape):
+    if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype is dtype and t.shape == shape):
         _refuse(t, name, device, dtype, shape)
     rows, heads, D = shape
     if t.is_contiguous():
@@ -66,58 +66,46 @@ def _rows(t, name, device, dtype, shape):
     return t.data_ptr(), s0 if rows > 1 else heads * D
 
 
-class _On:
-    """Makes `device` and the stream to launch on current (torch's allocator
-    then hands out memory of that stream); gives the stream's handle."""
-
-    __slots__ = ("guards", "handle")
-
-    def __init__(self, device, stream):
-        self.guards = []
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, not on {device}")
-            self.guards.append(torch.cuda.stream(stream))       # sets the device as well
-        else:
-            self.guards.append(torch.cuda.device(device))
-        for g in self.guards:
-            g.__enter__()
-        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-
-    def __enter__(self):
-        return self.handle
-
-    def __exit__(self, *exc):
-        for g in self.guards:
-            g.__exit__(*exc)
-
-
-class _Here:
-    """_On for the current stream of the current device, which needs no guards."""
-
-    def __enter__(self):
-        return _current_stream(torch.cuda.current_device())
-
-    def __exit__(self, *exc):
-        pass
-
-
-_HERE = _Here()
-
-# torch's own shortcut to the current stream's handle where it has one (a stream
-# object costs about 2 us, which a decode step's calls would notice).
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+# A decode step's calls take Python longer than the GPU, so the common case, the
+# current stream of the current device, goes through torch's own shortcuts where it
+# has them (a stream object alone costs 2 us).
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _on(device, stream):
-    if stream is None and device.index == torch.cuda.current_device():
-        return _HERE
-    return _On(device, stream)
+class _Other:
+    """Another stream or device than the current ones, made current until
+    close() (torch's allocator then hands out memory of that stream)."""
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, not on {device}")
+        self.guard = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+        self.guard.__enter__()
+
+    def close(self):
+        self.guard.__exit__(None, None, None)
+
+
+def _other(device, stream):
+    """None where work goes to the current stream of the current device."""
+    if not device.type == "cuda":
+        raise TypeError(f"tensors must be CUDA (HIP) tensors, not on {device}")
+    return None if stream is None and device.index == _device() else _Other(device, stream)
+
+
+_lib = None
+
+
+def _load():
+    global _lib
+    _lib = attn_lib()
+    return _lib
 
 
 def _call(name, *args):
-    st = getattr(attn_lib(), name)(*args)
+    st = getattr(_lib or _load(), name)(*args)
     if st != NM_OK:
         raise NmError(name, st)
 
@@ -134,26 +122,31 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, interlea
     len(inv_freq), further columns are not turned.  positions int32 [T],
     inv_freq float32.  Returns (q, k), contiguous; ``out`` is such a pair, and
     may be (q, k) themselves."""
-    T, hq, D = _size(q, "q", 3)
+    shape = _size(q, "q", 3)
+    T, hq, D = shape
     hk = _size(k, "k", 3)[1]
     pairs, = _size(inv_freq, "inv_freq", 1)
     dev, dt = q.device, q.dtype
     code = _dtype(dt)
-    qp, qs = _rows(q, "q", dev, dt, (T, hq, D))
+    qp, qs = _rows(q, "q", dev, dt, shape)
     kp, ks = _rows(k, "k", dev, dt, (T, hk, D))
     pos = _check(positions, "positions", dev, torch.int32, (T,))
     freq = _check(inv_freq, "inv_freq", dev, torch.float32, (pairs,))
     wqp = None if wq is None else _check(wq, "wq", dev, dt, (D,))
     wkp = None if wk is None else _check(wk, "wk", dev, dt, (D,))
-    with _on(dev, stream) as handle:
+    other = _other(dev, stream)
+    try:
         if out is None:
-            out = _empty(q, (T, hq, D)), _empty(k, (T, hk, D))
-            oq, ok = out[0].data_ptr(), out[1].data_ptr()
+            out = oq, ok = _empty(q, shape), _empty(k, (T, hk, D))
+            oqp, okp = oq.data_ptr(), ok.data_ptr()
         else:
-            oq = _check(out[0], "out[0]", dev, dt, (T, hq, D))
-            ok = _check(out[1], "out[1]", dev, dt, (T, hk, D))
+            oqp = _check(out[0], "out[0]", dev, dt, shape)
+            okp = _check(out[1], "out[1]", dev, dt, (T, hk, D))
         _call("nm_qk_norm_rope", qp, qs, kp, ks, T, hq, hk, D, code, wqp, wkp, eps, pos, freq, 2 * pairs,
-              1 if interleaved else 0, oq, ok, handle)
+              1 if interleaved else 0, oqp, okp, _stream(dev.index))
+    finally:
+        if other is not None:
+            other.close()
     return out[0], out[1]
 
 
@@ -163,7 +156,7 @@ class KVCache:
     "mx8" and "mx4" keep 8- and 4-bit floats (e4m3, e2m1) with one power-of-two
     scale per 32 columns.  A slot is page * page_size + place in the page."""
 
-    __slots__ = ("_buffers", "_struct", "_ref", "device", "dtype", "format", "n_pages", "page_size", "heads", "D")
+    __slots__ = ("_buffers", "_struct", "_ref", "_format", "device", "dtype", "format", "n_pages", "page_size", "heads", "D")
 
     def __init__(self, n_pages, page_size, heads, D, dtype, format="16", device="cuda"):
         if format not in _FORMATS:
@@ -177,7 +170,7 @@ class KVCache:
         k_scale, v_scale = (torch.zeros(sbytes, dtype=torch.uint8, device=device) if sbytes else None
                             for _ in range(2))
         self._buffers = (k, v, k_scale, v_scale)
-        self.device, self.dtype, self.format = k.device, dtype, format
+        self.device, self.dtype, self.format, self._format = k.device, dtype, format, fmt
         self.n_pages, self.page_size, self.heads, self.D = n_pages, page_size, heads, D
         self._struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if sbytes else None,
                                      v_scale.data_ptr() if sbytes else None, n_pages, page_size, heads, D, code, fmt)
@@ -221,8 +214,12 @@ def kv_write(cache, k, v, slots, stream=None):
     shape = (T, c.heads, c.D)
     kp, ks = _rows(k, "k", c.device, c.dtype, shape)
     vp, vs = _rows(v, "v", c.device, c.dtype, shape)
-    with _on(c.device, stream) as handle:
-        _call("nm_kv_write", c._ref, kp, ks, vp, vs, T, sp, handle)
+    other = _other(c.device, stream)
+    try:
+        _call("nm_kv_write", c._ref, kp, ks, vp, vs, T, sp, _stream(c.device.index))
+    finally:
+        if other is not None:
+            other.close()
 
 
 def kv_read(cache, slots, out=None, stream=None):
@@ -232,7 +229,8 @@ def kv_read(cache, slots, out=None, stream=None):
     T, = _size(slots, "slots", 1)
     sp = _check(slots, "slots", c.device, torch.int64, (T,))
     shape = (T, c.heads, c.D)
-    with _on(c.device, stream) as handle:
+    other = _other(c.device, stream)
+    try:
         if out is None:
             k = slots.new_empty(shape, dtype=c.dtype)
             out = k, torch.empty_like(k)
@@ -240,7 +238,10 @@ def kv_read(cache, slots, out=None, stream=None):
         else:
             kp = _check(out[0], "out[0]", c.device, c.dtype, shape)
             vp = _check(out[1], "out[1]", c.device, c.dtype, shape)
-        _call("nm_kv_read", c._ref, sp, T, kp, vp, handle)
+        _call("nm_kv_read", c._ref, sp, T, kp, vp, _stream(c.device.index))
+    finally:
+        if other is not None:
+            other.close()
     return out[0], out[1]
 
 
@@ -248,7 +249,7 @@ def attn_workspace(B, heads_q, cache, max_len, prefix_len=0):
     """A workspace for attn_decode calls of this shape on the cache's device
     (any contents; calls that may run at the same time need one each)."""
     c = _cache(cache)
-    nbytes = attn_lib().nm_attn_workspace_bytes(B, heads_q, c.heads, c.D, _FORMATS[c.format], prefix_len, max_len)
+    nbytes = attn_lib().nm_attn_workspace_bytes(B, heads_q, c.heads, c.D, c._format, prefix_len, max_len)
     if nbytes < 0:
         raise ValueError(f"no such attention: {B} sequences, {heads_q} query heads on {c.heads}, {prefix_len} + "
                          f"{max_len} tokens")
@@ -277,7 +278,7 @@ def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, pre
         if page_table.is_contiguous():
             table, stride = _check(page_table, "page_table", dev, torch.int32, (B, width)), width
         else:
-            if (width > 1 and page_table.stride(1) != 1) or not page_table.is_cuda or page_table.device != dev or \
+            if (width > 1 and page_table.stride(1) != 1) or page_table.device != dev or \
                     page_table.dtype != torch.int32 or page_table.shape[0] != B:
                 _refuse(page_table, "page_table (rows)", dev, torch.int32, (B, width))
             table, stride = page_table.data_ptr(), page_table.stride(0)
@@ -296,17 +297,21 @@ def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, pre
     if ws is not None:
         nbytes, = _size(ws, "ws", 1)
         wsp = _check(ws, "ws", dev, torch.uint8, (nbytes,))
-    with _on(dev, stream) as handle:
+    other = _other(dev, stream)
+    try:
         if out is None:
             out = _empty(q, shape)
             op = out.data_ptr()
         else:
             op = _check(out, "out", dev, dt, shape)
         if ws is None:
-            nbytes = attn_lib().nm_attn_workspace_bytes(B, hq, c.heads, c.D, _FORMATS[c.format], prefix_len, max_len)
+            nbytes = (_lib or _load()).nm_attn_workspace_bytes(B, hq, c.heads, c.D, c._format, prefix_len, max_len)
             if nbytes > 0:
                 ws = q.new_empty(nbytes, dtype=torch.uint8)
                 wsp = ws.data_ptr()
         _call("nm_attn_decode", qp, qs, B, hq, c._ref, pp, prefix_len, table, stride, lp, max_len,
-              c.D ** -0.5 if scale is None else scale, op, lsep, wsp, max(nbytes, 0), handle)
+              c.D ** -0.5 if scale is None else scale, op, lsep, wsp, max(nbytes, 0), _stream(dev.index))
+    finally:
+        if other is not None:
+            other.close()
     return out
