@@ -141,9 +141,11 @@ int nm_kv_read(const nm_kv_cache* cache, const int64_t* slots, int64_t T, void* 
  * Scores, softmax statistics and sums are fp32; the weights of the sum are
  * rounded to dtype, the operand type of the matrix cores, and o once to dtype.
  * Results do not depend on other calls and repeat bit for bit.
- * Infinities or NaN in a token that is seen give infinities or NaN in the rows
- * that see it; in a token that is not seen they have no effect.  (In a quantised
- * bfloat16 cache magnitudes of 2^127 and more count as infinities here.)
+ * Infinities and NaN in a token that is seen have the effect that the formula
+ * gives them, fp32 sums that overflow included (a score of -inf weighs nothing; a
+ * row with no other scores gets zeros); in a token that is not seen they have
+ * none.  (In a quantised bfloat16 cache magnitudes of 2^127 and more count as
+ * infinities here.)
  * B and Hq 1..65535, B * Hq below 2^26, prefix_len and max_len 0..2^30, |scale| <= 1e30.  o, lse
  * and workspace must not overlap anything else.
  */

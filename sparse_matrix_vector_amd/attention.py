@@ -162,7 +162,8 @@ class KVCache:
         if format not in _FORMATS:
             raise ValueError(f"format must be one of {', '.join(_FORMATS)}, not {format}")
         code, fmt = _dtype(dtype), _FORMATS[format]
-        nbytes = attn_lib().nm_kv_bytes(n_pages, page_size, heads, D, fmt)
+        # (ctypes would cut a larger integer to its low bits)
+        nbytes = -1 if max(n_pages, page_size, heads, D) >= 2 ** 31 else attn_lib().nm_kv_bytes(n_pages, page_size, heads, D, fmt)
         if nbytes < 0:
             raise ValueError(f"no cache of {n_pages} pages of {page_size} tokens, {heads} heads, {D} columns")
         sbytes = attn_lib().nm_kv_scale_bytes(n_pages, page_size, heads, D, fmt)
@@ -284,14 +285,14 @@ def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, pre
             table, stride = page_table.data_ptr(), page_table.stride(0)
         width *= c.page_size
     max_len = width if max_len is None else max_len
-    if max_len > width:
-        raise ValueError(f"max_len {max_len} is more than page_table holds ({width} tokens)")
+    if not 0 <= max_len <= width:
+        raise ValueError(f"max_len {max_len} is not within what page_table holds ({width} tokens)")
     pp = None
     if prefix_len:
         n, = _size(prefix_pages, "prefix_pages", 1)
         pp = _check(prefix_pages, "prefix_pages", dev, torch.int32, (n,))
-        if prefix_len > n * c.page_size:
-            raise ValueError(f"prefix_len {prefix_len} is more than prefix_pages holds ({n * c.page_size} tokens)")
+        if not 0 < prefix_len <= n * c.page_size:
+            raise ValueError(f"prefix_len {prefix_len} is not within what prefix_pages holds ({n * c.page_size} tokens)")
     lsep = None if lse is None else _check(lse, "lse", dev, torch.float32, (B, hq))
     wsp, nbytes = None, 0
     if ws is not None:

@@ -64,7 +64,7 @@ def test_qk_bad_shape(kw):
 @pytest.mark.parametrize("kw", [dict(q=None), dict(k=None), dict(pos=None), dict(f=None), dict(qo=None), dict(ko=None),
                                 dict(q=ADDR[0] + 2), dict(k=ADDR[1] + 8), dict(qo=ADDR[4] + 4), dict(wq=ADDR[6] + 2),
                                 dict(pos=ADDR[2] + 2), dict(qo=ADDR[0] + 16), dict(ko=ADDR[0]), dict(qo=ADDR[1]),
-                                dict(ko=ADDR[4] + 1024), dict(wq=ADDR[4]), dict(qo=ADDR[2] - 1024 * 3 + 16),
+                                dict(ko=ADDR[4] + 1024), dict(wq=ADDR[4]), dict(qo=ADDR[2] - 16),
                                 dict(qs=520, qo=ADDR[0]), dict(ko=ADDR[3] - 16)])
 def test_qk_invalid_pointer(kw):
     assert qk(**kw) == L.NM_ERR_INVALID_ARG
@@ -160,3 +160,15 @@ def test_python_refuses_host_tensors_and_formats():
               lambda: nm.attn_decode(x, c, None, torch.zeros(1, dtype=torch.int32))):
         with pytest.raises(TypeError, match="CUDA"):
             f()
+
+
+def test_python_refuses_sizes_that_ctypes_would_cut():
+    for sizes in ((4, 2 ** 32 + 16, 2, 64), (2 ** 64 + 4, 16, 2, 64), (4, 16, 2 ** 32 + 2, 64), (4, 16, 2, 2 ** 32 + 64)):
+        with pytest.raises(ValueError, match="no cache"):
+            nm.KVCache(*sizes, torch.float16, device="cpu")
+    c = nm.KVCache(4, 16, 2, 64, torch.float16, device="cpu")
+    q, lens, pages = torch.zeros((1, 2, 64), dtype=torch.float16), torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="max_len"):
+        nm.attn_decode(q, c, pages.view(1, 1), lens, max_len=2000 - 2 ** 64)
+    with pytest.raises(ValueError, match="prefix_len"):
+        nm.attn_decode(q, c, None, lens, prefix_pages=pages, prefix_len=2000 - 2 ** 64)

@@ -269,7 +269,7 @@ class Batch:
     (128, 4, 1, 16, 0, [1]), (128, 8, 8, 16, 0, [37]), (128, 32, 8, 64, 0, [0, 1, 15, 16, 17, 31, 32, 33, 127, 128, 129]),
     (64, 10, 2, 32, 0, [300, 5]), (256, 6, 2, 16, 0, [100, 0, 64]), (128, 5, 1, 128, 0, [1000]),
     (64, 32, 1, 16, 0, [70, 3]), (128, 20, 1, 32, 0, [40, 257]),
-    (128, 8, 2, 16, 40, [0, 3, 33]), (128, 8, 8, 64, 1, [0]), (64, 16, 2, 32, 161, [5] * 5), (128, 24, 8, 64, 300, [1, 0] * 6),
+    (128, 8, 2, 16, 40, [0, 3, 33]), (128, 8, 8, 64, 1, [0]), (64, 16, 2, 32, 161, [5] * 5), (128, 32, 8, 64, 300, [1, 0] * 6),
     (256, 8, 1, 16, 130, [7, 0, 50]), (128, 16, 2, 16, 515, [9] * 33), (64, 4, 4, 256, 257, [0, 0, -1, 2]),
     (256, 16, 2, 32, 100, [20] * 6)])
 def test_attention(nm, dtype, fmt, D, hq, heads, page, P, lens):
