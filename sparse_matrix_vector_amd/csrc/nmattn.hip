@@ -1,10 +1,10 @@
 // nmattn.hip -- nm_attn_decode: single-token attention over the paged cache.
 //
 // For the rows (query heads) q of a unit and its tokens t, with scores
-// s_t = scale * q . k_t, one pass keeps the running maximum m, the sum
-// l = sum exp(s_t - m) and the vector o = sum exp(s_t - m) v_t, multiplying l and
-// o by exp(m_old - m_new) where the maximum grows; units of one row are joined
-// by the same rule (combine_kernel).
+// s_t = scale * q . k_t, one pass keeps a reference m near the running maximum, the
+// sum l = sum exp(s_t - m) and the vector o = sum exp(s_t - m) v_t, multiplying l and
+// o by exp(m_old - m_new) where m is raised to the maximum; units of one row are
+// joined by the same rule (combine_kernel).
 //
 // Everything runs on the matrix cores with the cache as the left operand, 16
 // tokens or 16 columns by 16 rows (v_mfma_f32_16x16x32):
@@ -23,7 +23,7 @@
 // columns, MX8, take 45.5 us, 6.1 TB/s; with few or very different sequences the
 // start of the blocks and the joining of ranges show (16 of 0 .. 8192: 29 + 4 us, 5.1
 // TB/s; one of 131071, MX4: 27 + 5, 5.3).  A shared prefix is bound by the matrix
-// cores' and vector units' power at 256 rows (131072 tokens: 185 us, 740 TFLOP/s on
+// cores' and vector units' power at 256 rows (131072 tokens: 175 us, 790 TFLOP/s on
 // random values, 37% less time on zeros) and by HBM below.
 
 #include <hip/hip_runtime.h>
@@ -325,10 +325,16 @@ __device__ __forceinline__ void mask_scores(f32x4 (&sc)[MT][NT], const int (&n)[
 }
 
 // The softmax weights of a step of NT tiles, as right operands of the second
-// product (one for each pair of tiles); updates the rows' maxima, sums and,
-// where a maximum grows, what has been added up so far.
+// product (one for each pair of tiles); updates the rows' references (mx), sums and,
+// where a reference grows, what has been added up so far.
 template <int DT, int MT, int NT>
 struct Weights {
+    // A row's reference `mx` may lag behind its maximum by this much (base 2): weights
+    // are at most 2^8 then, which both types and the fp32 sums have room for, and in long
+    // ranges the sums are hardly ever multiplied.  32 sequences of 64 heads behind 32768
+    // tokens, 16-bit: 67.5 us without, 63.7 with it; MX8 and 4096 own tokens 82.6 / 78.6.
+    static constexpr float kSlack = 8.0f;
+
     u32x4 op[MT][NT / 2];
 
     template <int PER>
@@ -344,15 +350,15 @@ struct Weights {
                 for (int r = 0; r < 4; ++r)
                     top = fmaxf(top, sc[g][u][r]);
             top = fmaxf(mx[g], quarters_max(top) * scale);
-            const float base = top == NM_NEG_INF ? 0.0f : top;
-            if (__any(top > mx[g])) {
-                const float f = mx[g] == top ? 1.0f : __builtin_amdgcn_exp2f(mx[g] - base);
+            if (__any(top > mx[g] + kSlack)) {
+                const float f = mx[g] == top ? 1.0f : __builtin_amdgcn_exp2f(mx[g] - top);
                 sum[g] *= f;
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
                     acc[g][j] *= f;
                 mx[g] = top;
             }
+            const float base = mx[g] == NM_NEG_INF ? 0.0f : mx[g];
 #pragma unroll
             for (int t = 0; t < NT / 2; ++t) {
                 float p[8];

@@ -350,6 +350,23 @@ def test_attention_shared_prefix_peaked(nm, fmt):
     b.check(b.run(lse=lse), lse)
 
 
+@pytest.mark.parametrize("slope", (0.02, 0.1, 0.7, -0.1))
+@pytest.mark.parametrize("dtype,fmt", ((F16, "16"), (BF16, "16"), (F16, "mx8"), (BF16, "mx4")))
+@pytest.mark.parametrize("P,lens", ((0, [1000, 300, 40]), (900, [40, 90, 0] * 4)))
+def test_attention_climbing_scores(nm, dtype, fmt, P, lens, slope):
+    """Scores that rise (or fall) from token to token, less or more than e^5 a step of 32 or 64: references that lag
+    behind the maximum, and weights above one."""
+    b = Batch(nm, dtype, fmt, 128, 8, 2, 16, P, lens)
+    b.q = torch.zeros_like(b.q)
+    b.q[..., 0] = 1.0
+    b.q[..., 1] = 0.125
+    b.k[..., 0] = (slope * torch.arange(b.k.shape[0], device="cuda") % 200).view(-1, 1).to(dtype)
+    nm.kv_write(b.cache, b.k, b.v, b.slots.cuda())
+    b.qk = ref.quantised(ref.f64(b.k), fmt, dtype)
+    lse = torch.empty((len(lens), 8), device="cuda")
+    b.check(b.run(scale=1.0, lse=lse), lse, scale=1.0)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", (F16, BF16))
 def test_attention_seen_nan_stays_in_its_rows(nm, dtype, fmt):
