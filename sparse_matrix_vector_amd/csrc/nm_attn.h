@@ -148,7 +148,16 @@ inline AttnPlan attn_plan(int64_t B, int Hq, int heads, int D, int format, int64
     const double staged = 52.0 * (double)(prefix_len * heads * p.prefix_groups);
     const double own = 22.0 * 2 / 3 * format_bits(format) / 16 * (double)(B * heads * p.own_groups) * (double)max_len;
     const int64_t cus = max_len == 0 ? kCus : (int64_t)(kCus * (staged / (staged + own)));
-    cut(prefix_len, heads * p.prefix_groups, p.waves == 8 ? cus : 2 * kCus, kMaxTokens, &p.prefix_splits,
+    // Smaller prefix units: one block a CU, since every further range of a row costs its
+    // partial sums' way to memory and back; but two where ranges still hold 512 tokens
+    // and a block alone does not keep its CU busy (staged by four waves, or 4-bit).
+    // us with one / two, 8 key heads of 128 columns: 64 rows, MX8, 8192 tokens 17.8 /
+    // 19.7, 16384 24.4 / 24.2, 32768 37.5 / 31.8; 128 rows, 16-bit, 8192 21.1 / 26.6,
+    // 32768 42.6 / 45.1, 65536 70.9 / 67.2; 32 rows, MX8, 32768 20.7 / 23.9; 16 rows, MX4,
+    // 8192 10.9 / 11.6, 32768 16.9 / 15.1, MX8, 131072 50.1 / 51.8.
+    const int64_t prefix_units = heads * p.prefix_groups;
+    const bool two = (p.waves == 4 || format == NM_KV_MX4) && prefix_len * prefix_units >= 512 * 2 * kCus;
+    cut(prefix_len, prefix_units, p.waves == 8 ? cus : two ? 2 * kCus : kCus, kMaxTokens, &p.prefix_splits,
         &p.prefix_chunk);
     // Own tokens (us; 8 key heads, MX8, x blocks for each CU): 32 sequences of up to
     // 1024 tokens, one unit per CU: 1 block 12.3, 2 blocks 14.2, 3 blocks 14.8; 16 of up
