@@ -144,19 +144,29 @@ inline AttnPlan attn_plan(int64_t B, int Hq, int heads, int D, int format, int64
     // by its bytes), of which two thirds, since the batch is rarely full to max_len.
     // 32 sequences of 64 heads, 16-bit, 32741 tokens + up to 1024: 256 blocks 81.5 us, 192
     // 78.0, 160 79.2; 8192 + up to 1024: 47.9 / 45.0 / 39.8; MX8, 32768 + up to 4096: 96.0 /
-    // 94.7 / 83.1; 32768 alone: 68.4 / 71.7 / 77.4.
+    // 94.7 / 83.1; 32768 alone: 68.4 / 71.7 / 77.4.  Short own tokens have an eighth of the
+    // CUs left to them all the same, or they would wait for the prefix (16-bit, 16 own
+    // tokens, 256 / 224 blocks: 4096 + 28.0 / 22.4, 8192 + 32.9 / 28.6, 32768 + 58.3 / 59.0).
     const double staged = 52.0 * (double)(prefix_len * heads * p.prefix_groups);
     const double own = 22.0 * 2 / 3 * format_bits(format) / 16 * (double)(B * heads * p.own_groups) * (double)max_len;
-    const int64_t cus = max_len == 0 ? kCus : (int64_t)(kCus * (staged / (staged + own)));
+    int64_t cus = kCus;
+    if (max_len > 0) {
+        cus = (int64_t)(kCus * (staged / (staged + own)));
+        if (cus > kCus * 7 / 8)
+            cus = kCus * 7 / 8;
+    }
     // Smaller prefix units: one block a CU, since every further range of a row costs its
-    // partial sums' way to memory and back; but two where ranges still hold 512 tokens
-    // and a block alone does not keep its CU busy (staged by four waves, or 4-bit).
-    // us with one / two, 8 key heads of 128 columns: 64 rows, MX8, 8192 tokens 17.8 /
-    // 19.7, 16384 24.4 / 24.2, 32768 37.5 / 31.8; 128 rows, 16-bit, 8192 21.1 / 26.6,
-    // 32768 42.6 / 45.1, 65536 70.9 / 67.2; 32 rows, MX8, 32768 20.7 / 23.9; 16 rows, MX4,
-    // 8192 10.9 / 11.6, 32768 16.9 / 15.1, MX8, 131072 50.1 / 51.8.
-    const int64_t prefix_units = heads * p.prefix_groups;
-    const bool two = (p.waves == 4 || format == NM_KV_MX4) && prefix_len * prefix_units >= 512 * 2 * kCus;
+    // partial sums' way to memory and back; but two where ranges are long all the same,
+    // a block alone does not keep its CU busy (staged by four waves, or 4-bit) and few
+    // own tokens want the room.  us with one / two, 8 key heads of 128 columns: 64 rows,
+    // MX8, 8192 tokens 17.8 / 19.7, 16384 24.4 / 24.2, 32768 37.5 / 31.8; 128 rows, 16-bit,
+    // 8192 21.1 / 26.6, 32768 42.6 / 45.1, 65536 70.9 / 67.2; 32 rows, MX8, 32768 20.7 /
+    // 23.9; 16 rows, MX4, 8192 10.9 / 11.6, 32768 16.9 / 15.1, MX8, 131072 50.1 / 51.8.
+    // With up to 2048 own tokens: 64 rows, MX8, 32768 38.6 / 37.4, 65536 66.7 / 54.4; 128
+    // rows, MX8, 32768 42.9 / 46.3, 65536 73.3 / 68.3; 16 rows, MX4, 32768 15.9 / 18.4.
+    const int64_t prefix_units = heads * p.prefix_groups, longish = format == NM_KV_16 ? 1024 : 512;
+    const bool two = (p.waves == 4 || format == NM_KV_MX4) && prefix_len * prefix_units >= longish * 2 * kCus &&
+                     max_len * 32 <= prefix_len;
     cut(prefix_len, prefix_units, p.waves == 8 ? cus : two ? 2 * kCus : kCus, kMaxTokens, &p.prefix_splits,
         &p.prefix_chunk);
     // Own tokens (us; 8 key heads, MX8, x blocks for each CU): 32 sequences of up to
