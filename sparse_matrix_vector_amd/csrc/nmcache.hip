@@ -41,11 +41,10 @@ struct QkArgs {
 // row's heads hb, hb + blocks_per_row, ... in groups of 256 / LPH.  The row's
 // sines and cosines are computed once per block and kept in LDS; a thread's next
 // load is always in flight (16384 rows of 64 + 8 heads, 604 MB: 172 us with each
-// load waited for at once, 121 with the next one started first, 5.0 TB/s, which
-// is what the card copies at).
+// load waited for at once, 121 with the next one started first).
 //   y = n cos -+ n' sin  with n' the pair's other column: the same thread's for
 // neighbouring pairs, the one rot / 16 lanes away for pairs (i, i + rot / 2).
-template <int DT, int LPH, bool INTERLEAVED>
+template <int DT, int LPH, bool INTERLEAVED, bool ONCE>
 __global__ __launch_bounds__(kQkThreads) void qk_kernel(const QkArgs A)
 {
     __shared__ float cs[2][256];
@@ -63,7 +62,8 @@ __global__ __launch_bounds__(kQkThreads) void qk_kernel(const QkArgs A)
         u32x4 raw = {0u, 0u, 0u, 0u};
         if (live && hh < total) {
             const int side = hh >= A.heads[0], h = side ? hh - A.heads[0] : hh;
-            raw = *reinterpret_cast<const u32x4*>(A.x[side] + t * A.stride[side] + (int64_t)h * A.D + d0);
+            const u32x4* at = reinterpret_cast<const u32x4*>(A.x[side] + t * A.stride[side] + (int64_t)h * A.D + d0);
+            raw = ONCE ? __builtin_nontemporal_load(at) : *at;
         }
         return raw;
     };
@@ -141,20 +141,30 @@ __global__ __launch_bounds__(kQkThreads) void qk_kernel(const QkArgs A)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 out[i] = pack2<DT>(y[2 * i], y[2 * i + 1]);
-            *reinterpret_cast<u32x4*>(A.y[side] + (t * A.heads[side] + h) * A.D + d0) = out;
+            u32x4* at = reinterpret_cast<u32x4*>(A.y[side] + (t * A.heads[side] + h) * A.D + d0);
+            if constexpr (ONCE)
+                __builtin_nontemporal_store(out, at);
+            else
+                *at = out;
         }
     }
 }
 
-template <int DT, int LPH>
+template <int DT, int LPH, bool ONCE>
 int launch_qk(const QkArgs& A, bool interleaved, int64_t blocks, hipStream_t s)
 {
     (void)hipGetLastError();
     if (interleaved)
-        hipLaunchKernelGGL((qk_kernel<DT, LPH, true>), flat_grid(blocks), dim3(kQkThreads), 0, s, A);
+        hipLaunchKernelGGL((qk_kernel<DT, LPH, true, ONCE>), flat_grid(blocks), dim3(kQkThreads), 0, s, A);
     else
-        hipLaunchKernelGGL((qk_kernel<DT, LPH, false>), flat_grid(blocks), dim3(kQkThreads), 0, s, A);
+        hipLaunchKernelGGL((qk_kernel<DT, LPH, false, ONCE>), flat_grid(blocks), dim3(kQkThreads), 0, s, A);
     return hip_status(hipGetLastError());
+}
+
+template <int DT, int LPH>
+int launch_qk(const QkArgs& A, bool interleaved, bool once, int64_t blocks, hipStream_t s)
+{
+    return once ? launch_qk<DT, LPH, true>(A, interleaved, blocks, s) : launch_qk<DT, LPH, false>(A, interleaved, blocks, s);
 }
 
 template <int DT>
@@ -167,16 +177,20 @@ int launch_qk_dt(QkArgs A, bool interleaved, int64_t T, hipStream_t s)
     // One block per pass of a row while the rows are few (every head's loads in
     // flight at once), one block for the whole row when rows fill the GPU.
     A.blocks_per_row = T >= 2 * nma::kCus ? 1 : passes;
+    // Non-temporal from 64 MB of rows on (64 + 8 heads, us without / with: 16384 rows 125.1
+    // / 120.3, with the cache write behind it 143.5 / 137.8; 4096 36.6 / 34.3; 1237 13.5 /
+    // 13.9, 17.3 / 18.0).
+    const bool once = T * (A.heads[0] + A.heads[1]) * A.D * 2 >= int64_t(64) << 20;
     const int64_t row_limit = INT32_MAX / A.blocks_per_row;
     if (T > row_limit)
         return NM_ERR_BAD_SHAPE;
     const int64_t blocks = T * A.blocks_per_row;
     switch (lph) {
-    case 4: return launch_qk<DT, 4>(A, interleaved, blocks, s);
-    case 8: return launch_qk<DT, 8>(A, interleaved, blocks, s);
-    case 16: return launch_qk<DT, 16>(A, interleaved, blocks, s);
-    case 32: return launch_qk<DT, 32>(A, interleaved, blocks, s);
-    default: return launch_qk<DT, 64>(A, interleaved, blocks, s);
+    case 4: return launch_qk<DT, 4>(A, interleaved, once, blocks, s);
+    case 8: return launch_qk<DT, 8>(A, interleaved, once, blocks, s);
+    case 16: return launch_qk<DT, 16>(A, interleaved, once, blocks, s);
+    case 32: return launch_qk<DT, 32>(A, interleaved, once, blocks, s);
+    default: return launch_qk<DT, 64>(A, interleaved, once, blocks, s);
     }
 }
 
@@ -219,9 +233,19 @@ __device__ __forceinline__ int scale_byte(float top)
 // cache line on the rows' side, and on the cache's side eight tokens of a tile
 // make up whole lines.  32768 rows of 8 x 128 in MX8, write / read of 65536 back:
 // 4 rows x 128 columns 51 / 85 us, 8 x 64 48 / 81, 16 x 32 51 / 94 (a thread a
-// unit with 64-bit divisions, before: 63 / 128); the card copies at 4.9 TB/s,
-// which would take 41 / 82.
+// unit with 64-bit divisions, before: 63 / 128; all by one unit a wave); the card
+// copies at 4.9 TB/s, which would take 41 / 82.
+// The rows are touched once, so they are loaded and stored non-temporally and the caches
+// are left to the codes' pieces (us; written rows just produced / long ago, 32768 rows,
+// 16-bit: 52.0 / 69.5 without, 52.0 / 58.4 with; MX8 41.7 / 56.1, 38.6 / 44.2; MX4 31.3 /
+// 49.6, 32.4 / 39.5; 4096 rows, MX8: 10.2 / 13.2, 11.0 / 7.6; 65536 rows read back, MX8 77 ->
+// 62, MX4 68 -> 51, 16-bit 105).
 constexpr int kRows = 8, kCols = 64;
+
+// Units of a wave that reads codes back: two, eight rows apart, their loads in flight
+// together (as above, MX8 81.8 -> 74.7 us, MX4 86.5 -> 71.3; four 76.0 / 73.6).  Not for
+// 16-bit values (2474 rows 6.2 -> 6.7), and not for writes (32768 rows, MX8 47.9 -> 50.2).
+constexpr int read_units(int bits) { return bits == 16 ? 1 : 2; }
 
 struct Lane {
     int64_t t;          // row
@@ -229,13 +253,14 @@ struct Lane {
     bool live;
 };
 
+template <int UNITS>
 __device__ __forceinline__ Lane lane_of(int64_t T, int width)
 {
     const uint32_t lane = threadIdx.x % 64, per = (uint32_t)(width + kCols - 1) / kCols;
     const uint32_t item = flat_block() * (kCacheThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t group = item / per;          // uniform; cache_grid keeps items in 31 bits
     Lane l;
-    l.t = (int64_t)group * kRows + lane / (kCols / 8);
+    l.t = (int64_t)group * (kRows * UNITS) + lane / (kCols / 8);
     l.col = (int)(item - group * per) * kCols + (int)(lane % (kCols / 8)) * 8;
     l.live = l.t < T && l.col < width;
     return l;
@@ -319,11 +344,11 @@ __global__ __launch_bounds__(kCacheThreads) void kv_write_kernel(const CacheArgs
                                                                  const uint16_t* __restrict__ v, int64_t k_stride,
                                                                  int64_t v_stride)
 {
-    const Lane l = lane_of(A.T, A.heads * D);
+    const Lane l = lane_of<1>(A.T, A.heads * D);
     if (!l.live)                    // rows and blocks of 32 columns leave whole, and with them the lanes of a scale
         return;
-    const u32x4 kr = *reinterpret_cast<const u32x4*>(k + l.t * k_stride + l.col);
-    const u32x4 vr = *reinterpret_cast<const u32x4*>(v + l.t * v_stride + l.col);
+    const u32x4 kr = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(k + l.t * k_stride + l.col));
+    const u32x4 vr = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(v + l.t * v_stride + l.col));
     const int64_t slot = A.slots[l.t];
     if (slot < 0 || slot >= A.n_slots)
         return;
@@ -408,20 +433,33 @@ template <int DT, int BITS, int D>
 __global__ __launch_bounds__(kCacheThreads) void kv_read_kernel(const CacheArgs A, uint16_t* __restrict__ k,
                                                                 uint16_t* __restrict__ v)
 {
-    const Lane l = lane_of(A.T, A.heads * D);
+    constexpr int UNITS = read_units(BITS);
+    const Lane l = lane_of<UNITS>(A.T, A.heads * D);
     if (!l.live)
         return;
-    const int64_t slot = A.slots[l.t];
-    u32x4 kr = {0u, 0u, 0u, 0u}, vr = {0u, 0u, 0u, 0u};
-    if (slot >= 0 && slot < A.n_slots) {
-        int token;
-        const int64_t tile = tile_of(A, slot, l.col / D, token);
-        kr = read_unit<DT, BITS, D>(A, 0, tile, token, l.col % D);
-        vr = read_unit<DT, BITS, D>(A, 1, tile, token, l.col % D);
+    int64_t slot[UNITS];
+    u32x4 kr[UNITS], vr[UNITS];
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u)
+        slot[u] = l.t + u * kRows < A.T ? A.slots[l.t + u * kRows] : -1;
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+        kr[u] = vr[u] = u32x4{0u, 0u, 0u, 0u};
+        if (slot[u] >= 0 && slot[u] < A.n_slots) {
+            int token;
+            const int64_t tile = tile_of(A, slot[u], l.col / D, token);
+            kr[u] = read_unit<DT, BITS, D>(A, 0, tile, token, l.col % D);
+            vr[u] = read_unit<DT, BITS, D>(A, 1, tile, token, l.col % D);
+        }
     }
-    const int64_t at = l.t * A.heads * D + l.col;
-    *reinterpret_cast<u32x4*>(k + at) = kr;
-    *reinterpret_cast<u32x4*>(v + at) = vr;
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+        if (l.t + u * kRows >= A.T)
+            break;
+        const int64_t at = (l.t + u * kRows) * A.heads * D + l.col;
+        __builtin_nontemporal_store(kr[u], reinterpret_cast<u32x4*>(k + at));
+        __builtin_nontemporal_store(vr[u], reinterpret_cast<u32x4*>(v + at));
+    }
 }
 
 CacheArgs cache_args(const nm_kv_cache& c, const int64_t* slots, int64_t T)
@@ -461,9 +499,9 @@ int by_cache(const nm_kv_cache& c, Fn fn)
                               : by_bits(std::integral_constant<int, NM_BF16>());
 }
 
-int cache_grid(const nm_kv_cache& c, int64_t T, dim3* grid)
+int cache_grid(const nm_kv_cache& c, int64_t T, int units, dim3* grid)
 {
-    const int64_t items = nma::ceil_div(T, kRows) * nma::ceil_div((int64_t)c.heads * c.D, kCols);
+    const int64_t items = nma::ceil_div(T, kRows * units) * nma::ceil_div((int64_t)c.heads * c.D, kCols);
     if (items > INT32_MAX)
         return NM_ERR_BAD_SHAPE;
     *grid = flat_grid(nma::ceil_div(items, kCacheThreads / 64));
@@ -502,7 +540,7 @@ int nmk::kv_write(const nm_kv_cache& cache, const void* k, int64_t k_stride, con
                   const int64_t* slots, void* stream)
 {
     dim3 grid;
-    if (cache_grid(cache, T, &grid) != NM_OK)
+    if (cache_grid(cache, T, 1, &grid) != NM_OK)
         return NM_ERR_BAD_SHAPE;
     const CacheArgs A = cache_args(cache, slots, T);
     return by_cache(cache, [&](auto dt, auto bits, auto d) {
@@ -517,7 +555,7 @@ int nmk::kv_write(const nm_kv_cache& cache, const void* k, int64_t k_stride, con
 int nmk::kv_read(const nm_kv_cache& cache, const int64_t* slots, int64_t T, void* k, void* v, void* stream)
 {
     dim3 grid;
-    if (cache_grid(cache, T, &grid) != NM_OK)
+    if (cache_grid(cache, T, read_units(nma::format_bits(cache.format)), &grid) != NM_OK)
         return NM_ERR_BAD_SHAPE;
     const CacheArgs A = cache_args(cache, slots, T);
     return by_cache(cache, [&](auto dt, auto bits, auto d) {
