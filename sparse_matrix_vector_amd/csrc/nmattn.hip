@@ -22,9 +22,9 @@
 // Own tokens are bound by HBM: 32 sequences of 4096 tokens, 8 key heads of 128
 // columns, MX8, take 45.5 us, 6.1 TB/s; with few or very different sequences the
 // start of the blocks and the joining of ranges show (16 of 0 .. 8192: 29 + 4 us, 5.1
-// TB/s; one of 131071, MX4: 27 + 5, 5.3).  A shared prefix is bound by the matrix
-// cores' and vector units' power at 256 rows (131072 tokens: 175 us, 790 TFLOP/s on
-// random values, 37% less time on zeros) and by HBM below.
+// TB/s; one of 131071, MX4: 25 + 4, 5.8).  A shared prefix is bound by the matrix
+// cores' and vector units' power at 256 rows (131072 tokens: 165 to 199 us as the
+// clock allows, 690 to 830 TFLOP/s, on random values, 154 us on zeros) and by HBM below.
 
 #include <hip/hip_runtime.h>
 
