@@ -22,11 +22,14 @@ def _dtype(dtype):
     return _DT[dtype]
 
 
+# Devices are numbers here (of a GPU; -1: the host), since comparing device objects
+# is what a check of a tensor would spend most of its time on.
+
 def _refuse(t, name, device, dtype, shape):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
@@ -37,7 +40,7 @@ def _refuse(t, name, device, dtype, shape):
 def _check(t, name, device, dtype, shape):
     """Address of t, which is a contiguous tensor on the GPU `device` with
     `dtype` and `shape`."""
-    if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype is dtype and t.shape == shape and
+    if not (isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype is dtype and t.shape == shape and
             t.is_contiguous()):
         _refuse(t, name, device, dtype, shape)
     return t.data_ptr()
@@ -55,7 +58,7 @@ def _size(t, name, dims):
 
 def _rows(t, name, device, dtype, shape):
     """Address and row stride of strided rows [rows][heads][D] of that shape."""
-    if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype is dtype and t.shape == shape):
+    if not (isinstance(t, torch.Tensor) and t.get_device() == device and t.dtype is dtype and t.shape == shape):
         _refuse(t, name, device, dtype, shape)
     rows, heads, D = shape
     if t.is_contiguous():
@@ -79,8 +82,8 @@ class _Other:
     close() (torch's allocator then hands out memory of that stream)."""
 
     def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, not on {device}")
+        if stream is not None and stream.device.index != device:
+            raise ValueError(f"stream is on {stream.device}, not on cuda:{device}")
         self.guard = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
         self.guard.__enter__()
 
@@ -90,9 +93,9 @@ class _Other:
 
 def _other(device, stream):
     """None where work goes to the current stream of the current device."""
-    if not device.type == "cuda":
-        raise TypeError(f"tensors must be CUDA (HIP) tensors, not on {device}")
-    return None if stream is None and device.index == _device() else _Other(device, stream)
+    if device < 0:
+        raise TypeError("tensors must be CUDA (HIP) tensors")
+    return None if stream is None and device == _device() else _Other(device, stream)
 
 
 _lib = None
@@ -102,12 +105,6 @@ def _load():
     global _lib
     _lib = attn_lib()
     return _lib
-
-
-def _call(name, *args):
-    st = getattr(_lib or _load(), name)(*args)
-    if st != NM_OK:
-        raise NmError(name, st)
 
 
 def _empty(like, shape):
@@ -126,7 +123,7 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, interlea
     T, hq, D = shape
     hk = _size(k, "k", 3)[1]
     pairs, = _size(inv_freq, "inv_freq", 1)
-    dev, dt = q.device, q.dtype
+    dev, dt = q.get_device(), q.dtype
     code = _dtype(dt)
     qp, qs = _rows(q, "q", dev, dt, shape)
     kp, ks = _rows(k, "k", dev, dt, (T, hk, D))
@@ -142,11 +139,13 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, interlea
         else:
             oqp = _check(out[0], "out[0]", dev, dt, shape)
             okp = _check(out[1], "out[1]", dev, dt, (T, hk, D))
-        _call("nm_qk_norm_rope", qp, qs, kp, ks, T, hq, hk, D, code, wqp, wkp, eps, pos, freq, 2 * pairs,
-              1 if interleaved else 0, oqp, okp, _stream(dev.index))
+        st = (_lib or _load()).nm_qk_norm_rope(qp, qs, kp, ks, T, hq, hk, D, code, wqp, wkp, eps, pos, freq,
+                                               2 * pairs, 1 if interleaved else 0, oqp, okp, _stream(dev))
     finally:
         if other is not None:
             other.close()
+    if st != NM_OK:
+        raise NmError("nm_qk_norm_rope", st)
     return out[0], out[1]
 
 
@@ -156,7 +155,7 @@ class KVCache:
     "mx8" and "mx4" keep 8- and 4-bit floats (e4m3, e2m1) with one power-of-two
     scale per 32 columns.  A slot is page * page_size + place in the page."""
 
-    __slots__ = ("_buffers", "_struct", "_ref", "_format", "device", "dtype", "format", "n_pages", "page_size", "heads", "D")
+    __slots__ = ("_buffers", "_struct", "_ref", "_format", "_index", "device", "dtype", "format", "n_pages", "page_size", "heads", "D")
 
     def __init__(self, n_pages, page_size, heads, D, dtype, format="16", device="cuda"):
         if format not in _FORMATS:
@@ -172,6 +171,7 @@ class KVCache:
                             for _ in range(2))
         self._buffers = (k, v, k_scale, v_scale)
         self.device, self.dtype, self.format, self._format = k.device, dtype, format, fmt
+        self._index = k.get_device()
         self.n_pages, self.page_size, self.heads, self.D = n_pages, page_size, heads, D
         self._struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if sbytes else None,
                                      v_scale.data_ptr() if sbytes else None, n_pages, page_size, heads, D, code, fmt)
@@ -210,39 +210,45 @@ def kv_write(cache, k, v, slots, stream=None):
     to the cache's format.  A negative slot, or one behind the last, is
     skipped; no slot twice in one call."""
     c = _cache(cache)
+    dev, dt = c._index, c.dtype
     T, = _size(slots, "slots", 1)
-    sp = _check(slots, "slots", c.device, torch.int64, (T,))
+    sp = _check(slots, "slots", dev, torch.int64, (T,))
     shape = (T, c.heads, c.D)
-    kp, ks = _rows(k, "k", c.device, c.dtype, shape)
-    vp, vs = _rows(v, "v", c.device, c.dtype, shape)
-    other = _other(c.device, stream)
+    kp, ks = _rows(k, "k", dev, dt, shape)
+    vp, vs = _rows(v, "v", dev, dt, shape)
+    other = _other(dev, stream)
     try:
-        _call("nm_kv_write", c._ref, kp, ks, vp, vs, T, sp, _stream(c.device.index))
+        st = (_lib or _load()).nm_kv_write(c._ref, kp, ks, vp, vs, T, sp, _stream(dev))
     finally:
         if other is not None:
             other.close()
+    if st != NM_OK:
+        raise NmError("nm_kv_write", st)
 
 
 def kv_read(cache, slots, out=None, stream=None):
     """(k, v) [T][heads][D] in the cache's dtype from slots (int64 [T]); zeros
     for a slot outside the cache."""
     c = _cache(cache)
+    dev, dt = c._index, c.dtype
     T, = _size(slots, "slots", 1)
-    sp = _check(slots, "slots", c.device, torch.int64, (T,))
+    sp = _check(slots, "slots", dev, torch.int64, (T,))
     shape = (T, c.heads, c.D)
-    other = _other(c.device, stream)
+    other = _other(dev, stream)
     try:
         if out is None:
-            k = slots.new_empty(shape, dtype=c.dtype)
+            k = slots.new_empty(shape, dtype=dt)
             out = k, torch.empty_like(k)
             kp, vp = k.data_ptr(), out[1].data_ptr()
         else:
-            kp = _check(out[0], "out[0]", c.device, c.dtype, shape)
-            vp = _check(out[1], "out[1]", c.device, c.dtype, shape)
-        _call("nm_kv_read", c._ref, sp, T, kp, vp, _stream(c.device.index))
+            kp = _check(out[0], "out[0]", dev, dt, shape)
+            vp = _check(out[1], "out[1]", dev, dt, shape)
+        st = (_lib or _load()).nm_kv_read(c._ref, sp, T, kp, vp, _stream(dev))
     finally:
         if other is not None:
             other.close()
+    if st != NM_OK:
+        raise NmError("nm_kv_read", st)
     return out[0], out[1]
 
 
@@ -268,7 +274,7 @@ def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, pre
     [B][Hq][D]; ``lse`` (float32 [B][Hq]) receives the log of the softmax's
     sum.  ``ws``: an attn_workspace(), or None to allocate one."""
     c = _cache(cache)
-    dev, dt = c.device, c.dtype
+    dev, dt = c._index, c.dtype
     B, hq, _ = _size(q, "q", 3)
     shape = (B, hq, c.D)
     qp, qs = _rows(q, "q", dev, dt, shape)
@@ -279,7 +285,7 @@ def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, pre
         if page_table.is_contiguous():
             table, stride = _check(page_table, "page_table", dev, torch.int32, (B, width)), width
         else:
-            if (width > 1 and page_table.stride(1) != 1) or page_table.device != dev or \
+            if (width > 1 and page_table.stride(1) != 1) or page_table.get_device() != dev or \
                     page_table.dtype != torch.int32 or page_table.shape[0] != B:
                 _refuse(page_table, "page_table (rows)", dev, torch.int32, (B, width))
             table, stride = page_table.data_ptr(), page_table.stride(0)
@@ -310,9 +316,12 @@ def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, pre
             if nbytes > 0:
                 ws = q.new_empty(nbytes, dtype=torch.uint8)
                 wsp = ws.data_ptr()
-        _call("nm_attn_decode", qp, qs, B, hq, c._ref, pp, prefix_len, table, stride, lp, max_len,
-              c.D ** -0.5 if scale is None else scale, op, lsep, wsp, max(nbytes, 0), _stream(dev.index))
+        st = (_lib or _load()).nm_attn_decode(qp, qs, B, hq, c._ref, pp, prefix_len, table, stride, lp, max_len,
+                                              c.D ** -0.5 if scale is None else scale, op, lsep, wsp, max(nbytes, 0),
+                                              _stream(dev))
     finally:
         if other is not None:
             other.close()
+    if st != NM_OK:
+        raise NmError("nm_attn_decode", st)
     return out
