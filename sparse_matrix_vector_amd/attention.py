@@ -107,9 +107,11 @@ def _load():
     return _lib
 
 
-def _empty(like, shape):
-    """A new contiguous tensor of that shape on like's device, in its dtype."""
-    return torch.empty_like(like) if like.shape == shape and like.is_contiguous() else like.new_empty(shape)
+def _empty(like, stride):
+    """A new contiguous tensor of the shape, dtype and device of the rows `like`,
+    whose row stride _rows() found to be `stride`."""
+    rows, heads, D = like.shape
+    return torch.empty_like(like) if stride == heads * D else like.new_empty((rows, heads, D))
 
 
 def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, interleaved=False, out=None, stream=None):
@@ -134,7 +136,7 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, interlea
     other = _other(dev, stream)
     try:
         if out is None:
-            out = oq, ok = _empty(q, shape), _empty(k, (T, hk, D))
+            out = oq, ok = _empty(q, qs), _empty(k, ks)
             oqp, okp = oq.data_ptr(), ok.data_ptr()
         else:
             oqp = _check(out[0], "out[0]", dev, dt, shape)
@@ -307,7 +309,7 @@ def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, pre
     other = _other(dev, stream)
     try:
         if out is None:
-            out = _empty(q, shape)
+            out = _empty(q, qs)
             op = out.data_ptr()
         else:
             op = _check(out, "out", dev, dt, shape)
