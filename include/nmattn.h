@@ -138,8 +138,9 @@ int nm_kv_read(const nm_kv_cache* cache, const int64_t* slots, int64_t T, void* 
  *   workspace          nm_attn_workspace_bytes(...) bytes of device memory,
  *                      256-byte aligned, any contents; may be NULL when that is 0.
  * A page number outside the cache is not followed: its tokens count as absent.
- * Scores, softmax statistics and sums are fp32; the weights of the sum are
- * rounded to dtype, the operand type of the matrix cores, and o once to dtype.
+ * Scores, softmax statistics and sums are fp32; the weights of the sum go into
+ * the matrix cores as two operands of dtype each (2^-16 of a weight is lost in
+ * bfloat16, 2^-22 in fp16), and o is rounded once to dtype.
  * Results do not depend on other calls and repeat bit for bit.
  * Infinities and NaN in a token that is seen have the effect that the formula
  * gives them (a score of -inf weighs nothing; a row with no other scores gets

@@ -324,9 +324,30 @@ __device__ __forceinline__ void mask_scores(f32x4 (&sc)[MT][NT], const int (&n)[
                     sc[g][u][r] = NM_NEG_INF;               // whatever lies there, NaN included
 }
 
-// The softmax weights of a step of NT tiles, as right operands of the second
-// product (one for each pair of tiles); updates the rows' references (mx), sums and,
-// where a reference grows, what has been added up so far.
+// What a dword of two 16-bit floats, `whole`, leaves out of the fp32 a and b that were
+// rounded to it, as another such dword.  The differences are exact.  In fp16 the empty
+// statement keeps the compiler from rounding a and b a second time.  In bfloat16 a
+// difference is one dot product with (-1, 0) or (0, -1); these come from scalar
+// registers, since of the constants the compiler makes the first the instruction's
+// inline -1.0, which the hardware takes for (0, -1).
+template <int DT>
+__device__ __forceinline__ uint32_t left_out(uint32_t whole, float a, float b)
+{
+    if constexpr (DT == NM_FP16) {
+        asm("" : "+v"(whole));
+        const f32x2 w = unpack2<DT>(whole);
+        return pack2<DT>(a - w.x, b - w.y);
+    } else {
+        uint32_t low = 0x0000BF80u, high = 0xBF800000u;
+        asm("" : "+s"(low), "+s"(high));
+        const bf16x2 w = __builtin_bit_cast(bf16x2, whole);
+        return pack2<DT>(__builtin_amdgcn_fdot2_f32_bf16(w, __builtin_bit_cast(bf16x2, low), a, false),
+                         __builtin_amdgcn_fdot2_f32_bf16(w, __builtin_bit_cast(bf16x2, high), b, false));
+    }
+}
+
+// The softmax weights of a step of NT tiles, in place of its scores; updates the rows'
+// references (mx), sums and, where a reference grows, what has been added up so far.
 template <int DT, int MT, int NT>
 struct Weights {
     // A row's reference `mx` may lag behind its maximum by this much (base 2): weights
@@ -335,11 +356,10 @@ struct Weights {
     // tokens, 16-bit: 67.5 us without, 63.7 with it; MX8 and 4096 own tokens 82.6 / 78.6.
     static constexpr float kSlack = 8.0f;
 
-    u32x4 op[MT][NT / 2];
+    f32x4 p[MT][NT];
 
     template <int PER>
-    __device__ __forceinline__ void find(const f32x4 (&sc)[MT][NT], float (&mx)[MT], float (&sum)[MT],
-                                         f32x4 (&acc)[MT][PER], float scale)
+    __device__ __forceinline__ void find(float (&mx)[MT], float (&sum)[MT], f32x4 (&acc)[MT][PER], float scale)
     {
 #pragma unroll
         for (int g = 0; g < MT; ++g) {
@@ -348,7 +368,7 @@ struct Weights {
             for (int u = 0; u < NT; ++u)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    top = fmaxf(top, sc[g][u][r]);
+                    top = fmaxf(top, p[g][u][r]);
             top = fmaxf(mx[g], quarters_max(top) * scale);
             if (__any(top > mx[g] + kSlack)) {
                 const float f = mx[g] == top ? 1.0f : __builtin_amdgcn_exp2f(mx[g] - top);
@@ -360,18 +380,39 @@ struct Weights {
             }
             const float base = mx[g] == NM_NEG_INF ? 0.0f : mx[g];
 #pragma unroll
-            for (int t = 0; t < NT / 2; ++t) {
-                float p[8];
+            for (int u = 0; u < NT; ++u)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[g][2 * t + i / 4][i % 4], scale, -base));
-                    sum[g] += p[i];
+                for (int r = 0; r < 4; ++r) {
+                    p[g][u][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[g][u][r], scale, -base));
+                    sum[g] += p[g][u][r];
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    op[g][t][i] = pack2<DT>(p[2 * i], p[2 * i + 1]);
-            }
         }
+    }
+
+    // Right operands of the second product for tiles 2 t, 2 t + 1: a weight is the sum of
+    // two 16-bit floats, its own rounding (whole) and what that leaves out (rest).  That
+    // keeps it to 2^-16 of itself in bfloat16 and 2^-22 in fp16; one alone would leave
+    // 2^-8 and 2^-11, as much as o's own rounding.  Own tokens, bound by HBM, hardly
+    // notice the second product (32 sequences of 4096, us with one / two: 16-bit 83.7 / 83.7,
+    // MX8 45.6 / 45.4, MX4 34.3 / 37.2); staged prefix units, bound by the matrix cores,
+    // do (32 sequences of 64 heads behind 32768 tokens 64.5 / 75.7, of 32 heads behind 8192
+    // 23.4 / 25.0).
+    __device__ __forceinline__ void whole(u32x4 (&out)[MT], int t) const
+    {
+#pragma unroll
+        for (int g = 0; g < MT; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                out[g][i] = pack2<DT>(p[g][2 * t + i / 2][i % 2 * 2], p[g][2 * t + i / 2][i % 2 * 2 + 1]);
+    }
+
+    __device__ __forceinline__ void rest(u32x4 (&out)[MT], const u32x4 (&w)[MT], int t) const
+    {
+#pragma unroll
+        for (int g = 0; g < MT; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                out[g][i] = left_out<DT>(w[g][i], p[g][2 * t + i / 2][i % 2 * 2], p[g][2 * t + i / 2][i % 2 * 2 + 1]);
     }
 };
 
@@ -469,7 +510,8 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
             fetch();
         }
         // scores
-        f32x4 sc[MT][2];
+        Weights<DT, MT, 2> w;
+        auto& sc = w.p;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -491,8 +533,10 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
             const int n[2] = {cur[0].n, cur[1].n};
             mask_scores(sc, n, kg);
         }
-        Weights<DT, MT, 2> w;
-        w.find(sc, mx, sum, acc, A.scale);
+        w.find(mx, sum, acc, A.scale);
+        u32x4 wo[2][MT];
+        w.whole(wo[0], 0);
+        w.rest(wo[1], wo[0], 0);
         // values
         uint32_t vo[2][2 * kPer];
 #pragma unroll
@@ -511,13 +555,14 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
             }
         }
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const u32x4 a = {vo[0][2 * j], vo[0][2 * j + 1], vo[1][2 * j], vo[1][2 * j + 1]};
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int g = 0; g < MT; ++g) {
-                acc[g][j] = mfma<DT>(a, w.op[g][0], acc[g][j]);
+            for (int j = 0; j < kPer; ++j) {
+                const u32x4 a = {vo[0][2 * j], vo[0][2 * j + 1], vo[1][2 * j], vo[1][2 * j + 1]};
+#pragma unroll
+                for (int g = 0; g < MT; ++g)
+                    acc[g][j] = mfma<DT>(a, wo[i][g], acc[g][j]);
             }
-        }
         if constexpr (more()) {
             load_v(next);
             cur[0] = next[0];
@@ -792,7 +837,8 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, int unit, uint8
                 for (int j = 0; j < kGroup; ++j)
                     va[x % 2][j] = *reinterpret_cast<const u32x4*>(vb + (x * kGroup + j) * 1024 + lane * 16);
             };
-            f32x4 sc[MT][NT];
+            Weights<DT, MT, NT> w;
+            auto& sc = w.p;
             read_k(0);
 #pragma unroll
             for (int u = 0; u < NT; ++u) {
@@ -821,22 +867,29 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, int unit, uint8
             }
             if (!whole)
                 mask_scores(sc, n, kg);
-            Weights<DT, MT, NT> w;
-            w.find(sc, mx, sum, acc, A.scale);
+            w.find(mx, sum, acc, A.scale);
             constexpr int kGroups = NT / 2 * kPer / kGroup;
+            u32x4 wo[2][MT];
 #pragma unroll
             for (int x = 0; x < kGroups; ++x) {
+                const bool first = x * kGroup % kPer == 0;
+                const int t = x * kGroup / kPer;
                 if (x + 1 < kGroups)
                     read_v(x + 1);
+                if (first)
+                    w.whole(wo[0], t);
                 __builtin_amdgcn_sched_barrier(0);
+                if (first)              // beside the first products
+                    w.rest(wo[1], wo[0], t);
 #pragma unroll
-                for (int c = 0; c < kGroup; ++c) {
-                    const int j = (x * kGroup + c) % kPer, t = (x * kGroup + c) / kPer;
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int g = 0; g < MT; ++g) {
-                        acc[g][j] = mfma<DT>(va[x % 2][c], w.op[g][t], acc[g][j]);
-                    }
-                }
+                    for (int c = 0; c < kGroup; ++c)
+#pragma unroll
+                        for (int g = 0; g < MT; ++g) {
+                            const int j = (x * kGroup + c) % kPer;
+                            acc[g][j] = mfma<DT>(va[x % 2][c], wo[i][g], acc[g][j]);
+                        }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
