@@ -140,13 +140,14 @@ int nm_kv_read(const nm_kv_cache* cache, const int64_t* slots, int64_t T, void* 
  * A page number outside the cache is not followed: its tokens count as absent.
  * Scores, softmax statistics and sums are fp32; the weights of the sum go into
  * the matrix cores as two operands of dtype each (2^-16 of a weight is lost in
- * bfloat16, 2^-22 in fp16), and o is rounded once to dtype.
+ * bfloat16; in fp16 2^-22 of it, or 2^-32 of the row's largest one if that is
+ * more), and o is rounded once to dtype.
  * Results do not depend on other calls and repeat bit for bit.
  * Infinities and NaN in a token that is seen have the effect that the formula
  * gives them (a score of -inf weighs nothing; a row with no other scores gets
- * zeros), and so have fp32 sums that overflow, in which a token's value counts up
- * to 2^8 times; in a token that is not seen they have none.  (In a quantised bfloat16 cache magnitudes of 2^127 and more count as
- * infinities here.)
+ * zeros), and so have fp32 sums that overflow, in which a bfloat16 token's value
+ * counts up to 2^8 times; in a token that is not seen they have none.  (In a
+ * quantised bfloat16 cache magnitudes of 2^127 and more count as infinities here.)
  * B and Hq 1..65535, B * Hq below 2^26, prefix_len and max_len 0..2^30, |scale| <= 1e30.  o, lse
  * and workspace must not overlap anything else.
  */

@@ -3,8 +3,8 @@
 // For the rows (query heads) q of a unit and its tokens t, with scores
 // s_t = scale * q . k_t, one pass keeps a reference m near the running maximum, the
 // sum l = sum exp(s_t - m) and the vector o = sum exp(s_t - m) v_t, multiplying l and
-// o by exp(m_old - m_new) where m is raised to the maximum; units of one row are
-// joined by the same rule (combine_kernel).
+// o by exp(m_old - m_new) where m is raised (Weights); units of one row are joined by
+// the same rule (combine_kernel).
 //
 // Everything runs on the matrix cores with the cache as the left operand, 16
 // tokens or 16 columns by 16 rows (v_mfma_f32_16x16x32):
@@ -350,11 +350,17 @@ __device__ __forceinline__ uint32_t left_out(uint32_t whole, float a, float b)
 // references (mx), sums and, where a reference grows, what has been added up so far.
 template <int DT, int MT, int NT>
 struct Weights {
-    // A row's reference `mx` may lag behind its maximum by this much (base 2): weights
-    // are at most 2^8 then, which both types and the fp32 sums have room for, and in long
-    // ranges the sums are hardly ever multiplied.  32 sequences of 64 heads behind 32768
-    // tokens, 16-bit: 67.5 us without, 63.7 with it; MX8 and 4096 own tokens 82.6 / 78.6.
-    static constexpr float kSlack = 8.0f;
+    // Weights are relative to a row's reference `mx` (base 2), which need not be its maximum.
+    // It is raised where a score passes it by more than kRoom, and is then put kBelow under
+    // that score, so that the largest weight lies between 2^kBelow and 2^kRoom.
+    //   It may lag, so that in long ranges the sums are hardly ever multiplied: 32 sequences
+    // of 64 heads behind 32768 tokens, 16-bit: 67.5 us with the maximum itself, 63.7 with
+    // it up to 2^8 behind; MX8 and 4096 own tokens 82.6 / 78.6.  In fp16 it stays below:
+    // the operands' range then ends at 2^-32 of the largest weight, not at 2^-25, where
+    // the tokens behind a first one that takes most of the weight would be lost; 2^15 is
+    // the last power of two that fits (65504).
+    static constexpr float kBelow = DT == NM_FP16 ? 7.0f : 0.0f;
+    static constexpr float kRoom = DT == NM_FP16 ? 15.0f : 8.0f;
 
     f32x4 p[MT][NT];
 
@@ -369,8 +375,9 @@ struct Weights {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     top = fmaxf(top, p[g][u][r]);
-            top = fmaxf(mx[g], quarters_max(top) * scale);
-            if (__any(top > mx[g] + kSlack)) {
+            top = quarters_max(top) * scale;
+            if (__any(top > mx[g] + kRoom)) {
+                top = fmaxf(mx[g], top - kBelow);
                 const float f = mx[g] == top ? 1.0f : __builtin_amdgcn_exp2f(mx[g] - top);
                 sum[g] *= f;
 #pragma unroll

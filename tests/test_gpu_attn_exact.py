@@ -50,6 +50,10 @@ def attend_exact(q, keys, values, scale, dtype, small):
     return o, tol
 
 
+# A weight's two fp16 parts end at multiples of 2^-24 and the largest weight is at least 2^7; bfloat16 reaches 2^-126.
+SMALL = {F16: 2.0 ** -32, BF16: 0.0}
+
+
 def check(b, scale, small):
     """`small`: see attend_exact()."""
     o = b.run(scale=scale)
@@ -75,4 +79,24 @@ def test_weights_keep_their_bits(nm, dtype, fmt, D, hq, heads, P, lens):  # noqa
     b.q = rnd(b.q.shape, torch.float32, "eq", D).round().clamp(-1, 1).to(dtype)
     refill(b, grid(b.k.shape, dtype, "ek", D), grid(b.v.shape, dtype, "ev", D))
     assert np.array_equal(b.qk, ref.f64(b.k)) and np.array_equal(b.qv, ref.f64(b.v))
-    check(b, 0.5 / np.sqrt(D), 2.0 ** -25 if dtype == F16 else 0.0)
+    check(b, 0.5 / np.sqrt(D), SMALL[dtype])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", (F16, BF16))
+@pytest.mark.parametrize("gap", (16.7, 17.5, 19.0))
+@pytest.mark.parametrize("D,hq,heads,P,lens", ((128, 4, 2, 0, [32, 33]), (64, 4, 1, 0, [700]), (128, 4, 4, 200, [3]),
+                                               (128, 4, 1, 90, [1, 0, 2, 3, 1]), (64, 8, 1, 300, [5] * 20),
+                                               (128, 16, 1, 300, [2, 0] * 9), (256, 32, 4, 150, [1] * 6)))
+def test_far_tokens_count(nm, dtype, fmt, gap, D, hq, heads, P, lens):  # noqa: F811
+    """One token far above all others, with values of zero (a first token that takes most of the weight): what o is
+    comes from the others, each of them below fp16's least number beside that token's weight of one."""
+    b = Batch(nm, dtype, fmt, D, hq, heads, 16, P, lens)
+    b.q = torch.zeros_like(b.q)
+    b.q[..., 0] = 1.0
+    k = torch.zeros_like(b.k)
+    k[0, :, 0] = 6.0
+    v = grid(b.v.shape, dtype, "fv", D) * 4096
+    v[0] = 0.0
+    refill(b, k, v)
+    check(b, gap / 6, SMALL[dtype])
