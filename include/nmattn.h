@@ -146,7 +146,7 @@ int nm_kv_read(const nm_kv_cache* cache, const int64_t* slots, int64_t T, void* 
  * Infinities and NaN in a token that is seen have the effect that the formula
  * gives them (a score of -inf weighs nothing; a row with no other scores gets
  * zeros), and so have fp32 sums that overflow, in which a bfloat16 token's value
- * counts up to 2^8 times; in a token that is not seen they have none.  (In a
+ * counts once at most; in a token that is not seen they have none.  (In a
  * quantised bfloat16 cache magnitudes of 2^127 and more count as infinities here.)
  * B and Hq 1..65535, B * Hq below 2^26, prefix_len and max_len 0..2^30, |scale| <= 1e30.  o, lse
  * and workspace must not overlap anything else.

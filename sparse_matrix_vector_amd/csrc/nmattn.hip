@@ -358,9 +358,10 @@ struct Weights {
     // it up to 2^8 behind; MX8 and 4096 own tokens 82.6 / 78.6.  In fp16 it stays below:
     // the operands' range then ends at 2^-32 of the largest weight, not at 2^-25, where
     // the tokens behind a first one that takes most of the weight would be lost; 2^15 is
-    // the last power of two that fits (65504).
-    static constexpr float kBelow = DT == NM_FP16 ? 7.0f : 0.0f;
-    static constexpr float kRoom = DT == NM_FP16 ? 15.0f : 8.0f;
+    // the last power of two that fits (65504).  bfloat16 has fp32's range, and values near
+    // its end: the reference stays above, and no value is added more than once.
+    static constexpr float kBelow = DT == NM_FP16 ? 7.0f : -8.0f;
+    static constexpr float kRoom = DT == NM_FP16 ? 15.0f : 0.0f;
 
     f32x4 p[MT][NT];
 

@@ -100,3 +100,24 @@ def test_far_tokens_count(nm, dtype, fmt, gap, D, hq, heads, P, lens):  # noqa: 
     v[0] = 0.0
     refill(b, k, v)
     check(b, gap / 6, SMALL[dtype])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("size", (2.0 ** 121, 2.0 ** -118))
+@pytest.mark.parametrize("hq,heads,P,lens", ((4, 2, 0, [90, 33]), (4, 1, 0, [900]), (4, 1, 90, [40, 0, 2, 3, 1]),
+                                             (8, 1, 300, [5] * 20)))
+def test_bfloat16_values_near_the_ends(nm, fmt, size, hq, heads, P, lens):  # noqa: F811
+    """Values up to 6 2^121 with scores that climb from 0 over 0.9 to 7 (base 2) in the last tokens: weights above one
+    would take the sums past fp32, weights of at most one, 2^-8 for the first tokens, keep them below 2^127.  And
+    values down to the type's least normal ones."""
+    b.q = torch.zeros_like(b.q)
+    b.q[..., 0] = 1.0
+    k = torch.zeros_like(b.k)
+    k[..., 0] = 0.5                                   # (a value of every format)
+    for i in range(len(lens)):
+        t = b.tokens(i)
+        k[t[:16], :, 0] = 0.0
+        if len(t) > 32:
+            k[t[-2:], :, 0] = 4.0
+    refill(b, k, (grid(b.v.shape, BF16, "bv").float() * size).to(BF16))
+    check(b, 7 * np.log(2) / 4, SMALL[BF16])
