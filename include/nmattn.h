@@ -137,6 +137,8 @@ int nm_kv_read(const nm_kv_cache* cache, const int64_t* slots, int64_t T, void* 
  *                      token), or NULL.
  *   workspace          nm_attn_workspace_bytes(...) bytes of device memory,
  *                      256-byte aligned, any contents; may be NULL when that is 0.
+ *                      So many bytes also serve every call with the same Hq,
+ *                      heads, D and format and no larger B, prefix_len and max_len.
  * A page number outside the cache is not followed: its tokens count as absent.
  * Scores, softmax statistics and sums are fp32; the weights of the sum go into
  * the matrix cores as two operands of dtype each (2^-16 of a weight is lost in

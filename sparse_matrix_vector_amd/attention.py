@@ -255,8 +255,9 @@ def kv_read(cache, slots, out=None, stream=None):
 
 
 def attn_workspace(B, heads_q, cache, max_len, prefix_len=0):
-    """A workspace for attn_decode calls of this shape on the cache's device
-    (any contents; calls that may run at the same time need one each)."""
+    """A workspace for attn_decode calls of this shape, or of no larger B,
+    max_len and prefix_len, on the cache's device (any contents; calls that may
+    run at the same time need one each)."""
     c = _cache(cache)
     nbytes = attn_lib().nm_attn_workspace_bytes(B, heads_q, c.heads, c.D, c._format, prefix_len, max_len)
     if nbytes < 0:

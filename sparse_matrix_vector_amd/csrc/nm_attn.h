@@ -191,6 +191,37 @@ inline AttnPlan attn_plan(int64_t B, int Hq, int heads, int D, int format, int64
 // Workspace: every partial row's D sums, then every row's (maximum, sum).
 inline int64_t attn_workspace(const AttnPlan& p, int D) { return (p.prefix_parts + p.own_parts) * (D + 2) * 4; }
 
+// A workspace that serves every call of no larger B, prefix_len and max_len.  A plan's own
+// is no such thing: a longer max_len leaves the prefix fewer CUs, and ranges are rounded up
+// to whole steps, so that one sequence of 32 heads on 8 takes 1 064 960 bytes at 8192 tokens
+// and 549 120 at 8193.  From the rules of attn_plan and cut:
+//   own tokens, u = units of a sequence: a sequence has at most ceil(max_len / 128) ranges,
+//   and B sequences together ceil(512 / (B u)) B <= 512 / u + B while B u < 256, or B times
+//   the ranges of at most 4096 tokens (64; kMaxBlocks units in all);
+//   prefix: at most ceil(prefix_len / 128) ranges of heads * B G rows, and `blocks` blocks of
+//   at most 16 mt waves rows, beside one more range of every row for rounding up.
+inline int64_t attn_workspace_bound(int64_t B, int Hq, int heads, int D, int format, int64_t prefix_len, int64_t max_len)
+{
+    if (prefix_len == 0 && max_len <= 512)
+        return 0;
+    const auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+    const auto most = [](int64_t a, int64_t b) { return a > b ? a : b; };
+    const int64_t grain = kWaves * kStep, G = Hq / heads, rows = B * G, u = heads * ceil_div(G, 16);
+    const int64_t even = most(1, least(kMaxRanges, ceil_div(max_len, 4096)));
+    int64_t own = least(B * even, most(B, kMaxBlocks / u));
+    if (u < kCus)
+        own = most(own, 2 * kCus / u + least(B, (kCus - 1) / u));
+    own = least(own, B * ceil_div(max_len, grain)) * Hq;
+    const int64_t narrow = D == 256 ? 16 : 32;          // rows of a prefix unit's wave
+    int64_t prefix = (format == NM_KV_MX4 ? 2 * kCus : kCus) * least(rows, narrow);
+    if (rows > narrow && D != 256)
+        prefix = most(prefix, 2 * kCus * least(rows, 4 * narrow));
+    if (rows > narrow)
+        prefix = most(prefix, kCus * least(rows, 8 * narrow));
+    prefix = least(prefix + rows * heads, rows * heads * ceil_div(prefix_len, grain));
+    return (prefix + own) * (D + 2) * 4;
+}
+
 }  // namespace nma
 
 namespace nmk {

@@ -71,13 +71,11 @@ void cache_bufs(const nm_kv_cache& c, Buf* out)
     out[3] = {c.v_scale, s};
 }
 
-int64_t attn_shape(int64_t B, int Hq, int heads, int D, int format, int64_t prefix_len, int64_t max_len)
+bool attn_shape_ok(int64_t B, int Hq, int heads, int D, int format, int64_t prefix_len, int64_t max_len)
 {
-    if (B < 1 || B > 65535 || Hq < 1 || Hq > 65535 || heads < 1 || heads > 65535 || Hq % heads != 0 ||
-        B * Hq >= nma::kMaxRows || (D != 64 && D != 128 && D != 256) || format < NM_KV_16 || format > NM_KV_MX4 || prefix_len < 0 || prefix_len > nma::kMaxTokens ||
-        max_len < 0 || max_len > nma::kMaxTokens)
-        return -1;
-    return nma::attn_workspace(nma::attn_plan(B, Hq, heads, D, format, prefix_len, max_len), D);
+    return B >= 1 && B <= 65535 && Hq >= 1 && Hq <= 65535 && heads >= 1 && heads <= 65535 && Hq % heads == 0 &&
+           B * Hq < nma::kMaxRows && (D == 64 || D == 128 || D == 256) && format >= NM_KV_16 && format <= NM_KV_MX4 &&
+           prefix_len >= 0 && prefix_len <= nma::kMaxTokens && max_len >= 0 && max_len <= nma::kMaxTokens;
 }
 
 }  // namespace
@@ -180,7 +178,9 @@ int nm_kv_read(const nm_kv_cache* cache, const int64_t* slots, int64_t T, void* 
 
 int64_t nm_attn_workspace_bytes(int64_t B, int Hq, int heads, int D, int format, int64_t prefix_len, int64_t max_len)
 {
-    return attn_shape(B, Hq, heads, D, format, prefix_len, max_len);
+    return attn_shape_ok(B, Hq, heads, D, format, prefix_len, max_len)
+               ? nma::attn_workspace_bound(B, Hq, heads, D, format, prefix_len, max_len)
+               : -1;
 }
 
 int nm_attn_decode(const void* q, int64_t q_stride, int64_t B, int Hq, const nm_kv_cache* cache,
@@ -191,10 +191,12 @@ int nm_attn_decode(const void* q, int64_t q_stride, int64_t B, int Hq, const nm_
     int st = check_cache(cache);
     if (st != NM_OK)
         return st;
-    const int64_t need = attn_shape(B, Hq, cache->heads, cache->D, cache->format, prefix_len, max_len);
     const int64_t width = (int64_t)Hq * cache->D;
-    if (need < 0 || !stride_ok(B, q_stride, width) || !(std::fabs(scale) <= 1e30f))
+    if (!attn_shape_ok(B, Hq, cache->heads, cache->D, cache->format, prefix_len, max_len) || !stride_ok(B, q_stride, width) ||
+        !(std::fabs(scale) <= 1e30f))
         return NM_ERR_BAD_SHAPE;
+    const nma::AttnPlan plan = nma::attn_plan(B, Hq, cache->heads, cache->D, cache->format, prefix_len, max_len);
+    const int64_t need = nma::attn_workspace(plan, cache->D);
     const int64_t own_pages = nma::ceil_div(max_len, cache->page_size);
     if (max_len > 0 && B > 1 && (table_stride < own_pages || table_stride > kMaxStride))
         return NM_ERR_BAD_SHAPE;
@@ -214,9 +216,8 @@ int nm_attn_decode(const void* q, int64_t q_stride, int64_t B, int Hq, const nm_
         return NM_ERR_INVALID_ARG;
     if (!disjoint(outs, 3, ins, 8))
         return NM_ERR_INVALID_ARG;
-    return nmk::attn_decode(nma::attn_plan(B, Hq, cache->heads, cache->D, cache->format, prefix_len, max_len), q, q_stride, B, Hq,
-                            *cache, prefix_pages, prefix_len, page_table, table_stride, lens, max_len, scale, o, lse,
-                            workspace, stream);
+    return nmk::attn_decode(plan, q, q_stride, B, Hq, *cache, prefix_pages, prefix_len, page_table, table_stride, lens,
+                            max_len, scale, o, lse, workspace, stream);
 }
 
 }  // extern "C"
