@@ -18,3 +18,56 @@ def test_one_workspace_for_every_smaller_call(nm, fmt):  # noqa: F811
         kw = dict(max_len=max_len, prefix_pages=b.prefix_pages, prefix_len=P)
         o = nm.attn_decode(b.q[:n], b.cache, b.table[:n], every[:n], ws=ws, **kw)
         assert same(o, nm.attn_decode(b.q[:n], b.cache, b.table[:n], every[:n], **kw)), (n, max_len, P)
+
+
+def ask(b):
+    lse = torch.full(b.q.shape[:2], 7.0, device="cuda")
+    o = torch.full_like(b.q, 3.0)
+    b.run(out=o, lse=lse)
+    b.check(o, lse)
+    assert same(o, b.run(out=torch.full_like(b.q, 3.0)))
+    for i, n in enumerate(b.lens):
+        if n < 0:
+            assert (o[i] == 3.0).all() and (lse[i] == 7.0).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", (F16, BF16))
+@pytest.mark.parametrize("D,G,heads,P,lens", ((128, 17, 1, 300, [1500, 40]), (128, 20, 2, 0, [1500, 40]), (64, 33, 1, 300, [1500, 0, 40]),
+                                              (64, 20, 1, 0, [700, -1, 1500]), (256, 17, 2, 130, [600, 40]), (256, 40, 1, 0, [40, 900])))
+def test_many_query_heads_in_several_ranges(nm, dtype, fmt, D, G, heads, P, lens):  # noqa: F811
+    """More than 16 query heads a key head, whose rows lie in row groups of 16 that tiles of the joining launch cross,
+    with own tokens in several ranges."""
+    ask(Batch(nm, dtype, fmt, D, G * heads, heads, 16, P, lens))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", (F16, BF16))
+@pytest.mark.parametrize("D", (64, 128))
+@pytest.mark.parametrize("B,G", ((5, 4), (8, 4), (1, 20), (1, 32), (17, 1)))
+@pytest.mark.parametrize("P", (1, 1500))
+def test_two_row_tiles_behind_a_prefix(nm, dtype, fmt, D, B, G, P):  # noqa: F811
+    """17 to 32 rows of a key head: prefix units of two row tiles a wave that read the cache themselves, the second
+    tile whole or in part; one range and several; own tokens beside them, a padding row."""
+    lens = [(11 * b + P) % 45 for b in range(B)]
+    if B > 1:
+        lens[1] = -1
+    ask(Batch(nm, dtype, fmt, D, 2 * G, 2, 32, P, lens))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", (F16, BF16))
+@pytest.mark.parametrize("D,B,G,heads", ((128, 12, 4, 1), (64, 12, 4, 1), (128, 10, 16, 1), (64, 20, 8, 2), (256, 12, 4, 1)))
+def test_staged_prefix_beside_long_own_tokens(nm, dtype, fmt, D, B, G, heads):  # noqa: F811
+    """48 and 160 rows of a key head (prefix units of four and eight waves), own tokens in several ranges."""
+    lens = ([1500, 3, 0, -1, 700, 129] + [64] * B)[:B]
+    ask(Batch(nm, dtype, fmt, D, G * heads, heads, 64, 1500, lens))
+
+
+@pytest.mark.parametrize("fmt,dtype", (("16", BF16), ("mx8", F16), ("mx4", BF16)))
+@pytest.mark.parametrize("D,heads,G,P,lens", ((64, 1, 4, 0, [20000]), (64, 1, 2, 14000, [9000]), (64, 1, 4, 20000, [300, 0, -1]),
+                                              (128, 4, 8, 2500, [1, 0] * 16)))
+def test_more_parts_than_one_turn_joins(nm, dtype, fmt, D, heads, G, P, lens):  # noqa: F811
+    """A row with more parts than the joining launch takes at a time: over 64 with 16 waves (few key heads), over 16
+    with 4 (many row tiles)."""
+    ask(Batch(nm, dtype, fmt, D, G * heads, heads, 256, P, lens))
