@@ -918,8 +918,10 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, int unit, uint8
 // One launch for all units: the first prefix_blocks blocks take prefix units, staged
 // with W waves or (W = 0) like own tokens, the others own-token units = (range, row
 // group, sequence, key head).  Two waves a SIMD: with more than 256 registers to
-// spend the compiler keeps sums in accumulation registers and moves them to and fro
-// (and was seen to reuse a register of an operand too early doing so).
+// spend the compiler keeps sums in accumulation registers and moves them to and fro, a
+// thousand moves beside 64 products (tests/test_attn_registers.py holds the build to none).
+// That costs time only: in such a build, too, what reaches each operand of a product is its
+// own load, conversion or mask and nothing else, by the assembly of all these kernels.
 template <int DT, int BITS, int D, int MT, int W>
 __global__ __launch_bounds__((W ? W : nma::kWaves) * 64, 2) void units_kernel(const AttnArgs A, int prefix_blocks, int blocks, int direct)
 {
