@@ -259,11 +259,20 @@ def attn_workspace(B, heads_q, cache, max_len, prefix_len=0):
     max_len and prefix_len, on the cache's device (any contents; calls that may
     run at the same time need one each)."""
     c = _cache(cache)
-    nbytes = attn_lib().nm_attn_workspace_bytes(B, heads_q, c.heads, c.D, c._format, prefix_len, max_len)
+    nbytes = 0 if B == 0 else attn_lib().nm_attn_workspace_bytes(B, heads_q, c.heads, c.D, c._format, prefix_len, max_len)
     if nbytes < 0:
         raise ValueError(f"no such attention: {B} sequences, {heads_q} query heads on {c.heads}, {prefix_len} + "
                          f"{max_len} tokens")
     return torch.empty(nbytes, dtype=torch.uint8, device=c.device)
+
+
+def _no_sequences(q, c, max_len, prefix_len, out):
+    """attn_decode of an empty batch: what the arguments alone can refuse, and an empty result."""
+    attn_workspace(1, q.shape[1], c, max_len, prefix_len)
+    if out is None:
+        return torch.empty_like(q)
+    _check(out, "out", c._index, c.dtype, q.shape)
+    return out
 
 
 def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, prefix_len=0, scale=None, out=None,
@@ -275,7 +284,8 @@ def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, pre
     [B][pages]); lens[b] < 0 marks a padding row, which is left as it was.
     scale defaults to 1/sqrt(D); max_len to the table's width.  Returns out
     [B][Hq][D]; ``lse`` (float32 [B][Hq]) receives the log of the softmax's
-    sum.  ``ws``: an attn_workspace(), or None to allocate one."""
+    sum.  ``ws``: an attn_workspace(), or None to allocate one.  A batch of no
+    sequences gives an empty result."""
     c = _cache(cache)
     dev, dt = c._index, c.dtype
     B, hq, _ = _size(q, "q", 3)
@@ -307,6 +317,8 @@ def attn_decode(q, cache, page_table, lens, max_len=None, prefix_pages=None, pre
     if ws is not None:
         nbytes, = _size(ws, "ws", 1)
         wsp = _check(ws, "ws", dev, torch.uint8, (nbytes,))
+    if B == 0:                                        # no sequence: nothing to launch
+        return _no_sequences(q, c, max_len, prefix_len, out)
     other = _other(dev, stream)
     try:
         if out is None:

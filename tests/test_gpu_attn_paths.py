@@ -71,3 +71,20 @@ def test_more_parts_than_one_turn_joins(nm, dtype, fmt, D, heads, G, P, lens):  
     """A row with more parts than the joining launch takes at a time: over 64 with 16 waves (few key heads), over 16
     with 4 (many row tiles)."""
     ask(Batch(nm, dtype, fmt, D, G * heads, heads, 256, P, lens))
+
+
+def test_no_sequences(nm):  # noqa: F811
+    """An empty batch gives an empty result, as rows of none do in the other calls; wrong arguments are refused all
+    the same."""
+    cache = nm.KVCache(4, 16, 2, 64, F16, "mx8")
+    q, lens = torch.empty((0, 8, 64), dtype=F16, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    table, pages = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((0, 3), (2,)))
+    o = nm.attn_decode(q, cache, table, lens, prefix_pages=pages, prefix_len=20)
+    assert o.shape == (0, 8, 64) and o.dtype == F16 and o.is_cuda
+    out, lse = torch.empty_like(q), torch.empty((0, 8), device="cuda")
+    ws = nm.attn_workspace(0, 8, cache, 48, 20)
+    assert nm.attn_decode(q, cache, None, lens, out=out, lse=lse, ws=ws, stream=torch.cuda.Stream()) is out
+    for bad in (lambda: nm.attn_decode(q[:, :7], cache, table, lens), lambda: nm.attn_decode(q, cache, table, lens, max_len=49),
+                lambda: nm.attn_decode(q, cache, table, lens, out=torch.empty((0, 4, 64), dtype=F16, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
