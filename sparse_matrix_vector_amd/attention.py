@@ -107,6 +107,16 @@ def _load():
     return _lib
 
 
+def _fit(*sizes):
+    """Whether sizes are those of a C call's arguments: ctypes would cut others to their low bits."""
+    return all(0 <= n < 2 ** 31 for n in sizes)
+
+
+def _rot(pairs):
+    """Columns that so many frequencies turn, as a C int (more than any head has where they do not fit)."""
+    return 2 * min(pairs, 2 ** 30 - 1)
+
+
 def _empty(like, stride):
     """A new contiguous tensor of the shape, dtype and device of the rows `like`,
     whose row stride _rows() found to be `stride`."""
@@ -142,7 +152,7 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, eps=1e-6, interlea
             oqp = _check(out[0], "out[0]", dev, dt, shape)
             okp = _check(out[1], "out[1]", dev, dt, (T, hk, D))
         st = (_lib or _load()).nm_qk_norm_rope(qp, qs, kp, ks, T, hq, hk, D, code, wqp, wkp, eps, pos, freq,
-                                               2 * pairs, 1 if interleaved else 0, oqp, okp, _stream(dev))
+                                               _rot(pairs), 1 if interleaved else 0, oqp, okp, _stream(dev))
     finally:
         if other is not None:
             other.close()
@@ -163,8 +173,8 @@ class KVCache:
         if format not in _FORMATS:
             raise ValueError(f"format must be one of {', '.join(_FORMATS)}, not {format}")
         code, fmt = _dtype(dtype), _FORMATS[format]
-        # (ctypes would cut a larger integer to its low bits)
-        nbytes = -1 if max(n_pages, page_size, heads, D) >= 2 ** 31 else attn_lib().nm_kv_bytes(n_pages, page_size, heads, D, fmt)
+        sizes = (n_pages, page_size, heads, D)
+        nbytes = attn_lib().nm_kv_bytes(*sizes, fmt) if _fit(*sizes) else -1
         if nbytes < 0:
             raise ValueError(f"no cache of {n_pages} pages of {page_size} tokens, {heads} heads, {D} columns")
         sbytes = attn_lib().nm_kv_scale_bytes(n_pages, page_size, heads, D, fmt)
@@ -259,7 +269,10 @@ def attn_workspace(B, heads_q, cache, max_len, prefix_len=0):
     max_len and prefix_len, on the cache's device (any contents; calls that may
     run at the same time need one each)."""
     c = _cache(cache)
-    nbytes = 0 if B == 0 else attn_lib().nm_attn_workspace_bytes(B, heads_q, c.heads, c.D, c._format, prefix_len, max_len)
+    nbytes = 0
+    if B != 0:
+        nbytes = attn_lib().nm_attn_workspace_bytes(B, heads_q, c.heads, c.D, c._format, prefix_len, max_len) \
+            if _fit(B, heads_q, max_len, prefix_len) else -1
     if nbytes < 0:
         raise ValueError(f"no such attention: {B} sequences, {heads_q} query heads on {c.heads}, {prefix_len} + "
                          f"{max_len} tokens")
