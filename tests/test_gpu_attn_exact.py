@@ -110,6 +110,7 @@ def test_bfloat16_values_near_the_ends(nm, fmt, size, hq, heads, P, lens):  # no
     """Values up to 6 2^121 with scores that climb from 0 over 0.9 to 7 (base 2) in the last tokens: weights above one
     would take the sums past fp32, weights of at most one, 2^-8 for the first tokens, keep them below 2^127.  And
     values down to the type's least normal ones."""
+    b = Batch(nm, BF16, fmt, 128, hq, heads, 16, P, lens)
     b.q = torch.zeros_like(b.q)
     b.q[..., 0] = 1.0
     k = torch.zeros_like(b.k)
