@@ -114,7 +114,8 @@ int nm_kv_write(const nm_kv_cache* cache, const void* k, int64_t k_stride, const
  * nm_kv_read -- k and v [T][heads][D] (contiguous, 16-byte aligned) from slots
  * slots[t] (any order, repeats allowed); zeros for a slot outside the cache.
  * Quantised values are rounded to the cache's dtype, to nearest even,
- * saturating at its largest finite value.
+ * saturating at its largest finite value.  (The least e of an fp16 cache costs
+ * 2^-24 of a value at most.)
  */
 int nm_kv_read(const nm_kv_cache* cache, const int64_t* slots, int64_t T, void* k, void* v, void* stream);
 
@@ -131,6 +132,9 @@ int nm_kv_read(const nm_kv_cache* cache, const int64_t* slots, int64_t T, void* 
  *   lens [B] int32     tokens of b behind the prefix, at most max_len (a larger
  *                      one counts as max_len).  Negative: b is a padding row;
  *                      its rows of o and lse are left as they are.
+ *   max_len            the work is cut into ranges by it, since lens is on the
+ *                      device: one far above the lengths leaves most of the GPU
+ *                      without tokens.
  *   o [B][Hq][D]       contiguous, 16-byte aligned; a sequence without a token
  *                      to see gets zeros.
  *   lse [B][Hq]        fp32 (natural log of the softmax's sum; -inf without a
@@ -139,6 +143,8 @@ int nm_kv_read(const nm_kv_cache* cache, const int64_t* slots, int64_t T, void* 
  *                      256-byte aligned, any contents; may be NULL when that is 0.
  *                      So many bytes also serve every call with the same Hq,
  *                      heads, D and format and no larger B, prefix_len and max_len.
+ * Several query tokens of a sequence (a draft, a piece of a prompt) are a batch
+ * row each, with the same pages and a length that ends at the token.
  * A page number outside the cache is not followed: its tokens count as absent.
  * Scores, softmax statistics and sums are fp32; the weights of the sum go into
  * the matrix cores as two operands of dtype each (2^-16 of a weight is lost in

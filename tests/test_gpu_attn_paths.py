@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import attn_reference as ref
 from test_gpu_attn import BF16, F16, FORMATS, Batch, nm, same  # noqa: F401  (nm: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +89,19 @@ def test_no_sequences(nm):  # noqa: F811
                 lambda: nm.attn_decode(q, cache, table, lens, out=torch.empty((0, 4, 64), dtype=F16, device="cuda"))):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("fmt,dtype", (("16", F16), ("mx8", BF16), ("mx4", F16)))
+@pytest.mark.parametrize("P", (0, 100))
+def test_several_tokens_of_a_sequence(nm, fmt, dtype, P):  # noqa: F811
+    """Several query tokens of a sequence at once (a draft, or a prompt's piece): a batch row each, with the sequence's
+    pages and a length that ends at the token itself.  Each row sees what a row of its own batch would."""
+    b = Batch(nm, dtype, fmt, 128, 8, 2, 16, P, [70, 1, 33])
+    rows = torch.tensor([0, 0, 0, 0, 1, 2, 2], device="cuda")
+    lens = torch.tensor([67, 68, 69, 70, 1, 32, 33], dtype=torch.int32, device="cuda")
+    q = b.q[rows] + torch.arange(7, device="cuda").view(7, 1, 1).to(dtype) / 8
+    o = nm.attn_decode(q, b.cache, b.table[rows], lens, prefix_pages=b.prefix_pages, prefix_len=P)
+    for i, (r, n) in enumerate(zip(rows.tolist(), lens.tolist())):
+        t = b.tokens(r)[:P + n]
+        want, _, tol, _ = ref.attend(ref.f64(q[i]), b.qk[t], b.qv[t], 128 ** -0.5, dtype)
+        assert (abs(ref.f64(o[i]) - want) <= tol).all(), i
