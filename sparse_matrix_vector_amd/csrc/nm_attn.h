@@ -64,7 +64,8 @@ constexpr int v_scale_offset(int token, int block) { return block * kTile + toke
 // large value may be rounded, and at multiples of 2^-24.  So an fp16 cache's operands
 // are half its values (bias 126, made good in the scores' scale and in the output),
 // and its e stays where the smallest codes, 2^-9 (e4m3) and 2^-1 (e2m1), do not fall
-// below 2^-23.  255 marks a block that held a NaN or an infinity.
+// below 2^-23: values are off by 2^-24 at most for that, one step of fp16's own least
+// numbers.  255 marks a block that held a NaN or an infinity.
 constexpr int scale_bias(int dtype) { return dtype == NM_FP16 ? 126 : 127; }
 constexpr int least_exponent(int dtype, int bits) { return dtype == NM_BF16 ? -126 : bits == 8 ? -14 : -22; }
 
@@ -140,13 +141,17 @@ inline AttnPlan attn_plan(int64_t B, int Hq, int heads, int D, int format, int64
     // Prefix units of eight waves have a CU to themselves, and the matrix cores limit
     // them; own-token units are limited by HBM.  So they share the GPU side by side,
     // the prefix taking as many CUs as its share of the work: a token of a key head
-    // takes a staged block 52 units of time (at D = 128), an own-token block 22 (16-bit;
-    // by its bytes), of which two thirds, since the batch is rarely full to max_len.
-    // 32 sequences of 64 heads, 16-bit, 32741 tokens + up to 1024: 256 blocks 81.5 us, 192
-    // 78.0, 160 79.2; 8192 + up to 1024: 47.9 / 45.0 / 39.8; MX8, 32768 + up to 4096: 96.0 /
-    // 94.7 / 83.1; 32768 alone: 68.4 / 71.7 / 77.4.  Short own tokens have an eighth of the
-    // CUs left to them all the same, or they would wait for the prefix (16-bit, 16 own
-    // tokens, 256 / 224 blocks: 4096 + 28.0 / 22.4, 8192 + 32.9 / 28.6, 32768 + 58.3 / 59.0).
+    // counts 52 in a staged block and 22 in an own-token block (16-bit; by its bytes), of
+    // which two thirds, since the batch is rarely full to max_len.  (52 was a staged block's
+    // time before weights had a second operand; 65, its time since, gives the prefix more
+    // CUs and is slower, 52 / 65: 32741 + up to 1024 below 73.8 / 78.6, MX8, 32768 + up to
+    // 4096 85.1 / 95.3, 16384 + up to 1024 48.2 / 53.1, but 8192 + up to 2048 39.6 / 35.9.)
+    // 32 sequences of 64 heads on 8 of 128 columns, us for 256 / 192 / 160 prefix blocks:
+    // 16-bit, 32741 tokens + up to 1024 82.7 / 75.2 / 82.3, 8192 + up to 1024 49.4 / 45.3 /
+    // 39.6; MX8, 32768 + up to 4096 100.4 / 99.0 / 85.3; 32768 alone 68.7 / 74.6 / 81.8.
+    // Short own tokens have an eighth of the CUs left to them all the same, or they would
+    // wait for the prefix (16-bit, 16 own tokens, 256 / 224 blocks: 4096 + 29.7 / 24.7,
+    // 8192 + 35.0 / 31.7, 32768 + 67.5 / 69.6).
     const double staged = 52.0 * (double)(prefix_len * heads * p.prefix_groups);
     const double own = 22.0 * 2 / 3 * format_bits(format) / 16 * (double)(B * heads * p.own_groups) * (double)max_len;
     int64_t cus = kCus;
@@ -158,12 +163,13 @@ inline AttnPlan attn_plan(int64_t B, int Hq, int heads, int D, int format, int64
     // Smaller prefix units: one block a CU, since every further range of a row costs its
     // partial sums' way to memory and back; but two where ranges are long all the same,
     // a block alone does not keep its CU busy (staged by four waves, or 4-bit) and few
-    // own tokens want the room.  us with one / two, 8 key heads of 128 columns: 64 rows,
-    // MX8, 8192 tokens 17.8 / 19.7, 16384 24.4 / 24.2, 32768 37.5 / 31.8; 128 rows, 16-bit,
-    // 8192 21.1 / 26.6, 32768 42.6 / 45.1, 65536 70.9 / 67.2; 32 rows, MX8, 32768 20.7 /
-    // 23.9; 16 rows, MX4, 8192 10.9 / 11.6, 32768 16.9 / 15.1, MX8, 131072 50.1 / 51.8.
-    // With up to 2048 own tokens: 64 rows, MX8, 32768 38.6 / 37.4, 65536 66.7 / 54.4; 128
-    // rows, MX8, 32768 42.9 / 46.3, 65536 73.3 / 68.3; 16 rows, MX4, 32768 15.9 / 18.4.
+    // own tokens want the room.  us with one / two, 8 key heads of 128 columns (other widths
+    // and head counts go by the same rule, unmeasured): 64 rows, MX8, 8192 tokens 18.9 /
+    // 20.4, 16384 27.2 / 26.2, 32768 42.6 / 36.0; 128 rows, 16-bit, 8192 22.3 / 27.9, 32768
+    // 49.4 / 46.8, 65536 82.6 / 71.1; 32 rows, MX8, 32768 21.9 / 24.3; 16 rows, MX4, 8192
+    // 11.0 / 11.7, 32768 17.4 / 15.8, MX8, 131072 50.2 / 51.6.  With up to 2048 own tokens:
+    // 64 rows, MX8, 32768 44.4 / 42.0, 65536 77.5 / 62.2; 128 rows, MX8, 32768 48.5 / 50.9,
+    // 65536 81.6 / 76.3; 16 rows, MX4, 32768 17.8 / 16.8.
     const int64_t prefix_units = heads * p.prefix_groups, longish = format == NM_KV_16 ? 1024 : 512;
     const bool two = (p.waves == 4 || format == NM_KV_MX4) && prefix_len * prefix_units >= longish * 2 * kCus &&
                      max_len * 32 <= prefix_len;

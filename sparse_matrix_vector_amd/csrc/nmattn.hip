@@ -22,9 +22,9 @@
 // Own tokens are bound by HBM: 32 sequences of 4096 tokens, 8 key heads of 128
 // columns, MX8, take 45.5 us, 6.1 TB/s; with few or very different sequences the
 // start of the blocks and the joining of ranges show (16 of 0 .. 8192: 29 + 4 us, 5.1
-// TB/s; one of 131071, MX4: 25 + 4, 5.8).  A shared prefix is bound by the matrix
-// cores' and vector units' power at 256 rows (131072 tokens: 165 to 199 us as the
-// clock allows, 690 to 830 TFLOP/s, on random values, 154 us on zeros) and by HBM below.
+// TB/s; one of 131071, MX4: 27 + 4, 5.2).  A shared prefix of many rows is bound by the
+// matrix cores and the vector instructions beside them (attend_staged), one of few rows
+// by HBM.
 
 #include <hip/hip_runtime.h>
 
@@ -355,7 +355,8 @@ struct Weights {
     // that score, so that the largest weight lies between 2^kBelow and 2^kRoom.
     //   It may lag, so that in long ranges the sums are hardly ever multiplied: 32 sequences
     // of 64 heads behind 32768 tokens, 16-bit: 67.5 us with the maximum itself, 63.7 with
-    // it up to 2^8 behind; MX8 and 4096 own tokens 82.6 / 78.6.  In fp16 it stays below:
+    // it up to 2^8 behind; MX8 and 4096 own tokens 82.6 / 78.6 (both with a weight's first
+    // operand alone).  In fp16 it stays below:
     // the operands' range then ends at 2^-32 of the largest weight, not at 2^-25, where
     // the tokens behind a first one that takes most of the weight would be lost; 2^15 is
     // the last power of two that fits (65504).  bfloat16 has fp32's range, and values near
@@ -775,6 +776,12 @@ struct Stage {
 
 // Unit `unit` = (row group, range, key head); lds: two buffers and two counts of
 // each tile's tokens (staged_bytes).
+//   256 rows, 131072 tokens, 16-bit: 207 us at 2.1 GHz, 660 TFLOP/s of the formula.  A wave
+// and step has 96 products (a third of them for the weights' second operands) and 234
+// vector instructions, 32 of them exponentials; at 16, 4 and 16 cycles these are 1536 and
+// 1320 of the 3380 cycles that it takes.  So the matrix cores are busy 45% of the time: the
+// two waves of a SIMD leave each barrier together, and one's products hide little of the
+// other's vector work.  On zeros, where the card's power does not count, 198 us for 222.
 template <int BITS, int D, int W>
 constexpr int staged_bytes()
 {
@@ -920,8 +927,9 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, int unit, uint8
 // group, sequence, key head).  Two waves a SIMD: with more than 256 registers to
 // spend the compiler keeps sums in accumulation registers and moves them to and fro, a
 // thousand moves beside 64 products (tests/test_attn_registers.py holds the build to none).
-// That costs time only: in such a build, too, what reaches each operand of a product is its
-// own load, conversion or mask and nothing else, by the assembly of all these kernels.
+// That costs time only: in such a build, too, what reaches each key and value operand of a
+// product is its own loads, conversions and masks and nothing else, by the assembly of all
+// these kernels.
 template <int DT, int BITS, int D, int MT, int W>
 __global__ __launch_bounds__((W ? W : nma::kWaves) * 64, 2) void units_kernel(const AttnArgs A, int prefix_blocks, int blocks, int direct)
 {
@@ -969,9 +977,9 @@ __global__ __launch_bounds__((W ? W : nma::kWaves) * 64, 2) void units_kernel(co
 // + g) of one key head, a lane (kg, m) row m as in the partial results.  NW waves
 // share the parts, each keeps a reference and sums of its own as the units do, and
 // they meet in LDS.  A wave loads four parts at a time, with the next four on their
-// way, and the first four before the sequence's length is known (32 sequences of 32
-// heads behind 8192 tokens: 28.4 us with the maxima looked at first, 27.1 this way;
-// one sequence of 131071, MX4: 32.0 / 31.5).
+// way, and the first four before the sequence's length is known (units and join of 32
+// sequences of 32 heads behind 8192 tokens, when this was measured: 28.4 us with the
+// maxima looked at first, 27.1 this way; one sequence of 131071, MX4: 32.0 / 31.5).
 template <int DT, int D, int NW>
 __global__ __launch_bounds__(NW * 64) void combine_kernel(const AttnArgs A)
 {

@@ -41,7 +41,8 @@ struct QkArgs {
 // row's heads hb, hb + blocks_per_row, ... in groups of 256 / LPH.  The row's
 // sines and cosines are computed once per block and kept in LDS; a thread's next
 // load is always in flight (16384 rows of 64 + 8 heads, 604 MB: 172 us with each
-// load waited for at once, 121 with the next one started first).
+// load waited for at once, 125 with the next one started first, 115 to 121 with the
+// rows non-temporal as well; a non-temporal copy of as many bytes takes 100).
 //   y = n cos -+ n' sin  with n' the pair's other column: the same thread's for
 // neighbouring pairs, the one rot / 16 lanes away for pairs (i, i + rot / 2).
 template <int DT, int LPH, bool INTERLEAVED, bool ONCE>
@@ -233,13 +234,14 @@ __device__ __forceinline__ int scale_byte(float top)
 // cache line on the rows' side, and on the cache's side eight tokens of a tile
 // make up whole lines.  32768 rows of 8 x 128 in MX8, write / read of 65536 back:
 // 4 rows x 128 columns 51 / 85 us, 8 x 64 48 / 81, 16 x 32 51 / 94 (a thread a
-// unit with 64-bit divisions, before: 63 / 128; all by one unit a wave); the card
-// copies at 4.9 TB/s, which would take 41 / 82.
+// unit with 64-bit divisions, before: 63 / 128; all by one unit a wave).
 // The rows are touched once, so they are loaded and stored non-temporally and the caches
 // are left to the codes' pieces (us; written rows just produced / long ago, 32768 rows,
 // 16-bit: 52.0 / 69.5 without, 52.0 / 58.4 with; MX8 41.7 / 56.1, 38.6 / 44.2; MX4 31.3 /
 // 49.6, 32.4 / 39.5; 4096 rows, MX8: 10.2 / 13.2, 11.0 / 7.6; 65536 rows read back, MX8 77 ->
 // 62, MX4 68 -> 51, 16-bit 105).
+// With all of it, write / read back in a kernel trace: MX8 39 / 61 to 72, MX4 38 / 50 (a
+// non-temporal copy of as many bytes: 34 / 67, 28 / 56).
 constexpr int kRows = 8, kCols = 64;
 
 // Units of a wave that reads codes back: two, eight rows apart, their loads in flight
