@@ -325,25 +325,24 @@ __device__ __forceinline__ void mask_scores(f32x4 (&sc)[MT][NT], const int (&n)[
 }
 
 // What a dword of two 16-bit floats, `whole`, leaves out of the fp32 a and b that were
-// rounded to it, as another such dword.  The differences are exact.  In fp16 the empty
-// statement keeps the compiler from rounding a and b a second time.  In bfloat16 a
-// difference is one dot product with (-1, 0) or (0, -1); these come from scalar
-// registers, since of the constants the compiler makes the first the instruction's
-// inline -1.0, which the hardware takes for (0, -1).
+// rounded to it, as another such dword.  The differences are exact, each one dot product
+// of two 16-bit floats with (-1, 0) or (0, -1).  These come from scalar registers: of
+// bfloat16 constants the compiler makes the first the instruction's inline -1.0, which
+// the hardware takes for (0, -1).
 template <int DT>
 __device__ __forceinline__ uint32_t left_out(uint32_t whole, float a, float b)
 {
-    if constexpr (DT == NM_FP16) {
-        asm("" : "+v"(whole));
-        const f32x2 w = unpack2<DT>(whole);
-        return pack2<DT>(a - w.x, b - w.y);
-    } else {
-        uint32_t low = 0x0000BF80u, high = 0xBF800000u;
-        asm("" : "+s"(low), "+s"(high));
-        const bf16x2 w = __builtin_bit_cast(bf16x2, whole);
-        return pack2<DT>(__builtin_amdgcn_fdot2_f32_bf16(w, __builtin_bit_cast(bf16x2, low), a, false),
-                         __builtin_amdgcn_fdot2_f32_bf16(w, __builtin_bit_cast(bf16x2, high), b, false));
-    }
+    constexpr uint32_t kMinusOne = DT == NM_FP16 ? 0xBC00u : 0xBF80u;
+    uint32_t low = kMinusOne, high = kMinusOne << 16;
+    asm("" : "+s"(low), "+s"(high));
+    const auto minus = [&](uint32_t which, float x) {
+        if constexpr (DT == NM_FP16)
+            return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, whole), __builtin_bit_cast(f16x2, which), x, false);
+        else
+            return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, whole), __builtin_bit_cast(bf16x2, which), x,
+                                                   false);
+    };
+    return pack2<DT>(minus(low, a), minus(high, b));
 }
 
 // The softmax weights of a step of NT tiles, in place of its scores; updates the rows'
@@ -356,11 +355,12 @@ struct Weights {
     //   It may lag, so that in long ranges the sums are hardly ever multiplied: 32 sequences
     // of 64 heads behind 32768 tokens, 16-bit: 67.5 us with the maximum itself, 63.7 with
     // it up to 2^8 behind; MX8 and 4096 own tokens 82.6 / 78.6 (both with a weight's first
-    // operand alone).  In fp16 it stays below:
-    // the operands' range then ends at 2^-32 of the largest weight, not at 2^-25, where
-    // the tokens behind a first one that takes most of the weight would be lost; 2^15 is
-    // the last power of two that fits (65504).  bfloat16 has fp32's range, and values near
-    // its end: the reference stays above, and no value is added more than once.
+    // operand alone).
+    //   In fp16 it stays below: the operands' range then ends at 2^-32 of the largest weight,
+    // not at 2^-25, where the tokens behind a first one that takes most of the weight would
+    // be lost; 2^15 is the last power of two that fits (65504).  bfloat16 has fp32's range,
+    // and values near its end: the reference stays above, and no value is added more than
+    // once.
     static constexpr float kBelow = DT == NM_FP16 ? 7.0f : -8.0f;
     static constexpr float kRoom = DT == NM_FP16 ? 15.0f : 0.0f;
 
