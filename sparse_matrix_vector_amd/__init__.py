@@ -20,6 +20,13 @@ and, between a decode layer's q+k+v and o projections (``include/nmattn.h``):
     cache = KVCache(n_pages, 64, heads, 128, torch.bfloat16, "mx8")
     kv_write(cache, k, v, slots)                   # quantised as it is written
     o = attn_decode(q, cache, page_table, lens)    # optionally behind a prefix shared by the batch
+
+and around that step (``include/nmserve.h``):
+
+    pages = KVPages(sequences, width, n_pages, 64) # who has which pages of a cache
+    starts, slots, positions, _ = kv_plan(pages, adds, rows)
+    o = attn_prompt(q, k, v, starts)               # causal attention over packed prompts
+    o = attn_tree(q, cache, pages.table, pages.lens, visible)      # a tree of drafted tokens a sequence
 """
 import ctypes
 
@@ -31,7 +38,8 @@ from ._lib import (NM_BF16, NM_ERR_BAD_MASK, NM_ERR_BAD_SHAPE, NM_ERR_HIP, NM_ER
 __all__ = ["pack", "spmv", "spmv_multi", "spmv_swiglu", "gemv_dense", "gemv_dense_multi", "gemv_dense_swiglu",
            "calib_accumulate", "calib_keep_mask", "hybrid_row_loss", "hybrid_select_rows", "hybrid_pack", "spmv_hybrid",
            "Hybrid", "NmError", "dtype_code", "stream_handle", "workspace", "qk_norm_rope", "KVCache", "kv_write",
-           "kv_read", "attn_decode", "attn_workspace"]
+           "kv_read", "attn_decode", "attn_workspace", "attn_prompt", "attn_prompt_workspace", "KVPages",
+           "kv_plan", "attn_tree", "attn_tree_workspace"]
 
 _DT = {torch.float16: NM_FP16, torch.bfloat16: NM_BF16}
 
@@ -351,3 +359,5 @@ def spmv_hybrid(hyb, x, out=None, stream=None):
 
 
 from .attention import KVCache, attn_decode, attn_workspace, kv_read, kv_write, qk_norm_rope  # noqa: E402
+from .serving import (KVPages, attn_prompt, attn_prompt_workspace, attn_tree, attn_tree_workspace,  # noqa: E402
+                      kv_plan)

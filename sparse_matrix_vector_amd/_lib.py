@@ -51,6 +51,17 @@ ATTN_SIGNATURES = {
                             _P]),
 }
 
+# Likewise for include/nmserve.h; bound by serve_lib().
+SERVE_SIGNATURES = {
+    "nm_kv_plan_scratch_bytes": (_I64, [_I64]),
+    "nm_kv_plan": (_I, [_P, _P, _I64, _P, _P, _P, _P, _P]),
+    "nm_attn_prompt_workspace_bytes": (_I64, [_I64, _I64, _I64, _I, _I, _I]),
+    "nm_attn_prompt": (_I, [_P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I64, _I, _I, _I, _I, ctypes.c_float, _P,
+                            _P, _P, _I64, _P]),
+    "nm_attn_tree_workspace_bytes": (_I64, [_I64, _I, _I, _I, _I, _I, _I64]),
+    "nm_attn_tree": (_I, [_P, _I64, _I64, _I, _I, _P, _P, _P, _I64, _P, _I64, ctypes.c_float, _P, _P, _P, _I64, _P]),
+}
+
 
 class KvCacheStruct(ctypes.Structure):
     """nm_kv_cache of include/nmattn.h."""
@@ -58,8 +69,15 @@ class KvCacheStruct(ctypes.Structure):
                 ("heads", _I), ("D", _I), ("dtype", _I), ("format", _I)]
 
 
+class KvPagesStruct(ctypes.Structure):
+    """nm_kv_pages of include/nmserve.h."""
+    _fields_ = [("table", _P), ("lens", _P), ("free", _P), ("n_free", _P), ("scratch", _P), ("B", _I64), ("width", _I64),
+                ("n_pages", _I64), ("page_size", _I)]
+
+
 _lib = None
 _attn_lib = None
+_serve_lib = None
 
 
 class NmError(RuntimeError):
@@ -87,17 +105,30 @@ def lib():
     return _lib
 
 
+def _bound(signatures):
+    handle = lib()
+    for name, (res, args) in signatures.items():
+        fn = getattr(handle, name)
+        fn.restype = res
+        fn.argtypes = args
+    return handle
+
+
 def attn_lib():
     """lib() with the calls of include/nmattn.h bound as well."""
     global _attn_lib
     if _attn_lib is None:
-        handle = lib()
-        for name, (res, args) in ATTN_SIGNATURES.items():
-            fn = getattr(handle, name)
-            fn.restype = res
-            fn.argtypes = args
-        _attn_lib = handle
+        _attn_lib = _bound(ATTN_SIGNATURES)
     return _attn_lib
+
+
+def serve_lib():
+    """attn_lib() with the calls of include/nmserve.h bound as well."""
+    global _serve_lib
+    if _serve_lib is None:
+        attn_lib()
+        _serve_lib = _bound(SERVE_SIGNATURES)
+    return _serve_lib
 
 
 def call(name, *args):

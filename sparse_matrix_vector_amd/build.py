@@ -6,12 +6,16 @@ next to this file so it travels with the source tree.
 import os
 import shutil
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = [os.path.join(HERE, "csrc", "nmapi.cpp"), os.path.join(HERE, "csrc", "nmspmv.hip"),
        os.path.join(HERE, "csrc", "nmcalib.hip"), os.path.join(HERE, "csrc", "nmattn_api.cpp"),
-       os.path.join(HERE, "csrc", "nmattn.hip"), os.path.join(HERE, "csrc", "nmcache.hip")]
+       os.path.join(HERE, "csrc", "nmattn.hip"), os.path.join(HERE, "csrc", "nmcache.hip"),
+       os.path.join(HERE, "csrc", "nmserve_api.cpp"), os.path.join(HERE, "csrc", "nmprompt.hip"),
+       os.path.join(HERE, "csrc", "nmtree.hip"), os.path.join(HERE, "csrc", "nmpages.hip")]
 LIB = os.path.join(HERE, "libnmspmv.so")
 # (sources, library): the product library
 TARGETS = [(SRC, LIB)]
@@ -32,11 +36,20 @@ def build(verbose: bool = False) -> str:
 
 
 def build_one(src, lib, verbose=False):
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-           # packed-fp32 instructions stay off (the compiler would otherwise form them from float code)
-           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-           "-fno-gpu-rdc", "-Wall", "-Wno-unused-result",
-           "-I", os.path.join(ROOT, "include"), *src, "-o", lib + ".tmp"]
+    """Compiles each source by itself, all at once, then links them."""
+    cc = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
+          # packed-fp32 instructions stay off (the compiler would otherwise form them from float code)
+          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+          "-fno-gpu-rdc", "-Wall", "-Wno-unused-result", "-I", os.path.join(ROOT, "include")]
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(min(len(src), os.cpu_count() or 1)) as pool:
+        objs = [os.path.join(tmp, os.path.basename(s) + ".o") for s in src]
+        list(pool.map(lambda so: _run(cc + ["-c", so[0], "-o", so[1]], verbose), zip(src, objs)))
+        _run([hipcc(), f"--offload-arch={ARCH}", "-fno-gpu-rdc", "-fPIC", "-shared", *objs, "-o", lib + ".tmp"], verbose)
+    os.replace(lib + ".tmp", lib)
+    return lib
+
+
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     proc = subprocess.run(cmd, capture_output=True, text=True)
@@ -44,9 +57,7 @@ def build_one(src, lib, verbose=False):
     if proc.returncode != 0:
         raise RuntimeError(f"hipcc failed ({proc.returncode}):\n{err}")
     if verbose and err.strip():
-        print(err)
-    os.replace(lib + ".tmp", lib)
-    return lib
+        print(err, flush=True)
 
 
 if __name__ == "__main__":

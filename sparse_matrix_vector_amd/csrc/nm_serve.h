@@ -1,0 +1,118 @@
+// nm_serve.h -- shared by the entry points of include/nmserve.h and their
+// kernels: launch plans and the kernel-side declarations.  Host-only C++ (no HIP
+// types), so that the checks and plans also build with a plain compiler.
+#ifndef NM_SERVE_H
+#define NM_SERVE_H
+
+#include <cstdint>
+
+#include "nm_attn.h"
+#include "nmserve.h"
+
+namespace nms {
+
+using nma::ceil_div;
+
+// ---- nm_kv_plan -----------------------------------------------------------------
+constexpr int kPlanThreads = 1024;              // of the deciding block
+constexpr int64_t kPlanRows = 8192;             // most rows that it deals with itself
+
+constexpr int64_t plan_scratch(int64_t B) { return (B + 2) / 2 * 8; }       // B + 1 int32, in whole 8 bytes
+
+// ---- nm_attn_prompt -----------------------------------------------------------
+//
+// Work is cut into tiles of `rows` rows, a row being one query head of one query of
+// a sequence and key head (row r: query r / G, head r % G).  Lengths are on the
+// device, so the grid has room for every way of cutting T queries into B sequences:
+// sequence b's tiles are numbers from starts[b] G / rows + b on (rounded down), which
+// leaves each at least as many as it needs.
+constexpr int kPromptWave = 32;                 // rows of a wave
+constexpr int64_t kPromptMaxStride = int64_t(1) << 28;
+constexpr int64_t kPromptMaxRows = (int64_t(1) << 31) - (int64_t(1) << 16);     // T * G
+
+struct PromptPlan {
+    int G;
+    int waves;                                  // of a block
+    int64_t tiles;                              // per key head, most that may be needed
+};
+
+inline PromptPlan prompt_plan(int64_t T, int64_t, int64_t B, int Hq, int heads, int D)
+{
+    PromptPlan p;
+    p.G = Hq / heads;
+    p.waves = D == 256 ? 4 : 8;
+    p.tiles = T * p.G / (p.waves * kPromptWave) + B;
+    return p;
+}
+
+inline int64_t prompt_workspace(const PromptPlan&, int) { return 0; }
+inline int64_t prompt_workspace_bound(int64_t, int64_t, int64_t, int, int, int) { return 0; }
+
+// ---- nm_attn_tree ----------------------------------------------------------------
+//
+// Units of (rows of a sequence and key head, range of its tokens), one block each, as
+// for nm_attn_decode (nm_attn.h).
+struct TreePlan {
+    int64_t rows;                               // of a sequence and key head: N * G
+    int mt, waves;                              // of a unit: 16 mt rows a wave; waves 0: not staged
+    int64_t groups, splits, chunk;
+    bool direct;                                // one range: units write o
+    int64_t parts;                              // partial rows
+};
+
+inline TreePlan tree_plan(int64_t B, int N, int Hq, int heads, int D, int64_t max_len)
+{
+    TreePlan p;
+    p.rows = (int64_t)N * (Hq / heads);
+    p.mt = p.rows <= 16 || D == 256 ? 1 : 2;
+    p.waves = p.rows <= 16 * p.mt ? 0 : p.rows <= 64 * p.mt && D != 256 ? 4 : 8;
+    p.groups = ceil_div(p.rows, 16 * p.mt * (p.waves ? p.waves : 1));
+    const int64_t units = B * heads * p.groups;
+    nma::cut(max_len, units, units >= nma::kCus ? nma::kCus : 2 * nma::kCus, 4096, &p.splits, &p.chunk);
+    p.direct = p.splits <= 1;
+    if (p.direct)
+        p.splits = 1;
+    p.parts = p.direct ? 0 : p.splits * B * N * Hq;
+    return p;
+}
+
+inline int64_t tree_workspace(const TreePlan& p, int D) { return p.parts * (D + 2) * 4; }
+
+// A workspace that serves every call of no larger B and max_len (and the same N): a
+// sequence has at most ceil(max_len / 128) ranges, and all sequences together at most
+// 512 / u + B while they have fewer than 256 units (u of a sequence), or B times the
+// ranges of at most 4096 tokens (nma::cut).
+inline int64_t tree_workspace_bound(int64_t B, int N, int Hq, int heads, int D, int64_t max_len)
+{
+    const auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+    const auto most = [](int64_t a, int64_t b) { return a > b ? a : b; };
+    const int64_t grain = nma::kWaves * nma::kStep, u = heads * tree_plan(1, N, Hq, heads, D, 1).groups;
+    if (max_len <= grain)
+        return 0;
+    const int64_t even = most(1, least(nma::kMaxRanges, ceil_div(max_len, 4096)));
+    int64_t ranges = least(B * even, most(B, nma::kMaxBlocks / u));
+    if (u < nma::kCus)
+        ranges = most(ranges, 2 * nma::kCus / u + least(B, (nma::kCus - 1) / u));
+    ranges = least(ranges, B * ceil_div(max_len, grain));
+    return ranges * N * Hq * (D + 2) * 4;
+}
+
+}  // namespace nms
+
+namespace nmk {
+
+// The kernel side of the calls of the same names, on checked arguments with
+// work to do.
+int kv_plan(const nm_kv_pages& pages, const int32_t* adds, int64_t rows, int32_t* starts, int64_t* slots,
+            int32_t* positions, int32_t* granted, void* stream);
+
+int attn_prompt(const nms::PromptPlan& plan, const void* q, int64_t q_stride, int64_t T, const void* k, int64_t k_stride,
+                const void* v, int64_t v_stride, int64_t Tk, const int32_t* starts, const int32_t* k_starts, int64_t B,
+                int Hq, int heads, int D, int dtype, float scale, void* o, float* lse, void* workspace, void* stream);
+int attn_tree(const nms::TreePlan& plan, const void* q, int64_t q_stride, int64_t B, int N, int Hq,
+              const nm_kv_cache& cache, const uint64_t* visible, const int32_t* page_table, int64_t table_stride,
+              const int32_t* lens, int64_t max_len, float scale, void* o, float* lse, void* workspace, void* stream);
+
+}  // namespace nmk
+
+#endif  // NM_SERVE_H
