@@ -21,27 +21,31 @@ constexpr int64_t plan_scratch(int64_t B) { return (B + 2) / 2 * 8; }       // B
 
 // ---- nm_attn_prompt -----------------------------------------------------------
 //
-// Work is cut into tiles of `rows` rows, a row being one query head of one query of
+// Work is cut into tiles of kPromptRows rows, a row being one query head of one query of
 // a sequence and key head (row r: query r / G, head r % G).  Lengths are on the
 // device, so the grid has room for every way of cutting T queries into B sequences:
-// sequence b's tiles are numbers from starts[b] G / rows + b on (rounded down), which
+// sequence b's tiles are numbers from starts[b] G / kPromptRows + b on (rounded down), which
 // leaves each at least as many as it needs.
 constexpr int kPromptWave = 32;                 // rows of a wave
+// Waves of a block: two blocks of four share a CU and do not wait for each other.  One of
+// eight stages keys and values once for twice the rows, but its waves go in step and its
+// tiles are coarser (us with four / eight: 16 prompts of up to 1024 tokens 106 / 116, one of
+// 2048 61 / 69, one of 8192 on 64 heads 1165 / 1120; before the products were made to overlap).
+constexpr int kPromptWaves = 4;
+constexpr int kPromptRows = kPromptWave * kPromptWaves;
 constexpr int64_t kPromptMaxStride = int64_t(1) << 28;
 constexpr int64_t kPromptMaxRows = (int64_t(1) << 31) - (int64_t(1) << 16);     // T * G
 
 struct PromptPlan {
     int G;
-    int waves;                                  // of a block
     int64_t tiles;                              // per key head, most that may be needed
 };
 
-inline PromptPlan prompt_plan(int64_t T, int64_t, int64_t B, int Hq, int heads, int D)
+inline PromptPlan prompt_plan(int64_t T, int64_t, int64_t B, int Hq, int heads, int)
 {
     PromptPlan p;
     p.G = Hq / heads;
-    p.waves = D == 256 ? 4 : 8;
-    p.tiles = T * p.G / (p.waves * kPromptWave) + B;
+    p.tiles = T * p.G / kPromptRows + B;
     return p;
 }
 

@@ -1,6 +1,6 @@
 // nmprompt.hip -- nm_attn_prompt: causal attention over packed prompts.
 //
-// A block holds NW x 32 rows (query heads of one key head, nm_serve.h) and walks
+// A block holds 4 x 32 rows (query heads of one key head, nm_serve.h) and walks
 // over the keys that its last row sees, 64 at a time.  Each wave keeps its 32 rows
 // as matrix operands and, in one pass over the keys, a reference m near the running
 // maximum of their scores, the sum l of the weights exp(s - m) and the vector
@@ -22,11 +22,18 @@
 // or of their 16-byte pieces' numbers with the row's, which keeps the banks apart:
 // keys by row % 16 (reads of 16 rows' same piece), values by 2 (row % 8) (transposing
 // reads of 4 rows' same 32 bytes).
+//
+// The work on a step of 32 keys is spread over three: its scores are formed during the
+// step before, its weights (32 exponentials a pair of rows) beside other steps' products,
+// its sums during the step after, so that a wave always has products that wait for
+// nothing (one prompt of 8192 tokens, 64 heads on 8 of 128 columns: 1165 us with the three
+// in a row, 1050 this way, 1047 TFLOP/s of the formula).
 
 #include <hip/hip_runtime.h>
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "nm_device.h"
 #include "nm_serve.h"
@@ -101,10 +108,16 @@ __device__ __forceinline__ float halves_sum(float v)
     return bits_f32(p.x) + bits_f32(p.y);
 }
 
-// 1 KB from memory to LDS: the 16 bytes at lane i's address go to lds + 16 i.  The
-// compiler does not know that LDS is written nor that a load is in flight: whoever
-// reads waits (arrive) first.  (m0 is reserved: the compiler keeps nothing in it from
-// one statement to the next.)
+// 1 KB from memory to LDS: the 16 bytes at lane i's address (base + offset) go to
+// lds + 16 i.  The compiler does not know that LDS is written nor that a load is in
+// flight: whoever reads waits (arrive) first.  (m0 is reserved: the compiler keeps nothing
+// in it from one statement to the next.)
+__device__ __forceinline__ void to_lds(uint32_t lds, const uint8_t* base, uint32_t offset)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+                 : "memory");
+}
+
 __device__ __forceinline__ void to_lds(uint32_t lds, const uint8_t* address)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(address) : "memory");
@@ -143,44 +156,71 @@ __device__ __forceinline__ int find_sequence(const PromptArgs& A, int tile, int 
     return lo;
 }
 
-// The keys and values of one tile in LDS, and their way there.
+// A tile's rows (keys or values) in LDS, and their way there.
 template <int D, int NW>
 struct Tile {
     static constexpr int kRow = 2 * D;                          // bytes of a row
-    static constexpr int kBytes = kKeys * kRow;                 // of the keys, and of the values
+    static constexpr int kBytes = kKeys * kRow;
     static constexpr int kRows = 1024 / kRow;                   // rows of a load
     static constexpr int kLanes = kRow / 16;                    // lanes of a row
-    static constexpr int kLoads = kKeys / kRows / NW;           // of a wave, keys and values each
+    static constexpr int kLoads = kKeys / kRows / NW;           // of a wave
+    static constexpr int kKinds = 16 / (kRows * NW) > 1 ? 16 / (kRows * NW) : 1;    // loads whose pieces lie differently
     static_assert(kLoads >= 1 && kKeys % (kRows * NW) == 0, "every wave loads as much");
 
     // The exclusive or of a piece's number in row `row`.
     static __device__ __forceinline__ int k_swap(int row) { return D == 64 ? row / 2 % 8 : row % 16; }
     static __device__ __forceinline__ int v_swap(int row) { return D == 64 ? 2 * (row % 4) : 2 * (row % 8); }
 
-    // Rows key0 .. of a sequence that ends at key `end`: rows from there on are copies of its last one.
-    static __device__ __forceinline__ void load(uint32_t lds, const uint8_t* k, int64_t k_stride, const uint8_t* v,
-                                                int64_t v_stride, int key0, int end, int wave, int lane)
+    const uint8_t* rows;        // the sequence's first row of this head
+    int64_t stride;             // bytes
+    uint32_t offset[kKinds];    // of the lane's 16 bytes from a load's first row
+    int kind[kKinds];           // its piece
+
+    template <bool KEYS>
+    __device__ __forceinline__ void start(const uint8_t* first, int64_t stride_, int wave, int lane)
     {
+        rows = first;
+        stride = stride_;
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int row0 = (wave + NW * j) * kRows, row = row0 + lane / kLanes;
-            const int key = min(key0 + row, end - 1);
-            const int kc = lane % kLanes ^ k_swap(row), vc = lane % kLanes ^ v_swap(row);
-            to_lds(lds + row0 * kRow, k + key * k_stride + kc * 16);
-            to_lds(lds + kBytes + row0 * kRow, v + key * v_stride + vc * 16);
+        for (int x = 0; x < kKinds; ++x) {
+            const int row = (wave + NW * x) * kRows + lane / kLanes;
+            kind[x] = (lane % kLanes ^ (KEYS ? k_swap(row) : v_swap(row))) * 16;
+            offset[x] = (uint32_t)(lane / kLanes) * (uint32_t)stride + kind[x];
+        }
+    }
+
+    // Tile `tile` of a sequence of `n` rows; rows behind its last one are copies of that.
+    __device__ __forceinline__ void load(uint32_t lds, int tile, int n, int wave, int lane) const
+    {
+        const int row0 = tile * kKeys;
+        if (row0 + kKeys <= n) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int at = (wave + NW * j) * kRows;
+                to_lds(lds + at * kRow, rows + (row0 + at) * stride, offset[j % kKinds]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int at = (wave + NW * j) * kRows;
+                to_lds(lds + at * kRow, rows + min(row0 + at + lane / kLanes, n - 1) * stride + kind[j % kKinds]);
+            }
         }
     }
 };
 
-template <int DT, int D, int NW, bool LSE>
-__global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void prompt_kernel(const PromptArgs A, int blocks)
+template <int DT, int D, bool LSE>
+__global__ __launch_bounds__(nms::kPromptWaves * 64, D == 256 ? 1 : 2) void prompt_kernel(const PromptArgs A, int blocks)
 {
+    constexpr int NW = nms::kPromptWaves;
     using L = Tile<D, NW>;
     constexpr int kSteps = D / 16;                              // k-steps of the score product
     constexpr int kCols = D / 32;                               // tiles of columns of the output
+    constexpr int kQuarter = kSteps / 4;                        // products of each sort in a quarter of a step
     constexpr int kRows = NW * nms::kPromptWave;
     constexpr float kBelow = DT == NM_FP16 ? 7.0f : -8.0f, kRoom = DT == NM_FP16 ? 15.0f : 0.0f;
-    __shared__ __align__(1024) uint8_t lds[4 * L::kBytes];
+    constexpr uint32_t kOnes = DT == NM_FP16 ? 0x3C003C00u : 0x3F803F80u;
+    __shared__ __align__(1024) uint8_t lds[4 * L::kBytes];      // two buffers of keys, two of values
     const int lane = threadIdx.x % 64, m = lane % 32, g = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int block = (int)flat_block();
@@ -191,17 +231,28 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void prompt_kernel(const 
     const int h = block % A.heads, tile = A.tiles - 1 - block / A.heads;
     const int b = find_sequence(A, tile, kRows, lane);
     const int q0 = bound(A.starts[b], A.T), nq = bound(A.starts[b + 1], A.T) - q0;
-    const int k0 = bound(A.k_starts[b], A.Tk), nk = max(bound(A.k_starts[b + 1], A.Tk) - k0, 0);
+    const int k0 = bound(A.k_starts[b], A.Tk);
+    const int nk = __builtin_amdgcn_readfirstlane(max(bound(A.k_starts[b + 1], A.Tk) - k0, 0));
     const int64_t r0 = ((int64_t)tile - first_tile(A, b, kRows)) * kRows;        // the block's first row
     if (nq <= 0 || r0 >= (int64_t)nq * A.G)
         return;
     const int R = nq * A.G, row0 = (int)r0 + wave * nms::kPromptWave;
     const int r = min(row0 + m, R - 1), query = r / A.G, head = h * A.G + r % A.G;
     const int limit = query + nk - nq;                                           // the last key the lane's row sees
-    // Keys below `all` are seen by every row of the wave, from `some` on by none.
-    const int all = __builtin_amdgcn_readfirstlane(min(row0, R - 1) / A.G + nk - nq + 1);
-    const int some = __builtin_amdgcn_readfirstlane(row0 < R ? min(row0 + 31, R - 1) / A.G + nk - nq + 1 : 0);
+    // Of the wave's steps of 32 keys the first n_whole are seen by all its rows, those from n_steps on by none.
+    const int all = min(row0, R - 1) / A.G + nk - nq + 1, some = min(row0 + 31, R - 1) / A.G + nk - nq + 1;
+    const int n_whole = __builtin_amdgcn_readfirstlane(max(all, 0) / kPart);
+    const int n_steps = __builtin_amdgcn_readfirstlane(row0 < R ? (max(some, 0) + kPart - 1) / kPart : 0);
     const int end = __builtin_amdgcn_readfirstlane(((int)min(r0 + kRows, (int64_t)R) - 1) / A.G + nk - nq + 1);
+    const int tiles = (max(end, 0) + kKeys - 1) / kKeys;
+
+    L keys, values;
+    keys.template start<true>(A.k + k0 * A.k_stride + (int64_t)h * 2 * D, A.k_stride, wave, lane);
+    values.template start<false>(A.v + k0 * A.v_stride + (int64_t)h * 2 * D, A.v_stride, wave, lane);
+    const uint32_t k_buf = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    const uint32_t v_buf = k_buf + 2 * L::kBytes;
+    if (tiles > 0)
+        keys.load(k_buf, 0, nk, wave, lane);
 
     u32x4 q[kSteps];
     {
@@ -217,123 +268,198 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void prompt_kernel(const 
         for (int i = 0; i < 16; ++i)
             acc[c][i] = 0.0f;
     float mx = NM_NEG_INF, sum = 0.0f, plain_sum = 0.0f;
+    f32x16 s = acc[0];                                      // scores of the coming step
+    f32x16 w = acc[0];                                      // weights of the step before
 
-    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-    const uint8_t* kp = A.k + k0 * A.k_stride + (int64_t)h * 2 * D;
-    const uint8_t* vp = A.v + k0 * A.v_stride + (int64_t)h * 2 * D;
-    const int tiles = (end + kKeys - 1) / kKeys;
-    if (tiles > 0)
-        L::load(base, kp, A.k_stride, vp, A.v_stride, 0, nk, wave, lane);
-    // Where the lane's operands lie in a tile.
-    const uint32_t k_at = m * L::kRow, k_piece = g ^ L::k_swap(m);
+    // Where the lane's operands lie: keys of the buffer of tile t + 1, values of that of tile t.
+    uint32_t k_at[kSteps], v_at[kCols];
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c)
+        k_at[c] = k_buf + m * L::kRow + ((2 * c ^ g ^ L::k_swap(m)) << 4);
     const int vr = 4 * g + lane % 16 / 4;
-    const uint32_t v_at = vr * L::kRow + lane % 2 * 8;
-    const uint32_t v_piece = (lane / 16 % 2 * 2 + lane % 4 / 2) ^ L::v_swap(vr);
-
-    for (int t = 0; t < tiles; ++t) {
+#pragma unroll
+    for (int c = 0; c < kCols; ++c)
+        v_at[c] = v_buf + L::kBytes + vr * L::kRow + lane % 2 * 8 +
+                  ((4 * c ^ (lane / 16 % 2 * 2 + lane % 4 / 2) ^ L::v_swap(vr)) << 4);
+    const auto read_k = [&](int c, int part) {
+        return *(lds_u32x4*)(uintptr_t)(k_at[c] + part * kPart * L::kRow);
+    };
+    const auto read_v = [&](int x, int c, int part) {
+        const uint32_t at = v_at[c] + (part * kPart + 16 * x) * L::kRow;
+        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)at));
+        const u32x2 hi = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(at + 8 * L::kRow)));
+        return u32x4{lo.x, lo.y, hi.x, hi.y};
+    };
+    // The tile's loads, and the buffers' change of roles.
+    const auto begin = [&](int t) {
         arrive();
+        if (t + 2 < tiles)
+            keys.load(k_buf + (t & 1) * L::kBytes, t + 2, nk, wave, lane);
         if (t + 1 < tiles)
-            L::load(base + ((t + 1) & 1) * 2 * L::kBytes, kp, A.k_stride, vp, A.v_stride, (t + 1) * kKeys, nk, wave, lane);
-        const uint32_t kb = base + (t & 1) * 2 * L::kBytes, vb = kb + L::kBytes;
+            values.load(v_buf + (~t & 1) * L::kBytes, t + 1, nk, wave, lane);
+    };
+    const auto turn = [&]() {
 #pragma unroll
-        for (int part = 0; part < kKeys / kPart; ++part) {
-            const int key0 = t * kKeys + part * kPart;
-            if (key0 >= some)
-                break;
-            const bool whole = key0 + kPart <= all;
-            f32x16 s;
+        for (int c = 0; c < kSteps; ++c)
+            k_at[c] ^= L::kBytes;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[i] = 0.0f;
+        for (int c = 0; c < kCols; ++c)
+            v_at[c] ^= L::kBytes;
+    };
+    // Room for the scores s: raises the reference of rows that need it.
+    const auto make_room = [&]() {
+        float top = NM_NEG_INF;
 #pragma unroll
-            for (int c = 0; c < kSteps; ++c) {
-                const u32x4 a = *(lds_u32x4*)(uintptr_t)(kb + part * kPart * L::kRow + k_at + ((2 * c ^ k_piece) << 4));
-                s = mfma<DT>(a, q[c], s);
+        for (int i = 0; i < 16; ++i)
+            top = fmaxf(top, s[i]);
+        top *= A.scale;
+        if (__any(top > mx + kRoom)) {
+            top = halves_max(top);
+            top = top > mx + kRoom ? top - kBelow : mx;
+            const float f = mx == top ? 1.0f : __builtin_amdgcn_exp2f(mx - top);
+            sum *= f;
+            plain_sum *= f;
+            w *= f;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+                acc[c] *= f;
+            mx = top;
+        }
+    };
+    // Two weights as operands, added to the sum.
+    const auto pack = [&](int i) {
+        const uint32_t x = pack2<DT>(w[i], w[i + 1]);
+        sum = dot2<DT>(x, kOnes, sum);
+        if constexpr (LSE)
+            plain_sum += w[i] + w[i + 1];
+        return x;
+    };
+
+    const auto hot = [&](auto part_) {
+        constexpr int part = part_();
+        make_room();
+        const float ref = mx == NM_NEG_INF ? 0.0f : mx;
+        f32x16 next;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            next[i] = 0.0f;
+        // Operands are read one quarter ahead of the products that use them.
+        u32x4 ka[2][kQuarter], va[2][kQuarter], p[2];
+        const auto read = [&](int x) {
+#pragma unroll
+            for (int c = 0; c < kQuarter; ++c) {
+                const int at = x * kQuarter + c;
+                ka[x % 2][c] = read_k(at, part);
+                va[x % 2][c] = read_v(at / kCols, at % kCols, part);
             }
-            if (!whole)
+        };
+        read(0);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (key0 + 8 * (i / 4) + 4 * g + i % 4 > limit)
-                        s[i] = NM_NEG_INF;                       // whatever lies there, NaN included
-            float top = NM_NEG_INF;
+        for (int i = 0; i < 16; i += 2)
+            p[i / 8][i % 8 / 2] = pack(i);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                top = fmaxf(top, s[i]);
-            top *= A.scale;
-            if (__any(top > mx + kRoom)) {
-                // rows that need no more room stay as they are, whatever stands beside them
-                top = halves_max(top);
-                top = top > mx + kRoom ? top - kBelow : mx;
-                const float f = mx == top ? 1.0f : __builtin_amdgcn_exp2f(mx - top);
-                sum *= f;
-                plain_sum *= f;
+        for (int x = 0; x < 4; ++x) {
+            if (x < 3)
+                read(x + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int c = 0; c < kCols; ++c)
-                    acc[c] *= f;
-                mx = top;
+            for (int c = 0; c < kQuarter; ++c) {
+                const int at = x * kQuarter + c;
+                next = mfma<DT>(ka[x % 2][c], q[at], next);
+                acc[at % kCols] = mfma<DT>(va[x % 2][c], p[at / kCols], acc[at % kCols]);
             }
-            const float ref = mx == NM_NEG_INF ? 0.0f : mx;
-            u32x4 p[2];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], A.scale, -ref));
-                const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 1], A.scale, -ref));
-                const uint32_t w = pack2<DT>(w0, w1);
-                if constexpr (LSE)
-                    plain_sum += w0 + w1;
-                p[i / 8][i % 8 / 2] = w;
-                sum = dot2<DT>(w, DT == NM_FP16 ? 0x3C003C00u : 0x3F803F80u, sum);
+            for (int i = 4 * x; i < 4 * x + 4; ++i)
+                w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], A.scale, -ref));
+            
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        s = next;
+    };
+
+    // Step u with all its conditions.
+    const auto cold = [&](int u, int part) {
+        if (u >= 0 && u < n_steps) {
+            if (u >= n_whole)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)                     // whatever lies there, NaN included
+                    s[i] = u * kPart + 8 * (i / 4) + 4 * g + i % 4 > limit ? NM_NEG_INF : s[i];
+            make_room();
+        }
+        if (u >= 1 && u <= n_steps) {
+            u32x4 p0, p1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                p0[i] = pack(2 * i);
+                p1[i] = pack(8 + 2 * i);
             }
-            u32x4 va[2][kCols];
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) {
-                    const uint32_t at = vb + (part * kPart + 16 * x) * L::kRow + v_at + ((4 * c ^ v_piece) << 4);
-                    const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)at));
-                    const u32x2 hi = __builtin_bit_cast(
-                        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(at + 8 * L::kRow)));
-                    va[x][c] = u32x4{lo.x, lo.y, hi.x, hi.y};
-                }
-            if (!whole) {
-                // 0 * NaN must not reach a row that does not see the value.  Steps with
-                // infinities or NaN among the values take them key by key and keep the sums of
-                // the rows that do not see the key.
-                float odd = 0.0f;
+            float odd = 0.0f;
+            if (u > n_whole)
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c)
+                    for (int c = 0; c < kCols; ++c) {
+                        const u32x4 a = read_v(x, c, part);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            odd = dot2<DT>(va[x][c][i], 0u, odd);
-                if (__any(odd != 0.0f)) {
+                            odd = dot2<DT>(a[i], 0u, odd);
+                    }
+            if (__any(odd != 0.0f)) {
+                // 0 * NaN must not reach a row that does not see the value: steps with infinities
+                // or NaN among the values take them key by key, and rows that do not see the key
+                // keep their sums.
+#pragma unroll
+                for (int c = 0; c < kCols; ++c)
 #pragma unroll 1
                     for (int key = 0; key < kPart; ++key) {
                         const int in = key % 16, word = (in % 4 + in / 8 * 4) / 2;
                         const uint32_t keep = in / 4 % 2 == g ? (key % 2 ? 0xFFFF0000u : 0xFFFFu) : 0u;
-                        u32x4 mask;
+                        const bool sees = (u - 1) * kPart + key <= limit;
+                        u32x4 a = read_v(key / 16, c, part), p;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mask[i] = i == word ? keep : 0u;
-                        const u32x4 w = key < 16 ? p[0] : p[1];
-#pragma unroll
-                        for (int c = 0; c < kCols; ++c) {
-                            const u32x4 a = (key < 16 ? va[0][c] : va[1][c]) & mask;
-                            const f32x16 with = mfma<DT>(a, w, acc[c]);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                acc[c][i] = key0 + key <= limit ? with[i] : acc[c][i];
+                        for (int i = 0; i < 4; ++i) {
+                            a[i] &= i == word ? keep : 0u;
+                            p[i] = key < 16 ? p0[i] : p1[i];
                         }
-                    }
-                    continue;
-                }
-            }
+                        const f32x16 with = mfma<DT>(a, p, acc[c]);
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+                        for (int i = 0; i < 16; ++i)
+                            acc[c][i] = sees ? with[i] : acc[c][i];
+                    }
+            } else {
 #pragma unroll
                 for (int c = 0; c < kCols; ++c)
-                    acc[c] = mfma<DT>(va[x][c], p[x], acc[c]);
+                    acc[c] = mfma<DT>(read_v(1, c, part), p1, mfma<DT>(read_v(0, c, part), p0, acc[c]));
+            }
+        }
+        if (u >= 0 && u < n_steps) {
+            const float ref = mx == NM_NEG_INF ? 0.0f : mx;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], A.scale, -ref));
+        }
+        if (u + 1 < n_steps) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[i] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c)
+                s = mfma<DT>(read_k(c, part), q[c], s);
+        }
+    };
+
+    for (int t = -1; t < tiles;) {
+        begin(t);
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part)
+            cold(2 * t + 1 + part, part);
+        turn();
+        for (++t; 2 * t + 2 < n_whole && 2 * t + 3 < n_steps; ++t) {
+            begin(t);
+            hot(std::integral_constant<int, 0>());
+            hot(std::integral_constant<int, 1>());
+            turn();
         }
     }
     sum = halves_sum(sum);
@@ -356,17 +482,18 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void prompt_kernel(const 
             A.lse[row] = (mx + __builtin_amdgcn_logf(plain_sum)) * kLn2;
 }
 
-template <int DT, int D, int NW>
+template <int DT, int D>
 int launch(const nms::PromptPlan& P, const PromptArgs& A, hipStream_t s)
 {
     const int64_t blocks = P.tiles * A.heads;
     if (blocks > INT32_MAX)
         return NM_ERR_BAD_SHAPE;
+    constexpr int kThreads = nms::kPromptWaves * 64;
     (void)hipGetLastError();
     if (A.lse)
-        hipLaunchKernelGGL((prompt_kernel<DT, D, NW, true>), flat_grid(blocks), dim3(NW * 64), 0, s, A, (int)blocks);
+        hipLaunchKernelGGL((prompt_kernel<DT, D, true>), flat_grid(blocks), dim3(kThreads), 0, s, A, (int)blocks);
     else
-        hipLaunchKernelGGL((prompt_kernel<DT, D, NW, false>), flat_grid(blocks), dim3(NW * 64), 0, s, A, (int)blocks);
+        hipLaunchKernelGGL((prompt_kernel<DT, D, false>), flat_grid(blocks), dim3(kThreads), 0, s, A, (int)blocks);
     return hipGetLastError() == hipSuccess ? NM_OK : NM_ERR_HIP;
 }
 
@@ -374,9 +501,9 @@ template <int DT>
 int launch_width(const nms::PromptPlan& P, const PromptArgs& A, int D, hipStream_t s)
 {
     switch (D) {
-    case 64: return launch<DT, 64, 8>(P, A, s);
-    case 128: return launch<DT, 128, 8>(P, A, s);
-    default: return launch<DT, 256, 4>(P, A, s);
+    case 64: return launch<DT, 64>(P, A, s);
+    case 128: return launch<DT, 128>(P, A, s);
+    default: return launch<DT, 256>(P, A, s);
     }
 }
 
