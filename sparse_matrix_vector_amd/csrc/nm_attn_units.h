@@ -17,8 +17,6 @@ namespace nmu {
 
 using namespace nmd;
 
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -375,57 +373,43 @@ __device__ __forceinline__ void mask_scores(f32x4 (&sc)[MT][NT], const int (&n)[
     }
 }
 
-// acc += v w for the value operands v[j] of a pair of tiles (first tokens `first`) that
-// hold infinities or NaN which some rows do not see: token by token, each row keeping its
-// sums where it does not see the token.
-template <int DT, int MT, int PER>
-__device__ __forceinline__ void add_seen(f32x4 (&acc)[MT][PER], const u32x4 (&v)[PER], const u32x4 (&w)[2][MT],
-                                         const int (&first)[2], const Seen<Drafts, MT>& seen, int kg)
+// acc[g] += v w[.][g] for one column's operand v of a pair of tiles (first tokens `first`) of
+// which some rows do not see all.  If it holds infinities or NaN, token by token, each row
+// keeping its sums where it does not see the token: 0 * NaN must not reach them.
+template <int DT, int MT>
+__device__ __forceinline__ void add_seen(f32x4 (&acc)[MT], u32x4 v, const u32x4 (&w)[2][MT], const int (&first)[2],
+                                         const Seen<Drafts, MT>& seen, int kg)
 {
+    float odd = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        odd = dot2<DT>(v[i], 0u, odd);
+    if (!__any(odd != 0.0f)) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int g = 0; g < MT; ++g)
+                acc[g] = mfma<DT>(v, w[p][g], acc[g]);
+        return;
+    }
 #pragma unroll 1
     for (int x = 0; x < 2 * nma::kTile; ++x) {
         const int in = x % nma::kTile, word = x / nma::kTile * 2 + in % 4 / 2;
         const uint32_t keep = in / 4 == kg ? (in % 2 ? 0xFFFF0000u : 0xFFFFu) : 0u;
-        u32x4 mask;
+        const int t = (x < nma::kTile ? first[0] : first[1]) + in;
+        u32x4 one;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            mask[i] = i == word ? keep : 0u;
-        const int t = (x < nma::kTile ? first[0] : first[1]) + in;
+            one[i] = i == word ? v[i] & keep : 0u;
 #pragma unroll
         for (int g = 0; g < MT; ++g) {
             const bool sees = seen.four(g, t) & 1;
+            const f32x4 with = mfma<DT>(one, w[1][g], mfma<DT>(one, w[0][g], acc[g]));
 #pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                const f32x4 a = mfma<DT>(v[j] & mask, w[1][g], mfma<DT>(v[j] & mask, w[0][g], acc[g][j]));
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[g][j][i] = sees ? a[i] : acc[g][j][i];
-            }
+            for (int i = 0; i < 4; ++i)
+                acc[g][i] = sees ? with[i] : acc[g][i];
         }
     }
-}
-
-// sum + the products of two pairs of 16-bit floats.
-template <int DT>
-__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float sum)
-{
-    if constexpr (DT == NM_FP16)
-        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), __builtin_bit_cast(f16x2, b), sum, false);
-    else
-        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), sum, false);
-}
-
-// Whether any of the wave's value operands is an infinity or NaN.
-template <int DT, int PER>
-__device__ __forceinline__ bool any_odd(const u32x4 (&v)[PER])
-{
-    float odd = 0.0f;
-#pragma unroll
-    for (int j = 0; j < PER; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            odd = dot2<DT>(v[j][i], 0u, odd);
-    return __any(odd != 0.0f);
 }
 
 // What a dword of two 16-bit floats, `whole`, leaves out of the fp32 a and b that were
@@ -628,8 +612,8 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
         at += 2 * NW;
     };
     // One step; with `more`, the loads of the wave's next one start as soon as the
-    // registers they fill are free.
-    const auto step = [&](auto more) {
+    // registers they fill are free.  In a tree the caller says whether it is `masked`.
+    const auto step = [&](auto more, auto masked) {
         if constexpr (more()) {
             refer(next);
             fetch();
@@ -654,10 +638,9 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
         if constexpr (more())
             load_k(next);
         const int n[2] = {cur[0].n, cur[1].n}, first[2] = {cur[0].first, cur[1].first};
-        bool whole = n[0] == nma::kTile && n[1] == nma::kTile;
+        const bool whole = P::kTree ? !masked() : n[0] == nma::kTile && n[1] == nma::kTile;
         if constexpr (P::kTree) {
-            whole = whole && first[1] + nma::kTile <= seen.first_draft;
-            if (!whole)
+            if constexpr (masked())
                 mask_scores(sc, n, first, seen, kg);
         } else if (!whole) {
             mask_scores(sc, n, kg);
@@ -695,14 +678,22 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
                 }
         };
         if constexpr (P::kTree) {
-            u32x4 a[kPer];
+            if constexpr (masked()) {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                a[j] = u32x4{vo[0][2 * j], vo[0][2 * j + 1], vo[1][2 * j], vo[1][2 * j + 1]};
-            if (!whole && any_odd<DT>(a))
-                add_seen<DT>(acc, a, wo, first, seen, kg);
-            else
+                for (int j = 0; j < kPer; ++j) {
+                    const u32x4 a = {vo[0][2 * j], vo[0][2 * j + 1], vo[1][2 * j], vo[1][2 * j + 1]};
+                    f32x4 column[MT];
+#pragma unroll
+                    for (int g = 0; g < MT; ++g)
+                        column[g] = acc[g][j];
+                    add_seen<DT, MT>(column, a, wo, first, seen, kg);
+#pragma unroll
+                    for (int g = 0; g < MT; ++g)
+                        acc[g][j] = column[g];
+                }
+            } else {
                 products();
+            }
         } else {
             products();
         }
@@ -718,9 +709,21 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
         __builtin_amdgcn_sched_barrier(0);              // keys first: they are waited for first
         load_v(cur);
         fetch();
-        while (at < last)
-            step(std::true_type());
-        step(std::false_type());
+        if constexpr (P::kTree) {
+            // drafts, and what else is not whole, lie behind the whole tiles
+            const auto whole = [&]() {
+                return cur[0].n == nma::kTile && cur[1].n == nma::kTile && cur[1].first + nma::kTile <= seen.first_draft;
+            };
+            while (at < last && whole())
+                step(std::true_type(), std::false_type());
+            while (at < last)
+                step(std::true_type(), std::true_type());
+            step(std::false_type(), std::true_type());
+        } else {
+            while (at < last)
+                step(std::true_type(), std::false_type());
+            step(std::false_type(), std::false_type());
+        }
     }
 #pragma unroll
     for (int g = 0; g < MT; ++g)
@@ -776,7 +779,7 @@ __device__ __forceinline__ void attend(const AttnArgs& A, const int32_t* pages, 
 
 constexpr int join_bytes(int D, int mt, int waves) { return waves / 2 * mt * (D / 4 + 2) * 64 * 4; }
 
-// ---- staged units (prefixes, trees) --------------------------------------------
+// ---- staged prefix units -----------------------------------------------------
 //
 // W waves with 16 MT rows each share every tile of the range: four tiles at a
 // time are loaded by the block (each wave a half or a whole of one tile's keys and
@@ -850,15 +853,17 @@ struct Stage {
 
     // Operands of what was loaded into the tile's place in a buffer; values of
     // tokens that do not count become zeros (0 * NaN must not reach o).
-    __device__ __forceinline__ void put(uint8_t* buf, int tile, int part, int lane) const
+    // With `turned`, the keys' lanes of an odd tile change places (m with m ^ 8).
+    __device__ __forceinline__ void put(uint8_t* buf, int tile, int part, int lane, bool turned = false) const
     {
         uint8_t* kd = buf + tile * kTileBytes;
+        const int k_lane = lane ^ (turned ? tile % 2 * 8 : 0);
         uint8_t* vd = buf + (kTiles + tile / 2 * 2) * kTileBytes + tile % 2 * 8;
         const int kg = lane / 16;
         if constexpr (BITS == 16) {
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
-                *reinterpret_cast<u32x4*>(kd + (part * kMine + i) * 1024 + lane * 16) =
+                *reinterpret_cast<u32x4*>(kd + (part * kMine + i) * 1024 + k_lane * 16) =
                     u32x4{k[4 * i], k[4 * i + 1], k[4 * i + 2], k[4 * i + 3]};
                 u32x4 x = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
                 if (n < nma::kTile) {
@@ -875,7 +880,7 @@ struct Stage {
             // the operand functions take a lane's whole part; what this wave did not load is not used
 #pragma unroll
             for (int i = 0; i < kMine; ++i)
-                *reinterpret_cast<u32x4*>(kd + (part * kMine + i) * 1024 + lane * 16) =
+                *reinterpret_cast<u32x4*>(kd + (part * kMine + i) * 1024 + k_lane * 16) =
                     C::k_codes(k + i * BITS / 4, ks, part * kMine + i, kg);
 #pragma unroll
             for (int i = 0; i < kVPairs; ++i) {
@@ -910,9 +915,9 @@ constexpr int staged_bytes()
     return 2 * Stage<NM_FP16, BITS, D, W>::kBytes + 2 * Stage<NM_FP16, BITS, D, W>::kTiles * 4;
 }
 
-template <class P, int DT, int BITS, int D, int MT, int W>
-__device__ __forceinline__ void attend_staged(const AttnArgs& A, const int32_t* pages, int h, int b0, int group, int R,
-                                              int start, int end, bool direct, int64_t part_row, uint8_t* lds)
+template <int DT, int BITS, int D, int MT, int W>
+__device__ __forceinline__ void attend_staged(const AttnArgs& A, const int32_t* pages, int h, int group, int R, int start,
+                                              int end, int64_t part_row, uint8_t* lds)
 {
     using S = Stage<DT, BITS, D, W>;
     constexpr int NT = S::kTiles, kSteps = S::kSteps, kPer = S::kPer;
@@ -924,11 +929,8 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, const int32_t* 
     const int mine = wave % NT, part = wave / NT;            // the tile of each step that this wave loads
     const bool busy = row0 < R;
 
-    Rows<P, DT, BITS, D, MT> rows;
-    rows.load(A, h, b0, row0, R, m, kg);
-    Seen<P, MT> seen;
-    if constexpr (P::kTree)
-        seen.load(A, b0, min(A.lens[b0], A.max_len), row0, R, m);
+    Rows<OneToken, DT, BITS, D, MT> rows;
+    rows.load(A, h, 0, row0, R, m, kg);
     f32x4 acc[MT][kPer];
     float mx[MT], sum[MT];
 #pragma unroll
@@ -1004,48 +1006,11 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, const int32_t* 
                 n[u] = __builtin_amdgcn_readfirstlane(count[i & 1][u]);
                 whole = whole && n[u] == nma::kTile;
             }
-            int first[NT];
-            if constexpr (P::kTree) {
-#pragma unroll
-                for (int u = 0; u < NT; ++u)
-                    first[u] = start + (i * NT + u) * nma::kTile;
-                whole = whole && first[NT - 1] + nma::kTile <= seen.first_draft;
-                if (!whole)
-                    mask_scores(sc, n, first, seen, kg);
-            } else if (!whole) {
+            if (!whole)
                 mask_scores(sc, n, kg);
-            }
             w.find(mx, sum, acc, A.scale);
             constexpr int kGroups = NT / 2 * kPer / kGroup;
             u32x4 wo[2][MT];
-            bool done = false;
-            if constexpr (P::kTree)
-                if (!whole) {
-                    // the few steps with drafts: pairs of tiles one after the other
-                    done = true;
-#pragma unroll
-                    for (int t = 0; t < NT / 2; ++t) {
-                        u32x4 a[kPer];
-#pragma unroll
-                        for (int j = 0; j < kPer; ++j)
-                            a[j] = *reinterpret_cast<const u32x4*>(vb + (t * kPer + j) * 1024 + lane * 16);
-                        w.whole(wo[0], t);
-                        w.rest(wo[1], wo[0], t);
-                        if (any_odd<DT>(a)) {
-                            const int pair[2] = {first[2 * t], first[2 * t + 1]};
-                            add_seen<DT>(acc, a, wo, pair, seen, kg);
-                            continue;
-                        }
-#pragma unroll
-                        for (int p = 0; p < 2; ++p)
-#pragma unroll
-                            for (int j = 0; j < kPer; ++j)
-#pragma unroll
-                                for (int g = 0; g < MT; ++g)
-                                    acc[g][j] = mfma<DT>(a[j], wo[p][g], acc[g][j]);
-                    }
-                }
-            if (!P::kTree || !done)
 #pragma unroll
             for (int x = 0; x < kGroups; ++x) {
                 const bool first = x * kGroup % kPer == 0;
@@ -1077,11 +1042,7 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, const int32_t* 
     for (int g = 0; g < MT; ++g) {
         const int r = row0 + 16 * g;
         const float total = quarters_sum(sum[g]);
-        if (r + m >= R)
-            continue;
-        if (P::kTree && direct)
-            store_out<P, DT, D>(A, h, b0, r + m, kg, acc[g], mx[g], total);
-        else
+        if (r + m < R)
             store_part<D>(A, part_row + r, min(16, R - r), m, kg, acc[g], mx[g], total);
     }
 }

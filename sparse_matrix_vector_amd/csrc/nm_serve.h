@@ -54,12 +54,23 @@ inline int64_t prompt_workspace_bound(int64_t, int64_t, int64_t, int, int, int) 
 
 // ---- nm_attn_tree ----------------------------------------------------------------
 //
-// Units of (rows of a sequence and key head, range of its tokens), one block each, as
-// for nm_attn_decode (nm_attn.h).
+// Units of (rows of a sequence and key head, range of its tokens), one block each, in two
+// forms (nmtree.hip).
+constexpr int kTreeWaves = 4;
+constexpr int64_t kTreeRange = 4096;            // tokens of a range at most
+
+// Blocks that fill the GPU.
+inline int64_t tree_blocks(bool shared, int D, int64_t units)
+{
+    return shared && D == 256 ? nma::kCus : shared || units < nma::kCus ? 2 * nma::kCus : nma::kCus;
+}
+
 struct TreePlan {
     int64_t rows;                               // of a sequence and key head: N * G
-    int mt, waves;                              // of a unit: 16 mt rows a wave; waves 0: not staged
-    int64_t groups, splits, chunk;
+    bool shared;                                // the form that shares the cache through LDS
+    int mt;                                     // else: 16 mt rows
+    int waves;                                  // shared: row groups of 32 in a block (1, 2 or 4)
+    int64_t groups, splits, chunk;              // units of the rows, ranges of the tokens
     bool direct;                                // one range: units write o
     int64_t parts;                              // partial rows
 };
@@ -68,11 +79,12 @@ inline TreePlan tree_plan(int64_t B, int N, int Hq, int heads, int D, int64_t ma
 {
     TreePlan p;
     p.rows = (int64_t)N * (Hq / heads);
-    p.mt = p.rows <= 16 || D == 256 ? 1 : 2;
-    p.waves = p.rows <= 16 * p.mt ? 0 : p.rows <= 64 * p.mt && D != 256 ? 4 : 8;
-    p.groups = ceil_div(p.rows, 16 * p.mt * (p.waves ? p.waves : 1));
+    p.shared = p.rows > 32 || D == 256;
+    p.mt = p.rows <= 16 ? 1 : 2;
+    p.waves = p.rows <= 32 ? 1 : p.rows <= 64 ? 2 : 4;
+    p.groups = ceil_div(p.rows, 32 * p.waves);
     const int64_t units = B * heads * p.groups;
-    nma::cut(max_len, units, units >= nma::kCus ? nma::kCus : 2 * nma::kCus, 4096, &p.splits, &p.chunk);
+    nma::cut(max_len, units, tree_blocks(p.shared, D, units), kTreeRange, &p.splits, &p.chunk);
     p.direct = p.splits <= 1;
     if (p.direct)
         p.splits = 1;
@@ -84,8 +96,8 @@ inline int64_t tree_workspace(const TreePlan& p, int D) { return p.parts * (D + 
 
 // A workspace that serves every call of no larger B and max_len (and the same N): a
 // sequence has at most ceil(max_len / 128) ranges, and all sequences together at most
-// 512 / u + B while they have fewer than 256 units (u of a sequence), or B times the
-// ranges of at most 4096 tokens (nma::cut).
+// 512 / u + B while they have fewer than 512 units (u of a sequence), or B times the
+// ranges of at most kTreeRange tokens (nma::cut).
 inline int64_t tree_workspace_bound(int64_t B, int N, int Hq, int heads, int D, int64_t max_len)
 {
     const auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
@@ -93,10 +105,10 @@ inline int64_t tree_workspace_bound(int64_t B, int N, int Hq, int heads, int D, 
     const int64_t grain = nma::kWaves * nma::kStep, u = heads * tree_plan(1, N, Hq, heads, D, 1).groups;
     if (max_len <= grain)
         return 0;
-    const int64_t even = most(1, least(nma::kMaxRanges, ceil_div(max_len, 4096)));
+    const int64_t even = most(1, least(nma::kMaxRanges, ceil_div(max_len, kTreeRange)));
     int64_t ranges = least(B * even, most(B, nma::kMaxBlocks / u));
-    if (u < nma::kCus)
-        ranges = most(ranges, 2 * nma::kCus / u + least(B, (nma::kCus - 1) / u));
+    if (u < 2 * nma::kCus)
+        ranges = most(ranges, 2 * nma::kCus / u + least(B, (2 * nma::kCus - 1) / u));
     ranges = least(ranges, B * ceil_div(max_len, grain));
     return ranges * N * Hq * (D + 2) * 4;
 }

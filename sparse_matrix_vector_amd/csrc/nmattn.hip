@@ -64,8 +64,8 @@ __global__ __launch_bounds__((W ? W : nma::kWaves) * 64, 2) void units_kernel(co
         const int h = unit % A.heads, split = unit / A.heads % A.prefix_splits, group = unit / A.heads / A.prefix_splits;
         const int start = split * A.prefix_chunk, end = min(start + A.prefix_chunk, A.prefix_len);
         if constexpr (W > 0) {
-            attend_staged<OneToken, DT, BITS, D, MT, W>(A, A.prefix_pages, h, 0, group, A.prefix_rows, start, end, false,
-                                                        ((int64_t)split * A.heads + h) * A.prefix_rows, lds);
+            attend_staged<DT, BITS, D, MT, W>(A, A.prefix_pages, h, group, A.prefix_rows, start, end,
+                                              ((int64_t)split * A.heads + h) * A.prefix_rows, lds);
         } else {
             const int at = start / nma::kTile + 2 * wave;
             attend<OneToken, DT, BITS, D, MT, NW>(A, A.prefix_pages, h, 0, group * 16 * MT, A.prefix_rows, start, end,

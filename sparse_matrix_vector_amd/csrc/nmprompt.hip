@@ -42,9 +42,6 @@ namespace {
 
 using namespace nmd;
 
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
@@ -73,40 +70,6 @@ struct PromptArgs {
     float scale;
     uint32_t q_and, q_xor;
 };
-
-template <int DT>
-__device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c)
-{
-    if constexpr (DT == NM_FP16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
-                                                      0);
-    else
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                       0, 0);
-}
-
-// sum + a.x + a.y of the two 16-bit floats (times b's).
-template <int DT>
-__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float sum)
-{
-    if constexpr (DT == NM_FP16)
-        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), __builtin_bit_cast(f16x2, b), sum, false);
-    else
-        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), sum, false);
-}
-
-// Maximum / sum of a lane and lane ^ 32 (a row's two halves).
-__device__ __forceinline__ float halves_max(float v)
-{
-    const u32x2 p = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(f32_bits(v), f32_bits(v), false, false));
-    return fmaxf(bits_f32(p.x), bits_f32(p.y));
-}
-
-__device__ __forceinline__ float halves_sum(float v)
-{
-    const u32x2 p = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(f32_bits(v), f32_bits(v), false, false));
-    return bits_f32(p.x) + bits_f32(p.y);
-}
 
 // 1 KB from memory to LDS: the 16 bytes at lane i's address (base + offset) go to
 // lds + 16 i.  The compiler does not know that LDS is written nor that a load is in
@@ -366,8 +329,8 @@ __global__ __launch_bounds__(nms::kPromptWaves * 64, D == 256 ? 1 : 2) void prom
 #pragma unroll
             for (int c = 0; c < kQuarter; ++c) {
                 const int at = x * kQuarter + c;
-                next = mfma<DT>(ka[x % 2][c], q[at], next);
-                acc[at % kCols] = mfma<DT>(va[x % 2][c], p[at / kCols], acc[at % kCols]);
+                next = mfma32<DT>(ka[x % 2][c], q[at], next);
+                acc[at % kCols] = mfma32<DT>(va[x % 2][c], p[at / kCols], acc[at % kCols]);
             }
 #pragma unroll
             for (int i = 4 * x; i < 4 * x + 4; ++i)
@@ -422,7 +385,7 @@ __global__ __launch_bounds__(nms::kPromptWaves * 64, D == 256 ? 1 : 2) void prom
                             a[i] &= i == word ? keep : 0u;
                             p[i] = key < 16 ? p0[i] : p1[i];
                         }
-                        const f32x16 with = mfma<DT>(a, p, acc[c]);
+                        const f32x16 with = mfma32<DT>(a, p, acc[c]);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             acc[c][i] = sees ? with[i] : acc[c][i];
@@ -430,7 +393,7 @@ __global__ __launch_bounds__(nms::kPromptWaves * 64, D == 256 ? 1 : 2) void prom
             } else {
 #pragma unroll
                 for (int c = 0; c < kCols; ++c)
-                    acc[c] = mfma<DT>(read_v(1, c, part), p1, mfma<DT>(read_v(0, c, part), p0, acc[c]));
+                    acc[c] = mfma32<DT>(read_v(1, c, part), p1, mfma32<DT>(read_v(0, c, part), p0, acc[c]));
             }
         }
         if (u >= 0 && u < n_steps) {
@@ -445,7 +408,7 @@ __global__ __launch_bounds__(nms::kPromptWaves * 64, D == 256 ? 1 : 2) void prom
                 s[i] = 0.0f;
 #pragma unroll
             for (int c = 0; c < kSteps; ++c)
-                s = mfma<DT>(read_k(c, part), q[c], s);
+                s = mfma32<DT>(read_k(c, part), q[c], s);
         }
     };
 
