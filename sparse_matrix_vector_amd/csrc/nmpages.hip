@@ -2,7 +2,7 @@
 //
 // All of a step's decisions are sums over the sequences in order (pages given back,
 // pages and rows asked for), so one block makes them: thread t has the sequences
-// t c .. t c + c - 1, adds up its own, and a scan over the block's 1024 threads says
+// t c .. t c + c - 1, adds up its own, and a scan over the block's threads says
 // where each begins.  Pages and rows are then dealt with one a thread, each finding
 // its sequence by a binary search in the scanned sums, so that one sequence of many
 // pages costs no more than many of one.
@@ -22,8 +22,6 @@
 namespace {
 
 using namespace nmd;
-
-constexpr int kThreads = nms::kPlanThreads;
 
 struct PlanArgs {
     int32_t* table;
@@ -69,44 +67,68 @@ __device__ __forceinline__ Request request(const PlanArgs& A, int b)
     return q;
 }
 
-// Inclusive sums over the block's threads, in `sums`; returns the total.
-__device__ __forceinline__ int64_t scan(int64_t x, int64_t* sums, int64_t* waves)
+// What sequences give back and ask for, added up: pages (below 2^31, as B * width is) and rows,
+// of which more than `most` = rows + 1 count as that many (they do not fit whatever follows).
+struct Sums {
+    uint32_t freed, want, grow;
+};
+
+__device__ __forceinline__ Sums plus(Sums a, Sums b, uint32_t most)
 {
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-#pragma unroll
-    for (int i = 1; i < 64; i *= 2) {
-        const int64_t y = __shfl_up(x, i);
-        x += lane >= i ? y : 0;
-    }
-    if (lane == 63)
-        waves[wave] = x;
-    __syncthreads();
-    int64_t before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) {
-        before += w < wave ? waves[w] : 0;
-        total += waves[w];
-    }
-    sums[threadIdx.x] = x + before;
-    __syncthreads();
-    return total;
+    const uint64_t grow = (uint64_t)a.grow + b.grow;
+    return {a.freed + b.freed, a.want + b.want, grow > most ? most : (uint32_t)grow};
 }
 
-// The first of n entries that is above x (n - 1 if none is).
-template <class T>
-__device__ __forceinline__ int above(const T* sums, int n, int64_t x)
+// Inclusive sums over the lanes of a wave, of which the first N count.
+template <int N>
+__device__ __forceinline__ Sums scan_wave(Sums x, uint32_t most, int lane)
+{
+#pragma unroll
+    for (int i = 1; i < N; i *= 2) {
+        const Sums y = {__shfl_up(x.freed, i), __shfl_up(x.want, i), __shfl_up(x.grow, i)};
+        if (lane >= i)
+            x = plus(x, y, most);
+    }
+    return x;
+}
+
+// Inclusive sums over the block's threads, in sums[1 ..] with nothing in sums[0]; returns the totals.
+template <int NT>
+__device__ __forceinline__ Sums scan(Sums x, uint32_t most, Sums* sums, Sums* waves)
+{
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    x = scan_wave<64>(x, most, lane);
+    if (threadIdx.x == 0)
+        sums[0] = Sums{0, 0, 0};
+    if constexpr (NT > 64) {
+        if (lane == 63)
+            waves[wave] = x;
+        __syncthreads();
+        // every wave adds up the waves' totals for itself
+        const Sums y = scan_wave<NT / 64>(lane < NT / 64 ? waves[lane] : Sums{0, 0, 0}, most, lane);
+        if (wave > 0)
+            x = plus(x, {__shfl(y.freed, wave - 1), __shfl(y.want, wave - 1), __shfl(y.grow, wave - 1)}, most);
+    }
+    sums[1 + threadIdx.x] = x;
+    __syncthreads();
+    return sums[NT];
+}
+
+// The first of n entries whose value is above x (n - 1 if none is).
+template <class F>
+__device__ __forceinline__ int above(F value, int n, int64_t x)
 {
     int lo = 0;
-    for (int step = n; step > 0;) {
-        const int half = step / 2;
-        if (lo + half < n && sums[lo + half] <= x) {
+    for (int left = n - 1; left > 0;) {                 // among lo .. lo + left
+        const int half = left / 2;
+        if (value(lo + half) <= x) {
             lo += half + 1;
-            step -= half + 1;
+            left -= half + 1;
         } else {
-            step = half;
+            left = half;
         }
     }
-    return min(lo, n - 1);
+    return lo;
 }
 
 // Row r is token `at` of sequence b, which held `len` tokens on `held` pages.
@@ -132,109 +154,185 @@ __device__ __forceinline__ void no_row(const PlanArgs& A, int r)
     A.positions[r] = 0;
 }
 
-__global__ __launch_bounds__(kThreads) void plan_kernel(const PlanArgs A, int with_rows)
+// NT threads with EACH sequences, kept in registers; EACH 0: any number of sequences, read again
+// whenever they are looked at.
+template <int NT, int EACH>
+__global__ __launch_bounds__(NT) void plan_kernel(const PlanArgs A, int with_rows)
 {
-    __shared__ int64_t sums[kThreads], pops[kThreads], waves[kThreads / 64];
-    __shared__ int held_of[kThreads], len_of[kThreads];
-    __shared__ int64_t stop_rows, stop_pages;
+    __shared__ Sums sums[NT + 1], waves[NT / 64];
+    __shared__ int held_of[EACH == 1 ? NT : 1], len_of[EACH == 1 ? NT : 1];
     __shared__ int stop;
-    const int tid = threadIdx.x, b0 = min(tid * A.each, A.B), b1 = min(b0 + A.each, A.B);
+    __shared__ uint32_t stop_rows, stop_pages;
+    constexpr int kKept = EACH ? EACH : 1;
+    const int each = EACH ? EACH : A.each;
+    const int tid = threadIdx.x, b0 = min(tid * each, A.B), b1 = min(b0 + each, A.B);
+    const int n_free = min(max(A.n_free[0], 0), A.n_pages);
     if (tid == 0)
         stop = A.B;
-    const int n_free = min(max(A.n_free[0], 0), A.n_pages);
-
-    // Pages that come back, the first one on top.
-    int64_t own = 0;
-    for (int b = b0; b < b1; ++b)
-        own += request(A, b).freed;
-    const int64_t freed = scan(own, sums, waves);
-    for (int64_t k = tid; k < freed; k += kThreads) {
-        const int t = above(sums, kThreads, k);
-        int64_t in = k - (t > 0 ? sums[t - 1] : 0);
-        int b = t * A.each;
-        Request q = request(A, b);
-        while (in >= q.freed) {
-            in -= q.freed;
-            q = request(A, ++b);
-        }
-        const int64_t to = n_free + freed - 1 - k;
-        if (to < A.n_pages)
-            A.free[to] = A.table[(int64_t)b * A.width + q.held - q.freed + in];
-    }
-    const int64_t room = min(n_free + freed, (int64_t)A.n_pages);
-
-    // What is asked for, in order, until pages or rows run out.
-    int64_t want = 0, grow = 0;
-    for (int b = b0; b < b1; ++b) {
-        const Request q = request(A, b);
-        want += q.want;
-        grow += q.grow;
-    }
-    __syncthreads();
-    const int64_t all_pages = scan(want, pops, waves);
-    __syncthreads();
-    const int64_t all_rows = scan(grow, sums, waves);
-    const int64_t pages0 = pops[tid] - want, rows0 = sums[tid] - grow;
-    if (pops[tid] > room || sums[tid] > A.rows) {
-        int64_t p = pages0, n = rows0;
-        for (int b = b0; b < b1; ++b) {
-            const Request q = request(A, b);
-            if (p + q.want > room || n + q.grow > A.rows) {
-                atomicMin(&stop, b);
-                break;
+    Request kept[kKept];
+    const uint32_t most = (uint32_t)A.rows + 1;
+    Sums own = {0, 0, 0};
+    const auto asked = [&](const Request& q) { return Sums{(uint32_t)q.freed, (uint32_t)q.want, (uint32_t)q.grow}; };
+    const auto count = [&](const Request& q) { own = plus(own, asked(q), most); };
+    if constexpr (EACH > 0) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            kept[i] = Request{-1, 0, 0, 0, 0, 0, false};
+            if (b0 + i < b1) {
+                kept[i] = request(A, b0 + i);
+                count(kept[i]);
             }
-            p += q.want;
-            n += q.grow;
+        }
+    } else {
+        for (int b = b0; b < b1; ++b)
+            count(request(A, b));
+    }
+    // f(b, its request) for the thread's sequences, in order
+    const auto walk = [&](auto f) {
+        if constexpr (EACH > 0) {
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                if (b0 + i < b1)
+                    f(b0 + i, kept[i]);
+        } else {
+            for (int b = b0; b < b1; ++b)
+                f(b, request(A, b));
+        }
+    };
+    const Sums all = scan<NT>(own, most, sums, waves), before = sums[tid];
+
+    // Pages that come back, the first one on top: by their own threads where those have few each, else
+    // one a thread in turn.
+    const int64_t top = (int64_t)n_free + all.freed - 1;
+    const auto give = [&](int64_t k, int b, const Request& q, int64_t in) {
+        if (top - k < A.n_pages)
+            A.free[top - k] = A.table[(int64_t)b * A.width + q.held - q.freed + in];
+    };
+    if (all.freed > 0) {
+        if (__syncthreads_and(own.freed <= 8)) {
+            // the first pages' loads do not wait for one another's stores
+            int32_t first[kKept];
+            if constexpr (EACH > 0) {
+#pragma unroll
+                for (int i = 0; i < EACH; ++i)
+                    first[i] = kept[i].freed > 0
+                                   ? A.table[(int64_t)(b0 + i) * A.width + kept[i].held - kept[i].freed] : 0;
+            }
+            int64_t k = before.freed;
+            walk([&](int b, const Request& q) {
+                for (int in = 0; in < q.freed; ++in, ++k) {
+                    if (EACH > 0 && in == 0) {
+                        if (top - k < A.n_pages)
+                            A.free[top - k] = first[EACH > 0 ? b - b0 : 0];
+                    } else {
+                        give(k, b, q, in);
+                    }
+                }
+            });
+        } else if constexpr (EACH == 1) {
+            // four at a time, so that their loads do not wait for one another
+            held_of[tid] = kept[0].held - kept[0].freed;
+            __syncthreads();
+            for (int64_t k0 = tid; k0 < all.freed; k0 += 4 * NT) {
+                int32_t page[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t k = k0 + i * NT;
+                    page[i] = 0;
+                    if (k < all.freed) {
+                        const int b = above([&](int t) { return sums[t + 1].freed; }, NT, k);
+                        page[i] = A.table[(int64_t)b * A.width + held_of[b] + (k - sums[b].freed)];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t k = k0 + i * NT;
+                    if (k < all.freed && top - k < A.n_pages)
+                        A.free[top - k] = page[i];
+                }
+            }
+            __syncthreads();
+        } else {
+            for (int64_t k = tid; k < all.freed; k += NT) {
+                const int t = above([&](int i) { return sums[i + 1].freed; }, NT, k);
+                int64_t in = k - sums[t].freed;
+                int b = t * each;
+                Request q = request(A, b);
+                while (in >= q.freed) {
+                    in -= q.freed;
+                    q = request(A, ++b);
+                }
+                give(k, b, q, in);
+            }
         }
     }
-    __syncthreads();
-    const int last = stop;
-    if (last < A.B && b0 <= last && last < b1) {
-        int64_t p = pages0, n = rows0;
-        for (int b = b0; b < last; ++b) {
-            const Request q = request(A, b);
-            p += q.want;
-            n += q.grow;
+    const uint32_t room = (uint32_t)min(top + 1, (int64_t)A.n_pages);
+
+    // What is asked for, in order, until pages or rows run out: at sequence `last`, if at all.
+    int last = A.B;
+    uint32_t got_rows = all.grow, got_pages = all.want;
+    if (all.want > room || all.grow == most) {          // the same for all threads
+        if (sums[tid + 1].want > room || sums[tid + 1].grow == most) {
+            Sums x = before;
+            int first = A.B;
+            walk([&](int b, const Request& q) {
+                x = plus(x, asked(q), most);
+                if (first == A.B && (x.want > room || x.grow == most))
+                    first = b;
+            });
+            atomicMin(&stop, first);
         }
-        stop_pages = p;
-        stop_rows = n;
+        __syncthreads();
+        last = stop;
+        if (b0 <= last && last < b1) {
+            Sums x = before;
+            walk([&](int b, const Request& q) {
+                if (b < last)
+                    x = plus(x, asked(q), most);
+            });
+            stop_pages = x.want;
+            stop_rows = x.grow;
+        }
+        __syncthreads();
+        got_rows = stop_rows;
+        got_pages = stop_pages;
     }
-    __syncthreads();
-    const int64_t got_rows = last < A.B ? stop_rows : all_rows, got_pages = last < A.B ? stop_pages : all_pages;
+    if (all.freed > 0)
+        __syncthreads();                                // lens is read for the pages above
     {
-        int64_t p = pages0, n = rows0;
-        for (int b = b0; b < b1; ++b) {
-            const Request q = request(A, b);
+        Sums x = before;
+        walk([&](int b, const Request& q) {
             const bool ok = b < last;
             const int change = (ok ? q.grow : 0) - q.drop;
-            if (with_rows) {                    // one sequence a thread
+            if constexpr (EACH == 1) {
                 held_of[tid] = q.held;
                 len_of[tid] = q.len;
             }
-            A.first_pop[b] = (int)min(p, room);
-            p += q.want;
-            n += q.grow;
+            A.first_pop[b] = (int)min(x.want, room);
+            x = plus(x, asked(q), most);
             A.granted[b] = change;
-            A.starts[b + 1] = (int)(ok ? n : got_rows);
+            A.starts[b + 1] = (int)(ok ? x.grow : got_rows);
             if (change != 0)
                 A.lens[b] = q.len + change;
-        }
+        });
     }
     if (tid == 0) {
         A.starts[0] = 0;
         A.first_pop[A.B] = (int)room;
         A.n_free[0] = (int)(room - got_pages);
     }
-    if (!with_rows)
-        return;
-    __syncthreads();
-    for (int r = tid; r < A.rows; r += kThreads) {
-        if (r >= got_rows) {
-            no_row(A, r);
-            continue;
+    if constexpr (EACH == 1) {
+        if (!with_rows)
+            return;
+        __syncthreads();
+        for (int r = tid; r < A.rows; r += NT) {
+            if (r >= (int)got_rows) {
+                no_row(A, r);
+                continue;
+            }
+            const int b = above([&](int i) { return sums[i + 1].grow; }, A.B, r);
+            row(A, r, b, len_of[b] + r - (int)sums[b].grow, held_of[b], (int)sums[b].want, (int)room);
         }
-        const int b = above(sums, A.B, r);
-        row(A, r, b, len_of[b] + r - (int)(b > 0 ? sums[b - 1] : 0), held_of[b], (int)(b > 0 ? pops[b - 1] : 0), (int)room);
     }
 }
 
@@ -267,7 +365,7 @@ __global__ __launch_bounds__(kRowsBlock) void rows_kernel(const PlanArgs A)
         const int first = sequence_of(ends, A.B, (int)r0, lane);
         const int last = sequence_of(ends, A.B, (int)min(r0 + kRowsBlock, (int64_t)n) - 1, lane);
         if (r < n) {
-            const int b = first + above(ends + first, last - first + 1, r);
+            const int b = first + above([&](int i) { return ends[first + i]; }, last - first + 1, r);    // no load for one
             const int len = A.lens[b] - A.granted[b];
             row(A, (int)r, b, len + (int)r - A.starts[b], (int)pages_of(len, A.shift), A.first_pop[b], room);
             return;
@@ -298,11 +396,26 @@ int nmk::kv_plan(const nm_kv_pages& p, const int32_t* adds, int64_t rows, int32_
     A.n_pages = (int)p.n_pages;
     A.shift = __builtin_ctz((unsigned)p.page_size);
     A.rows = (int)rows;
-    A.each = (int)nma::ceil_div(p.B, kThreads);
+    A.each = (int)nma::ceil_div(p.B, nms::kPlanThreads);
     hipStream_t s = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    const bool with_rows = A.each == 1 && rows <= nms::kPlanRows;
-    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kThreads), 0, s, A, with_rows ? 1 : 0);
+    // Few sequences need no block of 16 waves that wait for each other (32 sequences and rows, us with
+    // 64 / 1024 threads: 2.7 / 9.8).
+    const int threads = p.B <= 64 && rows <= 256 ? 64 : p.B <= 256 ? 256 : 1024;
+    const bool with_rows = A.each == 1 && rows <= nms::kPlanRows * threads / nms::kPlanThreads;
+    const auto plan = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(1), dim3(threads), 0, s, A, with_rows ? 1 : 0);
+    };
+    if (threads == 64)
+        plan(plan_kernel<64, 1>);
+    else if (threads == 256)
+        plan(plan_kernel<256, 1>);
+    else if (A.each == 1)
+        plan(plan_kernel<nms::kPlanThreads, 1>);
+    else if (A.each <= 4)
+        plan(plan_kernel<nms::kPlanThreads, 4>);
+    else
+        plan(plan_kernel<nms::kPlanThreads, 0>);
     if (!with_rows && rows > 0)
         hipLaunchKernelGGL(rows_kernel, flat_grid(nma::ceil_div(rows, kRowsBlock)), dim3(kRowsBlock), 0, s, A);
     return hipGetLastError() == hipSuccess ? NM_OK : NM_ERR_HIP;
