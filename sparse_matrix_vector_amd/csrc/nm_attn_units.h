@@ -823,48 +823,71 @@ struct Stage {
         }
     }
 
-    __device__ __forceinline__ void load(const AttnArgs& A, const TileRef& t, int part, int lane)
+    __device__ __forceinline__ void load_k(const AttnArgs& A, const TileRef& t, int part, int lane)
     {
         const uint8_t* kt = A.k + t.tile * nma::tile_bytes(D, BITS);
-        const uint8_t* vt = A.v + t.tile * nma::tile_bytes(D, BITS);
-        n = t.n;
         if constexpr (BITS == 16) {
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) {
+            for (int i = 0; i < kMine; ++i)
                 get<16>(k + 4 * i, kt + (part * kMine + i) * 1024 + lane * 16);
-                get<16>(v + 4 * i, vt + (part * kMine + i) * 1024 + lane * 16);
-            }
         } else {
-            const int m = lane % 16, kg = lane / 16;
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
                 const int at = (part * kMine + i) * BITS;
                 get<BITS>(k + i * BITS / 4, kt + at / C::kCb * 64 * C::kCb + lane * C::kCb + at % C::kCb);
             }
+            C::load_k_scale(ks, A.k_scale + t.tile * nma::scale_tile_bytes(D), lane % 16);
+        }
+    }
+
+    __device__ __forceinline__ void load_v(const AttnArgs& A, const TileRef& t, int part, int lane)
+    {
+        const uint8_t* vt = A.v + t.tile * nma::tile_bytes(D, BITS);
+        n = t.n;
+        if constexpr (BITS == 16) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+                get<16>(v + 4 * i, vt + (part * kMine + i) * 1024 + lane * 16);
+        } else {
 #pragma unroll
             for (int i = 0; i < kVPairs * kVBytes; i += kVLoad) {
                 const int at = part * kVPairs * kVBytes + i;
                 get<kVLoad>(v + i / 4, vt + at / C::kVb * 64 * C::kVb + lane * C::kVb + at % C::kVb);
             }
-            C::load_k_scale(ks, A.k_scale + t.tile * nma::scale_tile_bytes(D), m);
-            C::load_v_scale(vs, A.v_scale + t.tile * nma::scale_tile_bytes(D), m, kg);
+            C::load_v_scale(vs, A.v_scale + t.tile * nma::scale_tile_bytes(D), lane % 16, lane / 16);
         }
     }
 
-    // Operands of what was loaded into the tile's place in a buffer; values of
-    // tokens that do not count become zeros (0 * NaN must not reach o).
-    // With `turned`, the keys' lanes of an odd tile change places (m with m ^ 8).
-    __device__ __forceinline__ void put(uint8_t* buf, int tile, int part, int lane, bool turned = false) const
+    __device__ __forceinline__ void load(const AttnArgs& A, const TileRef& t, int part, int lane)
     {
-        uint8_t* kd = buf + tile * kTileBytes;
-        const int k_lane = lane ^ (turned ? tile % 2 * 8 : 0);
-        uint8_t* vd = buf + (kTiles + tile / 2 * 2) * kTileBytes + tile % 2 * 8;
-        const int kg = lane / 16;
+        load_k(A, t, part, lane);
+        load_v(A, t, part, lane);
+    }
+
+    // Operands of what was loaded into the tile's place among keys, or values, of which those of
+    // tokens that do not count become zeros (0 * NaN must not reach o).  With `turned`, the keys'
+    // lanes of an odd tile change places (m with m ^ 8).
+    __device__ __forceinline__ void put_k(uint8_t* keys, int tile, int part, int lane, bool turned = false) const
+    {
+        uint8_t* kd = keys + tile * kTileBytes;
+        const int to = lane ^ (turned ? tile % 2 * 8 : 0);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            u32x4 x;
+            if constexpr (BITS == 16)
+                x = u32x4{k[4 * i], k[4 * i + 1], k[4 * i + 2], k[4 * i + 3]};
+            else                                // (the operand functions take a lane's whole part; what this wave did not load is not used)
+                x = C::k_codes(k + i * BITS / 4, ks, part * kMine + i, lane / 16);
+            *reinterpret_cast<u32x4*>(kd + (part * kMine + i) * 1024 + to * 16) = x;
+        }
+    }
+
+    __device__ __forceinline__ void put_v(uint8_t* values, int tile, int part, int lane) const
+    {
+        uint8_t* vd = values + tile / 2 * 2 * kTileBytes + tile % 2 * 8;
         if constexpr (BITS == 16) {
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
-                *reinterpret_cast<u32x4*>(kd + (part * kMine + i) * 1024 + k_lane * 16) =
-                    u32x4{k[4 * i], k[4 * i + 1], k[4 * i + 2], k[4 * i + 3]};
                 u32x4 x = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
                 if (n < nma::kTile) {
                     // 16 bytes here are two lanes' halves of one column: quarter (lane % 32) / 8
@@ -876,22 +899,29 @@ struct Stage {
                 *reinterpret_cast<u32x2*>(to + 16) = u32x2{x.z, x.w};
             }
         } else {
-            const int left = n - 4 * kg;
-            // the operand functions take a lane's whole part; what this wave did not load is not used
-#pragma unroll
-            for (int i = 0; i < kMine; ++i)
-                *reinterpret_cast<u32x4*>(kd + (part * kMine + i) * 1024 + k_lane * 16) =
-                    C::k_codes(k + i * BITS / 4, ks, part * kMine + i, kg);
-#pragma unroll
-            for (int i = 0; i < kVPairs; ++i) {
-                const int pair = part * kVPairs + i;
-                uint32_t out[kPer];
-                C::v_codes(out, v + i * kVBytes / 4, vs >> (16 * pair));
+            const int left = n - 4 * (lane / 16);
+            if constexpr (kVPairs == 2) {
+                uint32_t lo[kPer], hi[kPer];
+                C::v_codes(lo, v, vs);
+                C::v_codes(hi, v + kVBytes / 4, vs >> 16);
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
-                    *reinterpret_cast<uint32_t*>(vd + j * 1024 + lane * 16 + pair * 4) = out[j] & keep(left, pair);
+                    *reinterpret_cast<u32x2*>(vd + j * 1024 + lane * 16) =
+                        u32x2{lo[j] & keep(left, 0), hi[j] & keep(left, 1)};
+            } else {
+                uint32_t out[kPer];
+                C::v_codes(out, v, vs >> (16 * part));
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    *reinterpret_cast<uint32_t*>(vd + j * 1024 + lane * 16 + part * 4) = out[j] & keep(left, part);
             }
         }
+    }
+
+    __device__ __forceinline__ void put(uint8_t* buf, int tile, int part, int lane) const
+    {
+        put_k(buf, tile, part, lane);
+        put_v(buf + kTiles * kTileBytes, tile, part, lane);
     }
 
     // Mask of the token pair (2 i, 2 i + 1) of a quarter of which `left` tokens count.

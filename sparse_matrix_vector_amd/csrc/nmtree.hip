@@ -8,8 +8,10 @@
 //   else (shared_kernel) a block of four waves shares it through LDS, each wave 32 rows:
 //     four tiles at a time are loaded by the block, turned into operands once and written
 //     to one of two buffers, the next four being on their way meanwhile.  One wave's 32
-//     rows are the columns of 32 x 32 products (32 keys, or 32 columns of v, by 32 rows);
-//     with 64 rows or fewer two waves share a row group and take the tile pairs in turn.
+//     rows are the columns of 32 x 32 products (32 keys, or 32 columns of v, by 32 rows).
+//     A pair of tiles is worked on in three rounds, as in nmprompt.hip: its scores beside
+//     the weights of the pair before, its sums beside the scores of the next.  With 64 rows
+//     or fewer two waves share a row group and take a pair of every four tiles each.
 // Only pairs of tiles with drafts, or with fewer tokens than they could hold, look at the
 // masks.  Units of one row are joined by a second launch.
 
@@ -65,18 +67,63 @@ __device__ __forceinline__ int64_t piece_at(int piece, int g, int nr, int m)
     return ((int64_t)(piece * 2 + g) * nr + m) * 4;
 }
 
+// One wave's tile on its way to LDS.  16-bit rows go there directly (global_load_lds), as they
+// lie in the cache; codes through registers, as operands.  In LDS:
+//   keys    [tile][column piece of 8, token] 16 bytes; the tokens m of odd tiles are stored at m ^ 8 (banks)
+//   values  16-bit: [tile][column j of a group][quarter][group] 8 bytes (four tokens);
+//           codes: [pair][column j][quarter][group] 16 bytes (four tokens of each tile)
 template <int DT, int BITS, int D>
+struct Way {
+    using S = Stage<DT, BITS, D, nms::kTreeWaves>;
+    static constexpr int kBytes = nms::kTreeWaves * S::kTileBytes;        // keys, or values, of four tiles
+    S stage;
+
+    static __device__ __forceinline__ void direct(uint32_t lds, const uint8_t* tile, int lane, int turned)
+    {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds + i * 1024),
+                         "v"(tile + i * 1024 + (lane ^ turned) * 16)
+                         : "memory");
+    }
+    __device__ __forceinline__ void load_k(const AttnArgs& A, const TileRef& t, uint32_t lds, int wave, int lane)
+    {
+        if constexpr (BITS == 16)
+            direct(lds + wave * S::kTileBytes, A.k + t.tile * nma::tile_bytes(D, BITS), lane, wave % 2 * 8);
+        else
+            stage.load_k(A, t, 0, lane);
+    }
+    __device__ __forceinline__ void load_v(const AttnArgs& A, const TileRef& t, uint32_t lds, int wave, int lane)
+    {
+        if constexpr (BITS == 16)
+            direct(lds + wave * S::kTileBytes, A.v + t.tile * nma::tile_bytes(D, BITS), lane, 0);
+        else
+            stage.load_v(A, t, 0, lane);
+    }
+    __device__ __forceinline__ void put_k(uint8_t* buf, int wave, int lane) const
+    {
+        if constexpr (BITS != 16)
+            stage.put_k(buf, wave, 0, lane, true);
+    }
+    __device__ __forceinline__ void put_v(uint8_t* buf, int wave, int lane) const
+    {
+        if constexpr (BITS != 16)
+            stage.put_v(buf, wave, 0, lane);
+    }
+};
+
+template <int DT, int BITS, int D, int SHARES>
 __global__ __launch_bounds__(nms::kTreeWaves * 64, D == 256 ? 1 : 2) void shared_kernel(const AttnArgs A, int units,
                                                                                        int groups_w, int direct)
 {
     constexpr int NW = nms::kTreeWaves;
-    using S = Stage<DT, BITS, D, NW>;
-    using C = typename S::C;
-    constexpr int NT = S::kTiles, kPer = D / 16, kSteps = D / 16, kCols = D / 32;
+    using W = Way<DT, BITS, D>;
+    using C = Cache<DT, BITS, D>;
+    constexpr int kTileBytes = W::S::kTileBytes, kBytes = W::kBytes;
+    constexpr int NT = NW, kPer = D / 16, kSteps = D / 16, kCols = D / 32, kQuarter = kSteps / 4;
     constexpr float kBelow = Weights<DT, 1, 2>::kBelow, kRoom = Weights<DT, 1, 2>::kRoom;
-    static_assert(NT == NW, "a wave loads a tile");
-    __shared__ __align__(1024) uint8_t lds[2 * S::kBytes];
-    __shared__ int count[2][NT];
+    static_assert(W::S::kTiles == NT, "a wave loads a tile");
+    __shared__ __align__(1024) uint8_t lds[4 * kBytes];         // two buffers of keys, two of values
     const int lane = threadIdx.x % 64, m = lane % 32, g = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
 
@@ -92,14 +139,49 @@ __global__ __launch_bounds__(nms::kTreeWaves * 64, D == 256 ? 1 : 2) void shared
     const int len = __builtin_amdgcn_readfirstlane(min(A.lens[b], A.max_len));
     if (len < 0 || (start >= len && !direct))       // the join looks at the ranges that hold tokens only
         return;
-    const int end = min(start + A.own_chunk, len), R = A.G;
+    const int end = min(start + A.own_chunk, len), R = A.G, first_draft = len - A.drafts;
 
     // groups_w row groups in the block's waves; with one or two, two waves have the same rows and a
     // pair of tiles of every four each (share), of one, two waves only load.
-    const int share = wave / groups_w, shares = groups_w == 4 ? 1 : 2;
+    const int share = SHARES == 2 ? wave / groups_w : 0;
     const int row0 = (group * groups_w + wave % groups_w) * 32;
-    const bool busy = row0 < R && share < shares;
+    const bool busy = row0 < R && share < SHARES;
     const int r = min(row0 + m, R - 1);
+
+    // Four tiles (a stage) by their pages: which are there, and where the wave's own is.
+    struct Pages {
+        int page[NT];
+    };
+    const int tile0 = start / nma::kTile;
+    const auto pages_of = [&](int stage) {
+        Pages x;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            x.page[j] = page_of(A, pages, tile0 + stage * NT + j, end);
+        return x;
+    };
+    const auto tokens = [&](const Pages& x, int stage, int j) {         // that count in tile j
+        const bool inside = (unsigned)x.page[j] < (unsigned)A.n_pages;
+        return inside ? min(max(end - (tile0 + stage * NT + j) * nma::kTile, 0), nma::kTile) : 0;
+    };
+    const auto own_tile = [&](const Pages& x, int stage) {
+        const int page = wave == 0 ? x.page[0] : wave == 1 ? x.page[1] : wave == 2 ? x.page[2] : x.page[3];
+        return tile_ref(A, page, tile0 + stage * NT + wave, end, h);
+    };
+    const auto is_whole = [&](const Pages& x, int stage) {
+        bool whole = start + (stage + 1) * nma::kStaged <= min(end, first_draft);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            whole = whole && (unsigned)x.page[j] < (unsigned)A.n_pages;
+        return whole;
+    };
+
+    const uint32_t k_buf = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds, v_buf = k_buf + 2 * kBytes;
+    W way;
+    const int steps = (end - start + nma::kStaged - 1) / nma::kStaged;      // stages
+    // of stages t .. t + 3 in round t (begin)
+    Pages x2 = pages_of(0), x3 = pages_of(1), x0 = x2, x1 = x2;
+    way.load_k(A, own_tile(x2, 0), k_buf, wave, lane);
 
     u32x4 q[kSteps];
     {
@@ -108,45 +190,41 @@ __global__ __launch_bounds__(nms::kTreeWaves * 64, D == 256 ? 1 : 2) void shared
         for (int s = 0; s < kSteps; ++s)
             q[s] = (*reinterpret_cast<const u32x4*>(row + C::column(s / 2, s % 2 * 2 + g)) & A.q_and) ^ A.q_xor;
     }
-    const int first_draft = len - A.drafts;
     const uint64_t bits = A.visible[(int64_t)b * A.drafts + r / A.heads_g];
 
-    f32x16 acc[kCols];
+    f32x16 acc[kCols], s, w;                                    // s: scores of the coming pair, w: weights of the one before
 #pragma unroll
-    for (int c = 0; c < kCols; ++c)
+    for (int i = 0; i < 16; ++i) {
+        s[i] = w[i] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int c = 0; c < kCols; ++c)
             acc[c][i] = 0.0f;
+    }
     float mx = NM_NEG_INF, sum = 0.0f;
 
     // A pair's score rows: row 16 x + 8 y + 4 z + c is token 8 x + 4 z + c of its tile y, so that the
     // lane's scores 8 x .. 8 x + 7 are tokens 4 (2 x + g) .. + 3 of both tiles: the k indices of the
-    // value operands as they are staged.  Keys of odd tiles are staged 8 lanes along (banks).
-    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    // value operands as they are staged.  Value operand rows 16 z + i of tile c of columns are column
+    // 2 c + z of group i (of D / 16 columns).  Keys of stage t + 1, values of stage t:
     const int tile = m / 8 % 2, token = m / 16 * 8 + m % 8;
-    const uint32_t k_at = base + tile * S::kTileBytes + g * 256 + (token ^ 8 * tile) * 16;
-    const uint32_t v_at = base + NT * S::kTileBytes + m / 16 * 1024 + g * 256 + m % 16 * 16;
-
-    // Scores of pair `pair` of the buffer at `buf`, weights from them, and the weighted values.
-    const auto attend_pair = [&](uint32_t buf, int pair, auto masked, const int (&n)[2], int first) {
-        f32x16 s;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            s[i] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < kSteps; ++c)
-            s = mfma32<DT>(*(lds_u32x4*)(uintptr_t)(k_at + buf + pair * 2 * S::kTileBytes + c * 512), q[c], s);
-        const auto sees4 = [&](int x, int y) {          // whether the row sees its tokens of scores 8 x + 4 y ..
-            const int in = 8 * x + 4 * g;
-            const int t = first + y * nma::kTile + in, draft = t - first_draft, before = min(max(-draft, 0), 4);
-            const uint32_t held = (1u << min(max(n[y] - in, 0), 4)) - 1u;
-            return ((uint32_t)((bits >> (max(draft, 0) & 63)) << before) | ((1u << before) - 1u)) & held;
-        };
-        if constexpr (masked()) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[i] = sees4(i / 8, i / 4 % 2) >> i % 4 & 1 ? s[i] : NM_NEG_INF;
+    uint32_t k_at = k_buf + tile * kTileBytes + g * 256 + (token ^ 8 * tile) * 16;
+    uint32_t v_at = v_buf + kBytes + (BITS == 16 ? m / 16 * 512 + g * 128 + m % 16 * 8
+                                                 : m / 16 * 1024 + g * 256 + m % 16 * 16);
+    const auto key = [&](int c, int part) {
+        return *(lds_u32x4*)(uintptr_t)(k_at + part * 2 * kTileBytes + c * 512);
+    };
+    const auto value = [&](int x, int c, int part) {
+        if constexpr (BITS == 16) {
+            typedef __attribute__((address_space(3))) const u32x2 lds_u32x2;
+            const uint32_t at = v_at + part * 2 * kTileBytes + c * 1024 + x * 256;
+            const u32x2 lo = *(lds_u32x2*)(uintptr_t)at, hi = *(lds_u32x2*)(uintptr_t)(at + kTileBytes);
+            return u32x4{lo.x, lo.y, hi.x, hi.y};
+        } else {
+            return *(lds_u32x4*)(uintptr_t)(v_at + (part * kPer + 2 * c) * 1024 + x * 512);
         }
+    };
+    // Room for the scores s: raises the reference of rows that need it.
+    const auto make_room = [&]() {
         float top = NM_NEG_INF;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -157,138 +235,276 @@ __global__ __launch_bounds__(nms::kTreeWaves * 64, D == 256 ? 1 : 2) void shared
             top = top > mx + kRoom ? top - kBelow : mx;
             const float f = mx == top ? 1.0f : __builtin_amdgcn_exp2f(mx - top);
             sum *= f;
+            w *= f;
 #pragma unroll
             for (int c = 0; c < kCols; ++c)
                 acc[c] *= f;
             mx = top;
         }
+    };
+    // s = weights of its scores i .. i + n - 1, added to the sum
+    const auto weigh = [&](int i, int n) {
         const float ref = mx == NM_NEG_INF ? 0.0f : mx;
-        // A weight is the sum of two operands, its rounding and the rest (nm_attn_units.h, Weights).
-        u32x4 p[2], rest[2];
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], A.scale, -ref));
-            const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 1], A.scale, -ref));
-            sum += w0 + w1;
-            const uint32_t w = pack2<DT>(w0, w1);
-            p[i / 8][i % 8 / 2] = w;
-            rest[i / 8][i % 8 / 2] = left_out<DT>(w, w0, w1);
+        for (int j = i; j < i + n; ++j) {
+            s[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], A.scale, -ref));
+            sum += s[j];
         }
-        const auto value = [&](int x, int c) {
-            return *(lds_u32x4*)(uintptr_t)(v_at + buf + (pair * kPer + 2 * c) * 1024 + x * 512);
+    };
+    // Weights 8 x .. 8 x + 7 as operands: each is the sum of two, its rounding and the rest
+    // (nm_attn_units.h, Weights).
+    const auto pack = [&](const f32x16& w, int x, u32x4& p, u32x4& rest) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p[i] = pack2<DT>(w[8 * x + 2 * i], w[8 * x + 2 * i + 1]);
+            rest[i] = left_out<DT>(p[i], w[8 * x + 2 * i], w[8 * x + 2 * i + 1]);
+        }
+    };
+    // Whole tiles, a pair of every stage for each of two waves: the next pair's scores beside this one's weights.
+    const auto hot_share = [&]() {
+        u32x4 ka[2][kQuarter], va[2][kCols], p[2], rest[2];
+#pragma unroll
+        for (int c = 0; c < kQuarter; ++c)
+            ka[0][c] = key(c, share);
+        make_room();
+        f32x16 next;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            next[i] = 0.0f;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (x < 3)
+#pragma unroll
+                for (int c = 0; c < kQuarter; ++c)
+                    ka[(x + 1) % 2][c] = key((x + 1) * kQuarter + c, share);
+            if (x == 1)
+#pragma unroll
+                for (int c = 0; c < kCols; ++c)
+                    va[0][c] = value(0, c, share);
+            weigh(4 * x, 4);
+#pragma unroll
+            for (int c = 0; c < kQuarter; ++c)
+                next = mfma32<DT>(ka[x % 2][c], q[x * kQuarter + c], next);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+            va[1][c] = value(1, c, share);
+        pack(s, 0, p[0], rest[0]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+                acc[c] = mfma32<DT>(va[x][c], p[x], acc[c]);
+            if (x == 0)
+                pack(s, 1, p[1], rest[1]);
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+                acc[c] = mfma32<DT>(va[x][c], rest[x], acc[c]);
+        }
+        s = next;
+    };
+    // Whole tiles, all pairs: scores of the next (keys of stage t + 1), weights, sums of the one before
+    // (values of stage t), all independent of each other.
+    const auto hot = [&](auto part_) {
+        constexpr int part = part_();
+        u32x4 ka[2][kQuarter], va[2][kQuarter], p[2], rest[2];
+        const auto read = [&](int x) {
+#pragma unroll
+            for (int c = 0; c < kQuarter; ++c) {
+                const int at = x * kQuarter + c;
+                ka[x % 2][c] = key(at, part);
+                va[x % 2][c] = value(at / kCols, at % kCols, part);
+            }
         };
-        if constexpr (masked()) {
-            // 0 * NaN must not reach a row that does not see the token: value operands with
-            // infinities or NaN are taken token by token, rows that do not see it keep their sums.
+        read(0);
+        make_room();
+        pack(w, 0, p[0], rest[0]);
+        f32x16 next;
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+        for (int i = 0; i < 16; ++i)
+            next[i] = 0.0f;
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) {
-                    const u32x4 v = value(x, c);
-                    float odd = 0.0f;
+        for (int x = 0; x < 4; ++x) {
+            if (x < 3)
+                read(x + 1);
+            if (x == 1)
+                pack(w, 1, p[1], rest[1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        odd = dot2<DT>(v[i], 0u, odd);
-                    if (!__any(odd != 0.0f)) {
-                        acc[c] = mfma32<DT>(v, rest[x], mfma32<DT>(v, p[x], acc[c]));
-                        continue;
-                    }
-#pragma unroll 1
-                    for (int k = 0; k < 16; ++k) {                  // k index (k / 8, k % 8)
-                        const uint32_t keep = k / 8 == g ? (k % 2 ? 0xFFFF0000u : 0xFFFFu) : 0u;
-                        u32x4 one;
+            for (int c = 0; c < kQuarter; ++c) {
+                const int at = x * kQuarter + c;
+                next = mfma32<DT>(ka[x % 2][c], q[at], next);
+                acc[at % kCols] = mfma32<DT>(va[x % 2][c], p[at / kCols], acc[at % kCols]);
+            }
+            weigh(4 * x, 4);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            one[i] = i == k % 8 / 2 ? v[i] & keep : 0u;
-                        const int y = k / 4 % 2, in = 8 * x + 4 * (k / 8) + k % 4;
-                        const int t = first + y * nma::kTile + in, draft = t - first_draft;
-                        const bool sees = (draft < 0) | (int)((bits >> (max(draft, 0) & 63)) & 1);
-                        const f32x16 with = mfma32<DT>(one, rest[x], mfma32<DT>(one, p[x], acc[c]));
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            acc[c][i] = sees ? with[i] : acc[c][i];
-                    }
-                }
-        } else {
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) {
-                    const u32x4 v = value(x, c);
-                    acc[c] = mfma32<DT>(v, rest[x], mfma32<DT>(v, p[x], acc[c]));
-                }
+            for (int c = 0; c < kQuarter; ++c) {
+                const int at = x * kQuarter + c;
+                acc[at % kCols] = mfma32<DT>(va[x % 2][c], rest[at / kCols], acc[at % kCols]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+        w = s;
+        s = next;
     };
 
-    S stage;
-    int at = start / nma::kTile + wave;
-    const int steps = (end - start + nma::kStaged - 1) / nma::kStaged;
-    stage.load(A, tile_ref(A, page_of(A, pages, at, end), at, end, h), 0, lane);
-    int page = page_of(A, pages, at + NT, end);
-    const auto put = [&](int which) {
-        stage.put(lds + which * S::kBytes, wave, 0, lane, true);
-        if (lane == 0)
-            count[which][wave] = stage.n;
+    // Whether the row sees its tokens of scores 8 x + 4 y .. + 3 of a pair: bits 0 .. 3.
+    const auto sees4 = [&](int x, int y, int n, int first) {
+        const int in = 8 * x + 4 * g;
+        const int draft = first + y * nma::kTile + in - first_draft, before = min(max(-draft, 0), 4);
+        const uint32_t held = (1u << min(max(n - in, 0), 4)) - 1u;
+        return ((uint32_t)((bits >> (max(draft, 0) & 63)) << before) | ((1u << before) - 1u)) & held;
     };
-    // The four tiles after those of step i begin their way.
-    const auto fetch = [&](int i) {
-        if (i + 1 >= steps)
-            return;
-        at += NT;
-        stage.load(A, tile_ref(A, page, at, end, h), 0, lane);
-        page = page_of(A, pages, at + NT, end);
-    };
-    const auto arrived = [&](int i) {
-        if (i + 1 < steps)
-            put((i + 1) & 1);                       // that buffer's readers passed the barrier before this step
-        __syncthreads();
-    };
-    const auto counted = [&](int i, int pair, int (&n)[2]) {
-        n[0] = __builtin_amdgcn_readfirstlane(count[i & 1][2 * pair]);
-        n[1] = __builtin_amdgcn_readfirstlane(count[i & 1][2 * pair + 1]);
-    };
-    const int pair0 = share, pairs = NT / 2 / shares;
-    put(0);
-    __syncthreads();
-    for (int i = 0; i < steps;) {
-        // whole pairs, then, where there are others, with their masks
-        for (; i < steps; ++i) {
-            int n[NT / 2][2];
-            bool whole = start + (i + 1) * nma::kStaged <= first_draft;
+    const auto mask = [&](int n0, int n1, int first) {
 #pragma unroll
-            for (int pair = 0; pair < NT / 2; ++pair) {
-                counted(i, pair, n[pair]);
-                whole = whole && n[pair][0] == nma::kTile && n[pair][1] == nma::kTile;
-            }
-            if (!whole)
-                break;
-            fetch(i);
-            if (busy) {
-                const uint32_t buf = (i & 1) * S::kBytes;
-                attend_pair(buf, pair0, std::false_type(), n[0], 0);
-                if (pairs == 2)
-                    attend_pair(buf, 1, std::false_type(), n[0], 0);
-            }
-            arrived(i);
-        }
-        if (i < steps) {
-            fetch(i);
-            if (busy)
-#pragma unroll 1
-                for (int pair = pair0; pair < pair0 + pairs; ++pair) {
-                    int n[2];
-                    counted(i, pair, n);
-                    attend_pair((i & 1) * S::kBytes, pair, std::true_type(), n,
-                                start + i * nma::kStaged + pair * 2 * nma::kTile);
+        for (int i = 0; i < 16; ++i)
+            s[i] = sees4(i / 8, i / 4 % 2, i / 4 % 2 ? n1 : n0, first) >> i % 4 & 1 ? s[i] : NM_NEG_INF;
+    };
+    // The values of a pair, of whose tiles n[.] tokens count, times the weights x.
+    const auto add = [&](const f32x16& weights, int part, int n0, int n1, int first) {
+        u32x4 p[2], rest[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            pack(weights, x, p[x], rest[x]);
+        // 0 * NaN must not reach a row that does not see the token: value operands with
+        // infinities or NaN are taken token by token, rows that do not see it keep their sums.
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                const u32x4 v = value(x, c, part);
+                float odd = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    odd = dot2<DT>(v[i], 0u, odd);
+                if (!__any(odd != 0.0f)) {
+                    acc[c] = mfma32<DT>(v, rest[x], mfma32<DT>(v, p[x], acc[c]));
+                    continue;
                 }
-            arrived(i);
-            ++i;
+#pragma unroll 1
+                for (int k = 0; k < 16; ++k) {                  // k index (k / 8, k % 8)
+                    const uint32_t keep = k / 8 == g ? (k % 2 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+                    u32x4 one;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        one[i] = i == k % 8 / 2 ? v[i] & keep : 0u;
+                    const int y = k / 4 % 2, in = 8 * x + 4 * (k / 8) + k % 4;
+                    const int draft = first + y * nma::kTile + in - first_draft;
+                    const bool sees = ((draft < 0) | (int)((bits >> (max(draft, 0) & 63)) & 1)) & (in < (y ? n1 : n0));
+                    const f32x16 with = mfma32<DT>(one, rest[x], mfma32<DT>(one, p[x], acc[c]));
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        acc[c][i] = sees ? with[i] : acc[c][i];
+                }
+            }
+    };
+    const auto scores = [&](int part) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            s[i] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kSteps; ++c)
+            s = mfma32<DT>(key(c, part), q[c], s);
+    };
+    // The same rounds with all conditions and masks.  (Arrays that are indexed as they run would go to LDS here, and
+    // finding their place there takes a read of the launch's packet from host memory, some 10 us a block.)
+    const auto cold_share = [&](int t) {
+        if (t >= 0) {
+            const int n0 = share ? tokens(x0, t, 2) : tokens(x0, t, 0), n1 = share ? tokens(x0, t, 3) : tokens(x0, t, 1);
+            const int first = start + t * nma::kStaged + share * 2 * nma::kTile;
+            mask(n0, n1, first);
+            make_room();
+            weigh(0, 16);
+            add(s, share, n0, n1, first);
+        }
+        if (t + 1 < steps)
+            scores(share);
+    };
+    const auto cold = [&](int t, int part) {
+        // pair 2 t + 1 + part: of stage t, or (part 1) of stage t + 1
+        const int stage = t + part, side = 1 - part;
+        if (stage >= 0 && stage < steps) {
+            const int n0 = part == 0 ? tokens(x0, t, 2) : tokens(x1, t + 1, 0);
+            const int n1 = part == 0 ? tokens(x0, t, 3) : tokens(x1, t + 1, 1);
+            mask(n0, n1, start + stage * nma::kStaged + side * 2 * nma::kTile);
+            make_room();
+        }
+        if (t >= 0) {
+            const int n0 = part == 0 ? tokens(x0, t, 0) : tokens(x0, t, 2), n1 = part == 0 ? tokens(x0, t, 1) : tokens(x0, t, 3);
+            add(w, part, n0, n1, start + t * nma::kStaged + part * 2 * nma::kTile);
+        }
+        if (stage >= 0 && stage < steps) {
+            weigh(0, 16);
+            w = s;
+        }
+        if (t + 1 < steps)
+            scores(part);
+    };
+
+    // Round t: keys of stage t + 1 and values of stage t lie in LDS, keys of t + 2 and values of t + 1 begin
+    // their way.
+    const auto begin = [&](int t) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        x0 = x1;
+        x1 = x2;
+        x2 = x3;
+        x3 = pages_of(t + 3);
+        if (t + 2 < steps) {
+            way.load_k(A, own_tile(x2, t + 2), k_buf + (t & 1) * kBytes, wave, lane);
+        }
+        if (t + 1 < steps)
+            way.load_v(A, own_tile(x1, t + 1), v_buf + (~t & 1) * kBytes, wave, lane);
+    };
+    const auto finish = [&](int t) {
+        if (t + 2 < steps)
+            way.put_k(lds + (t & 1) * kBytes, wave, lane);
+        if (t + 1 < steps)
+            way.put_v(lds + (2 + (~t & 1)) * kBytes, wave, lane);
+        k_at ^= kBytes;
+        v_at ^= kBytes;
+    };
+    way.put_k(lds, wave, lane);
+    for (int t = -1; t < steps;) {
+        begin(t);
+        if (busy) {
+            if constexpr (SHARES == 2) {
+                cold_share(t);
+            } else {
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part)
+                    cold(t, part);
+            }
+        }
+        finish(t);
+        ++t;
+        if constexpr (SHARES == 2) {
+            for (; t + 1 < steps && is_whole(x1, t); ++t) {
+                begin(t);
+                if (busy)
+                    hot_share();
+                finish(t);
+            }
+        } else {
+            for (; t + 1 < steps && is_whole(x1, t) && is_whole(x2, t + 1); ++t) {
+                begin(t);
+                if (busy) {
+                    hot(std::integral_constant<int, 0>());
+                    hot(std::integral_constant<int, 1>());
+                }
+                finish(t);
+            }
         }
     }
     sum = halves_sum(sum);
 
     // Two waves of the same rows are joined through LDS, lane to lane.
-    if (shares == 2) {
+    if constexpr (SHARES == 2) {
+        __syncthreads();                            // the last readers of what lay there
         float* const box = reinterpret_cast<float*>(lds) + wave % groups_w * (16 * kCols + 2) * 64 + lane;
         if (share == 1) {
             box[16 * kCols * 64] = mx;
@@ -311,8 +527,7 @@ __global__ __launch_bounds__(nms::kTreeWaves * 64, D == 256 ? 1 : 2) void shared
     }
     if (share != 0 || row0 + m >= R)
         return;
-    // Value operand rows 16 z + c of tile `t` of columns are column 2 t + z of group c (of D / 16 columns):
-    // the lane holds column j of group 8 a + 4 g + i in acc[j / 2][8 (j % 2) + 4 a + i].
+    // The lane holds column j of group 8 a + 4 g + i in acc[j / 2][8 (j % 2) + 4 a + i].
     if (direct) {
         const float f = sum > 0.0f || sum != sum ? A.o_scale / sum : 0.0f;
         const int64_t row = Drafts::out_row(A, h, b, r);
@@ -343,23 +558,23 @@ __global__ __launch_bounds__(nms::kTreeWaves * 64, D == 256 ? 1 : 2) void shared
         A.part_ml[part + m] = f32x2{mx, sum};
 }
 
-// Joins the ranges of 32 rows of one sequence and key head: a block takes one piece of them, a
-// lane (g, m) row m as in the partial results.  NW waves share the ranges, each keeps a reference
-// and sums of its own, and they meet in LDS.
+// Joins the ranges of 32 rows of one sequence and key head: NW waves take one piece of them, a
+// lane (g, m) row m as in the partial results.  They share the ranges, each keeps a reference and
+// sums of its own, and they meet in LDS.
 template <int DT, int D, int NW>
-__global__ __launch_bounds__(NW * 64) void shared_join_kernel(const AttnArgs A, int blocks)
+__global__ __launch_bounds__(256) void shared_join_kernel(const AttnArgs A, int units)
 {
     constexpr int kBatch = 4, kPer = D / 16, kPieces = D / 8;
-    __shared__ float tops[NW][64], sums[NW][64];
-    __shared__ f32x4 box[NW][64];
+    __shared__ float tops[4][64], sums[4][64];
+    __shared__ f32x4 box[4][64];
     const int lane = threadIdx.x % 64, m = lane % 32, g = lane / 32;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const unsigned block = flat_block();
-    if (block >= (unsigned)blocks)
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), w0 = wave % NW;
+    const unsigned unit = flat_block() * (4 / NW) + wave / NW;
+    if (unit >= (unsigned)units)
         return;
     const int R = A.G, tiles = (R + 31) / 32;
-    const int piece = block % kPieces, tile = block / kPieces % tiles;
-    const int h = block / kPieces / tiles % A.heads, b = block / kPieces / tiles / A.heads;
+    const int piece = unit % kPieces, tile = unit / kPieces % tiles;
+    const int h = unit / kPieces / tiles % A.heads, b = unit / kPieces / tiles / A.heads;
     const int len = __builtin_amdgcn_readfirstlane(min(A.lens[b], A.max_len));
     if (len < 0)
         return;
@@ -368,22 +583,19 @@ __global__ __launch_bounds__(NW * 64) void shared_join_kernel(const AttnArgs A, 
     const int64_t first = (int64_t)b * A.Hq + (int64_t)h * R + row0, step = (int64_t)A.B * A.Hq;
     float mx = NM_NEG_INF, sum = 0.0f;
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i = wave; i < parts; i += kBatch * NW) {
+    for (int i = w0; i < parts; i += kBatch * NW) {
         f32x2 x[kBatch];
         f32x4 o[kBatch];
         float top = mx;
 #pragma unroll
         for (int c = 0; c < kBatch; ++c) {
-            const int at = i + c * NW;
-            x[c] = f32x2{NM_NEG_INF, 0.0f};
-            o[c] = acc * 0.0f;
-            if (at < parts) {
-                const int64_t part = first + at * step;
-                x[c] = A.part_ml[part + row];
-                o[c] = *reinterpret_cast<const f32x4*>(A.part_o + part * D + piece_at(piece, g, nr, row));
-            }
-            top = fmaxf(top, x[c].x);
+            const int64_t part = first + min(i + c * NW, parts - 1) * step;     // (others are not added)
+            x[c] = A.part_ml[part + row];
+            o[c] = *reinterpret_cast<const f32x4*>(A.part_o + part * D + piece_at(piece, g, nr, row));
         }
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c)
+            top = i + c * NW < parts ? fmaxf(top, x[c].x) : top;
         const float ref = top == NM_NEG_INF ? 0.0f : top, f = __builtin_amdgcn_exp2f(mx - ref);
         mx = top;
         sum *= f;
@@ -398,24 +610,28 @@ __global__ __launch_bounds__(NW * 64) void shared_join_kernel(const AttnArgs A, 
                     acc[e] += o[c][e] * w;
             }
     }
-    tops[wave][lane] = mx;
-    sums[wave][lane] = sum;
-    box[wave][lane] = acc;
-    __syncthreads();
-    if (wave > 0 || m >= nr)
-        return;
+    if constexpr (NW > 1) {
+        tops[wave][lane] = mx;
+        sums[wave][lane] = sum;
+        box[wave][lane] = acc;
+        __syncthreads();
+        if (w0 > 0)
+            return;
 #pragma unroll
-    for (int w = 1; w < NW; ++w)
-        mx = fmaxf(mx, tops[w][lane]);
-    const float ref = mx == NM_NEG_INF ? 0.0f : mx;
-    sum = 0.0f;
-    acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int w = 1; w < NW; ++w)
+            mx = fmaxf(mx, tops[wave + w][lane]);
+        const float ref = mx == NM_NEG_INF ? 0.0f : mx;
+        sum = 0.0f;
+        acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        const float f = __builtin_amdgcn_exp2f(tops[w][lane] - ref);
-        sum += sums[w][lane] * f;
-        acc += box[w][lane] * f;
+        for (int w = 0; w < NW; ++w) {
+            const float f = __builtin_amdgcn_exp2f(tops[wave + w][lane] - ref);
+            sum += sums[wave + w][lane] * f;
+            acc += box[wave + w][lane] * f;
+        }
     }
+    if (m >= nr)
+        return;
     acc *= sum > 0.0f || sum != sum ? A.o_scale / sum : 0.0f;
     const int64_t out = Drafts::out_row(A, h, b, row0 + m);
     const int e = piece / (kPer / 4), column = (e / 4 * 8 + 4 * g + e % 4) * kPer + piece % (kPer / 4) * 4;
@@ -443,9 +659,17 @@ int launch(const nms::TreePlan& P, const AttnArgs& A, hipStream_t s)
     constexpr int kThreads = nms::kTreeWaves * 64;
     (void)hipGetLastError();
     if (P.shared) {
-        hipLaunchKernelGGL((shared_kernel<DT, BITS, D>), flat_grid(blocks), dim3(kThreads), 0, s, A, (int)units, P.waves,
-                           direct);
-        if (!direct)
+        if (P.waves == 4)
+            hipLaunchKernelGGL((shared_kernel<DT, BITS, D, 1>), flat_grid(blocks), dim3(kThreads), 0, s, A, (int)units, 4,
+                               direct);
+        else
+            hipLaunchKernelGGL((shared_kernel<DT, BITS, D, 2>), flat_grid(blocks), dim3(kThreads), 0, s, A, (int)units,
+                               P.waves, direct);
+        // One wave joins up to 8 ranges, four share more.
+        if (!direct && P.splits <= 8)
+            hipLaunchKernelGGL((shared_join_kernel<DT, D, 1>), flat_grid(nma::ceil_div(join, 4)), dim3(256), 0, s, A,
+                               (int)join);
+        else if (!direct)
             hipLaunchKernelGGL((shared_join_kernel<DT, D, 4>), flat_grid(join), dim3(256), 0, s, A, (int)join);
         return hipGetLastError() == hipSuccess ? NM_OK : NM_ERR_HIP;
     }
