@@ -65,6 +65,9 @@ struct PromptArgs {
     int64_t k_stride, v_stride;             // bytes
     int T, Tk, B, Hq, heads, G;
     int tiles;                              // per key head
+    int splits;                             // ranges of a tile's keys, one block each
+    f32x4* part_o;                          // partial results (more than one range)
+    f32x4* part_ml;
     // Scores are kept in base 2: q . k times `scale` = |scale| log2(e) > 0, the sign
     // (and a scale of zero) being put into q, which is exact.
     float scale;
@@ -191,27 +194,33 @@ __global__ __launch_bounds__(nms::kPromptWaves * 64, D == 256 ? 1 : 2) void prom
         return;
     // Key heads side by side, so that blocks of one share an XCD's cache where there are
     // eight; long tiles (the last ones of a sequence) first.
-    const int h = block % A.heads, tile = A.tiles - 1 - block / A.heads;
+    const int h = block % A.heads, split = block / A.heads % A.splits;
+    const int tile = A.tiles - 1 - block / A.heads / A.splits;
     const int b = find_sequence(A, tile, kRows, lane);
     const int q0 = bound(A.starts[b], A.T), nq = bound(A.starts[b + 1], A.T) - q0;
     const int k0 = bound(A.k_starts[b], A.Tk);
-    const int nk = __builtin_amdgcn_readfirstlane(max(bound(A.k_starts[b + 1], A.Tk) - k0, 0));
+    const int all_keys = max(bound(A.k_starts[b + 1], A.Tk) - k0, 0);
     const int64_t r0 = ((int64_t)tile - first_tile(A, b, kRows)) * kRows;        // the block's first row
     if (nq <= 0 || r0 >= (int64_t)nq * A.G)
         return;
     const int R = nq * A.G, row0 = (int)r0 + wave * nms::kPromptWave;
+    // The block's range: tiles of keys from `first` on, and keys counted from there.
+    const int last_key = ((int)min(r0 + kRows, (int64_t)R) - 1) / A.G + all_keys - nq;
+    const int all_tiles = max(last_key + kKeys, 0) / kKeys, per = (all_tiles + A.splits - 1) / A.splits;
+    const int first = __builtin_amdgcn_readfirstlane(min(split * per, all_tiles));
+    const int tiles = __builtin_amdgcn_readfirstlane(min(per, all_tiles - first));
+    const int key0 = first * kKeys, nk = __builtin_amdgcn_readfirstlane(all_keys - key0);
     const int r = min(row0 + m, R - 1), query = r / A.G, head = h * A.G + r % A.G;
     const int limit = query + nk - nq;                                           // the last key the lane's row sees
     // Of the wave's steps of 32 keys the first n_whole are seen by all its rows, those from n_steps on by none.
     const int all = min(row0, R - 1) / A.G + nk - nq + 1, some = min(row0 + 31, R - 1) / A.G + nk - nq + 1;
     const int n_whole = __builtin_amdgcn_readfirstlane(max(all, 0) / kPart);
-    const int n_steps = __builtin_amdgcn_readfirstlane(row0 < R ? (max(some, 0) + kPart - 1) / kPart : 0);
-    const int end = __builtin_amdgcn_readfirstlane(((int)min(r0 + kRows, (int64_t)R) - 1) / A.G + nk - nq + 1);
-    const int tiles = (max(end, 0) + kKeys - 1) / kKeys;
+    const int n_steps = __builtin_amdgcn_readfirstlane(
+        row0 < R ? min((max(some, 0) + kPart - 1) / kPart, tiles * (kKeys / kPart)) : 0);
 
     L keys, values;
-    keys.template start<true>(A.k + k0 * A.k_stride + (int64_t)h * 2 * D, A.k_stride, wave, lane);
-    values.template start<false>(A.v + k0 * A.v_stride + (int64_t)h * 2 * D, A.v_stride, wave, lane);
+    keys.template start<true>(A.k + ((int64_t)k0 + key0) * A.k_stride + (int64_t)h * 2 * D, A.k_stride, wave, lane);
+    values.template start<false>(A.v + ((int64_t)k0 + key0) * A.v_stride + (int64_t)h * 2 * D, A.v_stride, wave, lane);
     const uint32_t k_buf = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
     const uint32_t v_buf = k_buf + 2 * L::kBytes;
     if (tiles > 0)
@@ -431,6 +440,19 @@ __global__ __launch_bounds__(nms::kPromptWaves * 64, D == 256 ? 1 : 2) void prom
     if (row0 + m >= R)
         return;
     // The lane holds columns 32 c + 8 (i / 4) + 4 g + i % 4 of its row in acc[c][i].
+    if (A.splits > 1) {
+        // Partial results lie as the lanes hold them: [range][tile][key head][wave][four columns][lane] 16 bytes.
+        const int64_t part = (((int64_t)split * A.tiles + tile) * A.heads + h) * NW + wave;
+        f32x4* o = A.part_o + part * (kCols * 4) * 64 + lane;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[(c * 4 + i) * 64] = f32x4{acc[c][4 * i], acc[c][4 * i + 1], acc[c][4 * i + 2], acc[c][4 * i + 3]};
+        if (g == 0)
+            A.part_ml[part * 32 + m] = f32x4{mx, sum, plain_sum, 0.0f};
+        return;
+    }
     const float f = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
     const int64_t row = (int64_t)(q0 + query) * A.Hq + head;
     uint16_t* o = A.o + row * D + 4 * g;
@@ -445,18 +467,82 @@ __global__ __launch_bounds__(nms::kPromptWaves * 64, D == 256 ? 1 : 2) void prom
             A.lse[row] = (mx + __builtin_amdgcn_logf(plain_sum)) * kLn2;
 }
 
+// Joins the ranges of a tile: a block takes four columns (piece) of every lane, a wave the rows
+// that a wave of the tile's blocks had.
+template <int DT, int D, bool LSE>
+__global__ __launch_bounds__(nms::kPromptWaves * 64) void prompt_join_kernel(const PromptArgs A, int blocks)
+{
+    constexpr int NW = nms::kPromptWaves, kPieces = D / 8, kRows = NW * nms::kPromptWave, kBatch = 4;
+    const int lane = threadIdx.x % 64, m = lane % 32, g = lane / 32;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int block = (int)flat_block();
+    if (block >= blocks)
+        return;
+    const int piece = block % kPieces, h = block / kPieces % A.heads, tile = block / kPieces / A.heads;
+    const int b = find_sequence(A, tile, kRows, lane);
+    const int q0 = bound(A.starts[b], A.T), nq = bound(A.starts[b + 1], A.T) - q0;
+    const int64_t r = ((int64_t)tile - first_tile(A, b, kRows)) * kRows + wave * nms::kPromptWave + m;
+    if (nq <= 0 || r >= (int64_t)nq * A.G)
+        return;
+    const int64_t part0 = ((int64_t)tile * A.heads + h) * NW + wave, step = (int64_t)A.tiles * A.heads * NW;
+    float mx = NM_NEG_INF, sum = 0.0f, plain_sum = 0.0f;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < A.splits; i += kBatch) {
+        f32x4 x[kBatch], o[kBatch];
+        float top = mx;
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+            const int64_t part = part0 + min(i + c, A.splits - 1) * step;           // (others are not added)
+            x[c] = A.part_ml[part * 32 + m];
+            o[c] = A.part_o[(part * kPieces + piece) * 64 + lane];
+        }
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c)
+            top = i + c < A.splits ? fmaxf(top, x[c].x) : top;
+        const float ref = top == NM_NEG_INF ? 0.0f : top, f = __builtin_amdgcn_exp2f(mx - ref);
+        mx = top;
+        sum *= f;
+        plain_sum *= f;
+        acc *= f;
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c)
+            if (i + c < A.splits) {
+                const float w = __builtin_amdgcn_exp2f(x[c].x - ref);
+                sum += x[c].y * w;
+                plain_sum += x[c].z * w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[e] += o[c][e] * w;
+            }
+    }
+    acc *= sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    const int64_t row = (q0 + r / A.G) * A.Hq + h * A.G + r % A.G;
+    *reinterpret_cast<u32x2*>(A.o + row * D + piece / 4 * 32 + piece % 4 * 8 + 4 * g) =
+        u32x2{pack2<DT>(acc[0], acc[1]), pack2<DT>(acc[2], acc[3])};
+    if constexpr (LSE)
+        if (g == 0 && piece == 0)
+            A.lse[row] = (mx + __builtin_amdgcn_logf(plain_sum)) * kLn2;
+}
+
 template <int DT, int D>
 int launch(const nms::PromptPlan& P, const PromptArgs& A, hipStream_t s)
 {
-    const int64_t blocks = P.tiles * A.heads;
-    if (blocks > INT32_MAX)
+    const int64_t blocks = P.tiles * P.splits * A.heads, join = P.tiles * A.heads * (D / 8);
+    if (blocks > INT32_MAX || (P.splits > 1 && join > INT32_MAX))
         return NM_ERR_BAD_SHAPE;
     constexpr int kThreads = nms::kPromptWaves * 64;
+    const auto run = [&](auto kernel, int64_t n) {
+        hipLaunchKernelGGL(kernel, flat_grid(n), dim3(kThreads), 0, s, A, (int)n);
+    };
     (void)hipGetLastError();
     if (A.lse)
-        hipLaunchKernelGGL((prompt_kernel<DT, D, true>), flat_grid(blocks), dim3(kThreads), 0, s, A, (int)blocks);
+        run(prompt_kernel<DT, D, true>, blocks);
     else
-        hipLaunchKernelGGL((prompt_kernel<DT, D, false>), flat_grid(blocks), dim3(kThreads), 0, s, A, (int)blocks);
+        run(prompt_kernel<DT, D, false>, blocks);
+    if (P.splits > 1 && A.lse)
+        run(prompt_join_kernel<DT, D, true>, join);
+    else if (P.splits > 1)
+        run(prompt_join_kernel<DT, D, false>, join);
     return hipGetLastError() == hipSuccess ? NM_OK : NM_ERR_HIP;
 }
 
@@ -475,7 +561,7 @@ int launch_width(const nms::PromptPlan& P, const PromptArgs& A, int D, hipStream
 int nmk::attn_prompt(const nms::PromptPlan& plan, const void* q, int64_t q_stride, int64_t T, const void* k,
                      int64_t k_stride, const void* v, int64_t v_stride, int64_t Tk, const int32_t* starts,
                      const int32_t* k_starts, int64_t B, int Hq, int heads, int D, int dtype, float scale, void* o,
-                     float* lse, void*, void* stream)
+                     float* lse, void* workspace, void* stream)
 {
     PromptArgs A;
     A.q = static_cast<const uint16_t*>(q);
@@ -495,6 +581,9 @@ int nmk::attn_prompt(const nms::PromptPlan& plan, const void* q, int64_t q_strid
     A.heads = heads;
     A.G = plan.G;
     A.tiles = (int)plan.tiles;
+    A.splits = (int)plan.splits;
+    A.part_ml = static_cast<f32x4*>(workspace);
+    A.part_o = A.part_ml + plan.splits * plan.tiles * heads * nms::kPromptRows;
     A.scale = scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e;
     A.q_and = scale == 0.0f ? 0u : 0xFFFFFFFFu;
     A.q_xor = scale < 0.0f ? 0x80008000u : 0u;

@@ -82,7 +82,7 @@ int nm_attn_prompt(const void* q, int64_t q_stride, int64_t T, const void* k, in
         !stride_ok(Tk, v_stride, kw, nms::kPromptMaxStride) || !(std::fabs(scale) <= 1e30f))
         return NM_ERR_BAD_SHAPE;
     const nms::PromptPlan plan = nms::prompt_plan(T, Tk, B, Hq, heads, D);
-    const int64_t need = nms::prompt_workspace(plan, D);
+    const int64_t need = nms::prompt_workspace(plan, heads, D);
     const size_t sb = B > 0 ? (size_t)(B + 1) * 4 : 0;
     const Buf ins[5] = {{q, rows_bytes(T, q_stride, qw)}, {k, rows_bytes(Tk, k_stride, kw)},
                         {v, rows_bytes(Tk, v_stride, kw)}, {starts, sb}, {k_starts, k_starts ? sb : 0}};

@@ -164,10 +164,10 @@ def test_large_values(nm, dtype):
 
 def reordered(got, want, v):
     """Equal but for the order of the fp32 sums.  A step with infinities or NaN among its values adds them up key by
-    key: the terms w v are the same, two orders of at most 150 of them differ by at most 2 * 150 * 2^-24 of the sum of
-    |w v| over the sum of w, which is at most max |v|; then both are rounded, half a step each."""
+    key: the terms w v are the same, two orders of n of them differ by at most 2 n 2^-24 of the sum of |w v| over the sum
+    of w, which is at most max |v|; then both are rounded, half a step each."""
     got, want = got.double(), want.double()
-    near = 2 * 150 * 2.0 ** -24 * v[v.isfinite()].double().abs().max()
+    near = 2 * max(150, v.shape[0]) * 2.0 ** -24 * v[v.isfinite()].double().abs().max()
     unit = ref.UNIT[v.dtype]
     return bool(((got - want).abs() <= near + unit * (2 * want.abs() + near) + 2 * ref.TINY[v.dtype]).all())
 
@@ -220,16 +220,49 @@ def test_far_rows(nm):
     q = rnd((200, 2, D), F16, 1)
     k[-200:], v[-200:] = rnd((200, 1, D), F16, 2), rnd((200, 1, D), F16, 3)
     st = torch.tensor([rows - 200, rows], dtype=torch.int32, device="cuda")
-    out = nm.attn_prompt(q, k, v, starts_of([200]), st)
-    assert torch.equal(out, nm.attn_prompt(q, k[-200:], v[-200:], starts_of([200])))
+
+    def same(out, qq, kk, vv):
+        n = qq.shape[0]
+        o, _, tol, _ = sref.prompt(ref.f64(qq), ref.f64(kk), ref.f64(vv), [0, n], [0, n], D ** -0.5, F16)
+        sref.close(ref.f64(out), o, tol, "far")
+
+    same(nm.attn_prompt(q, k, v, starts_of([200]), st), q, k[-200:], v[-200:])
     # and of widely strided rows
     big = torch.empty((40, 1 << 27), dtype=F16, device="cuda")
     kk = big[:, 64:64 + D].unflatten(1, (1, D))
     kk.copy_(k[-40:])
     vv = big[:, 1024:1024 + D].unflatten(1, (1, D))
     vv.copy_(v[-40:])
-    assert torch.equal(nm.attn_prompt(q[-40:], kk, vv, starts_of([40])),
-                       nm.attn_prompt(q[-40:], k[-40:], v[-40:], starts_of([40])))
+    same(nm.attn_prompt(q[-40:], kk, vv, starts_of([40])), q[-40:], k[-40:], v[-40:])
+
+
+@pytest.mark.parametrize("dtype,D,hq,heads", [(BF16, 128, 4, 1), (F16, 64, 3, 3), (F16, 256, 2, 1)])
+@pytest.mark.parametrize("pieces", [[(1, 5000)], [(40, 3001), (7, 20), (0, 900), (3, 2)], [(130, 4097)]])
+def test_few_rows_behind_many_keys(nm, dtype, D, hq, heads, pieces):
+    """Keys cut into ranges that a second launch joins; some sequences shorter than the ranges are many."""
+    nq, nk = zip(*pieces)
+    q, k, v = (rnd((n, h, D), dtype, "few", n, i) for i, (n, h) in enumerate(((sum(nq), hq), (sum(nk), heads), (sum(nk), heads))))
+    ws = nm.attn_prompt_workspace(sum(nq), sum(nk), len(nq), hq, heads, D)
+    assert ws.numel() > 0
+    ws.fill_(255)
+    out = check(nm, q, k, v, starts_of(nq), starts_of(nk), ws=ws)
+    assert torch.equal(out, nm.attn_prompt(q, k, v, starts_of(nq), starts_of(nk)))
+    with pytest.raises(nm.NmError):
+        nm.attn_prompt(q, k, v, starts_of(nq), starts_of(nk), ws=ws[:256])
+
+
+def test_masked_in_ranges(nm):
+    """NaN and infinities behind the rows' last keys, in the last of many ranges; zeros where no range has a key."""
+    q, k, v = rnd((20, 2, 64), BF16, "r"), rnd((4000, 1, 64), BF16, "k"), rnd((4000, 1, 64), BF16, "v")
+    clean = nm.attn_prompt(q, k, v, starts_of([20]), starts_of([4000]))
+    k[3990:] = math.nan
+    v[3990:] = math.inf
+    got = nm.attn_prompt(q, k, v, starts_of([20]), starts_of([4000]))
+    assert got[:10].isfinite().all() and reordered(got[:10], clean[:10], v[:3990])
+    assert not got[10:].isfinite().any()
+    out = torch.full_like(q, 7.0)
+    nm.attn_prompt(q, k[:3000], v[:3000], starts_of([20]), starts_of([0]), out=out)
+    assert not out.any()
 
 
 def test_long_prompt_rows(nm):
