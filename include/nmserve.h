@@ -101,9 +101,9 @@ int nm_kv_plan(const nm_kv_pages* pages, const int32_t* adds, int64_t rows, int3
  * Infinities and NaN in a key or value that a query does not see do not reach it; in
  * one that it sees they have the effect that the formula gives them, and so have fp32
  * sums that overflow.  Results do not depend on other calls and repeat bit for bit.
- * T and Tk 0 .. 2^31 - 1, B 0 .. 65535, Hq and heads 1 .. 65535, T * Hq / heads below
- * 2^31 - 2^16, T * Hq * D and Tk * heads * D below 2^40, row strides up to 2^28 elements,
- * |scale| <= 1e30.  o, lse and workspace must not overlap anything else.
+ * B 0 .. 65535, Hq and heads 1 .. 65535, B * heads below 2^30, T * Hq / heads and Tk
+ * below 2^31 - 2^16, T * Hq * D and Tk * heads * D below 2^40, row strides up to 2^28
+ * elements, |scale| <= 1e30.  o, lse and workspace must not overlap anything else.
  */
 int64_t nm_attn_prompt_workspace_bytes(int64_t T, int64_t Tk, int64_t B, int Hq, int heads, int D);
 int nm_attn_prompt(const void* q, int64_t q_stride, int64_t T, const void* k, int64_t k_stride, const void* v,

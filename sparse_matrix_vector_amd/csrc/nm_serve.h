@@ -34,7 +34,8 @@ constexpr int kPromptWave = 32;                 // rows of a wave
 constexpr int kPromptWaves = 4;
 constexpr int kPromptRows = kPromptWave * kPromptWaves;
 constexpr int64_t kPromptMaxStride = int64_t(1) << 28;
-constexpr int64_t kPromptMaxRows = (int64_t(1) << 31) - (int64_t(1) << 16);     // T * G
+constexpr int64_t kPromptMaxRows = (int64_t(1) << 31) - (int64_t(1) << 16);     // T * G, and Tk
+constexpr int64_t kPromptMaxHeads = int64_t(1) << 30;                           // B * heads
 
 struct PromptPlan {
     int G;

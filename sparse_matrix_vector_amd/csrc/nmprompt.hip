@@ -344,7 +344,6 @@ __global__ __launch_bounds__(nms::kPromptWaves * 64, D == 256 ? 1 : 2) void prom
 #pragma unroll
             for (int i = 4 * x; i < 4 * x + 4; ++i)
                 w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], A.scale, -ref));
-            
             __builtin_amdgcn_sched_barrier(0);
         }
         s = next;
@@ -528,8 +527,6 @@ template <int DT, int D>
 int launch(const nms::PromptPlan& P, const PromptArgs& A, hipStream_t s)
 {
     const int64_t blocks = P.tiles * P.splits * A.heads, join = P.tiles * A.heads * (D / 8);
-    if (blocks > INT32_MAX || (P.splits > 1 && join > INT32_MAX))
-        return NM_ERR_BAD_SHAPE;
     constexpr int kThreads = nms::kPromptWaves * 64;
     const auto run = [&](auto kernel, int64_t n) {
         hipLaunchKernelGGL(kernel, flat_grid(n), dim3(kThreads), 0, s, A, (int)n);

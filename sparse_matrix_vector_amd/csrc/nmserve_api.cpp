@@ -22,8 +22,9 @@ bool heads_ok(int Hq, int heads, int D)
 
 bool prompt_shape_ok(int64_t T, int64_t Tk, int64_t B, int Hq, int heads, int D)
 {
-    return heads_ok(Hq, heads, D) && T >= 0 && T <= INT32_MAX && Tk >= 0 && Tk <= INT32_MAX && B >= 0 && B <= 65535 &&
-           T * (Hq / heads) < nms::kPromptMaxRows && T * Hq * D < kMaxElements && Tk * heads * D < kMaxElements;
+    return heads_ok(Hq, heads, D) && T >= 0 && T <= INT32_MAX && Tk >= 0 && Tk < nms::kPromptMaxRows && B >= 0 &&
+           B <= 65535 && B * heads < nms::kPromptMaxHeads && T * (Hq / heads) < nms::kPromptMaxRows &&
+           T * Hq * D < kMaxElements && Tk * heads * D < kMaxElements;
 }
 
 bool tree_shape_ok(int64_t B, int N, int Hq, int heads, int D, int format, int64_t max_len)

@@ -653,8 +653,6 @@ int launch(const nms::TreePlan& P, const AttnArgs& A, hipStream_t s)
     const int64_t blocks = P.shared ? nma::ceil_div(units, 8) * 8 * P.groups : units * P.groups;
     const int64_t join = P.shared ? (int64_t)A.B * A.heads * nma::ceil_div(A.G, 32) * (D / 8)
                                   : nma::ceil_div((int64_t)A.B * A.G, 16) * A.heads * (D / 16);
-    if (blocks > INT32_MAX || join > INT32_MAX)
-        return NM_ERR_BAD_SHAPE;
     const int direct = P.direct ? 1 : 0;
     constexpr int kThreads = nms::kTreeWaves * 64;
     (void)hipGetLastError();
