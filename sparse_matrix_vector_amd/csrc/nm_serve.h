@@ -91,9 +91,12 @@ inline int64_t prompt_workspace_bound(int64_t T, int64_t Tk, int64_t B, int Hq, 
 // Units of (rows of a sequence and key head, range of its tokens), one block each, in two
 // forms (nmtree.hip).
 constexpr int kTreeWaves = 4;
-constexpr int64_t kTreeRange = 4096;            // tokens of a range at most
+// Tokens of a range at most (us with 1024 / 2048 / 4096: 16 sequences of 24 drafts, 4 heads a key head, up to
+// 8192 tokens, MX8 104 / 109 / 109; 4 of 64 drafts, 16384 tokens, 16-bit 148 / 135 / 134).
+constexpr int64_t kTreeRange = 4096;
 
-// Blocks that fill the GPU.
+// Blocks that fill the GPU: two a CU, but one where a block of the shared form takes a CU's registers and
+// LDS (256 columns), and one where the plain form has enough units without ranges to give each CU one.
 inline int64_t tree_blocks(bool shared, int D, int64_t units)
 {
     return shared && D == 256 ? nma::kCus : shared || units < nma::kCus ? 2 * nma::kCus : nma::kCus;
@@ -118,7 +121,11 @@ inline TreePlan tree_plan(int64_t B, int N, int Hq, int heads, int D, int64_t ma
     p.waves = p.rows <= 32 ? 1 : p.rows <= 64 ? 2 : 4;
     p.groups = ceil_div(p.rows, 32 * p.waves);
     const int64_t units = B * heads * p.groups;
-    nma::cut(max_len, units, tree_blocks(p.shared, D, units), kTreeRange, &p.splits, &p.chunk);
+    // Few tokens are one range: a second launch costs more than it spreads (8 key heads of 128
+    // columns, 16-bit, us in one range / ranges of 128: one sequence of 32 rows, 256 tokens 8.5 / 10.4,
+    // 512 10.3 / 10.5, 1024 14.0 / 10.6; four of 128 rows, 256 tokens 17.0 / 18.6, 512 22.9 / 21.2).
+    const int64_t blocks = max_len <= (p.shared ? 256 : 512) ? 1 : tree_blocks(p.shared, D, units);
+    nma::cut(max_len, units, blocks, kTreeRange, &p.splits, &p.chunk);
     p.direct = p.splits <= 1;
     if (p.direct)
         p.splits = 1;
