@@ -88,7 +88,8 @@ int nm_kv_plan(const nm_kv_pages* pages, const int32_t* adds, int64_t rows, int3
  *     behind nk - nq earlier tokens (nm_kv_read gives their rows).
  *   starts, k_starts   int32 [B + 1], not decreasing, 0 .. T and 0 .. Tk (bounds
  *     outside count as the nearest of these, a sequence that ends before it starts
- *     as empty).  k_starts NULL: starts, and Tk is T.
+ *     as empty; starts that decrease say nothing about which rows of o are written,
+ *     but no others than o's and lse's are).  k_starts NULL: starts, and Tk is T.
  *   o [T][Hq][D]       contiguous, 16-byte aligned; a query that sees no key gets
  *     zeros.  Rows that no sequence has are left as they are.
  *   lse [T][Hq]        fp32 (natural log of the softmax's sum; -inf where no key is

@@ -17,6 +17,13 @@
 // its k index (g, j) means key 4 g + j for j < 4 and 8 + 4 g + j - 4 for j >= 4; the
 // values are read from LDS in that order by transposing reads.
 //
+// A weight enters the second product as one 16-bit operand, where the paged cache's attention has
+// two (the rounding and the rest, nm_attn_units.h).  A prompt's products are what bounds it, and
+// the second operand would make them half as many again; one loses half a step of each weight, as
+// much as rounding the output does (error against 64 bits 1.25 to 1.44 times that rounding's).  So that
+// the weights still add up to one, the sum they are divided by adds the rounded ones; lse adds
+// them as they were.
+//
 // Keys and values go from memory to LDS directly (global_load_lds, 1 KB a wave and
 // instruction), one tile ahead.  Rows lie in LDS as in memory but for an exclusive
 // or of their 16-byte pieces' numbers with the row's, which keeps the banks apart:
@@ -201,7 +208,7 @@ __global__ __launch_bounds__(nms::kPromptWaves * 64, D == 256 ? 1 : 2) void prom
     const int k0 = bound(A.k_starts[b], A.Tk);
     const int all_keys = max(bound(A.k_starts[b + 1], A.Tk) - k0, 0);
     const int64_t r0 = ((int64_t)tile - first_tile(A, b, kRows)) * kRows;        // the block's first row
-    if (nq <= 0 || r0 >= (int64_t)nq * A.G)
+    if (nq <= 0 || r0 < 0 || r0 >= (int64_t)nq * A.G)           // (below 0: starts that decrease)
         return;
     const int R = nq * A.G, row0 = (int)r0 + wave * nms::kPromptWave;
     // The block's range: tiles of keys from `first` on, and keys counted from there.
@@ -480,8 +487,8 @@ __global__ __launch_bounds__(nms::kPromptWaves * 64) void prompt_join_kernel(con
     const int piece = block % kPieces, h = block / kPieces % A.heads, tile = block / kPieces / A.heads;
     const int b = find_sequence(A, tile, kRows, lane);
     const int q0 = bound(A.starts[b], A.T), nq = bound(A.starts[b + 1], A.T) - q0;
-    const int64_t r = ((int64_t)tile - first_tile(A, b, kRows)) * kRows + wave * nms::kPromptWave + m;
-    if (nq <= 0 || r >= (int64_t)nq * A.G)
+    const int64_t r0 = ((int64_t)tile - first_tile(A, b, kRows)) * kRows, r = r0 + wave * nms::kPromptWave + m;
+    if (nq <= 0 || r0 < 0 || r >= (int64_t)nq * A.G)
         return;
     const int64_t part0 = ((int64_t)tile * A.heads + h) * NW + wave, step = (int64_t)A.tiles * A.heads * NW;
     float mx = NM_NEG_INF, sum = 0.0f, plain_sum = 0.0f;

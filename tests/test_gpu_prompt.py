@@ -113,6 +113,19 @@ def test_gaps_and_bad_bounds(nm):
     assert (out == 0).all()                                             # no keys
 
 
+@pytest.mark.parametrize("tk", (200, 9000))
+def test_starts_that_decrease(nm, tk):
+    """No rows are written but those of o and lse, with and without ranges of keys."""
+    q = torch.cat([rnd((200, 8, 64), BF16, i) for i in range(3)])[200:400]
+    k, v = rnd((tk, 1, 64), BF16, 2), rnd((tk, 1, 64), BF16, 3)
+    for starts in ([0, 100, 120, 10, 200], [5, 200, 0, 200, 0], [200, 190, 180, 5, 6, 7], [0, 180, 20, 30, 40, 0, 200, 1]):
+        st = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        out, lse = torch.full((600, 8, 64), 7.0, dtype=BF16, device="cuda"), torch.full((600, 8), 7.0, device="cuda")
+        nm.attn_prompt(q, k, v, st, starts_of([tk] + [0] * (len(starts) - 2)), out=out[200:400], lse=lse[200:400])
+        for t in (out, lse):
+            assert (t[:200] == 7).all() and (t[400:] == 7).all()
+
+
 def test_no_rows(nm):
     q, k = torch.empty((0, 4, 64), dtype=F16, device="cuda"), torch.empty((0, 2, 64), dtype=F16, device="cuda")
     assert nm.attn_prompt(q, k, k, starts_of([0])).shape == (0, 4, 64)
