@@ -49,10 +49,8 @@ struct Request {
     bool live;
 };
 
-__device__ __forceinline__ Request request(const PlanArgs& A, int b)
+__device__ __forceinline__ Request request(const PlanArgs& A, int len, int64_t add)
 {
-    const int len = A.lens[b];
-    const int64_t add = A.adds[b];
     Request q;
     q.live = len >= 0;
     q.len = max(len, 0);
@@ -66,6 +64,11 @@ __device__ __forceinline__ Request request(const PlanArgs& A, int b)
     q.want = fits ? (int)need - q.held : 0;
     return q;
 }
+
+__device__ __forceinline__ Request request(const PlanArgs& A, int b) { return request(A, A.lens[b], A.adds[b]); }
+
+// Four int32 of a thread, at any 4-byte aligned address.
+typedef int i32x4 __attribute__((ext_vector_type(4), aligned(4)));
 
 // What sequences give back and ask for, added up: pages (below 2^31, as B * width is) and rows,
 // of which more than `most` = rows + 1 count as that many (they do not fit whatever follows).
@@ -160,7 +163,7 @@ template <int NT, int EACH>
 __global__ __launch_bounds__(NT) void plan_kernel(const PlanArgs A, int with_rows)
 {
     __shared__ Sums sums[NT + 1], waves[NT / 64];
-    __shared__ int held_of[EACH == 1 ? NT : 1], len_of[EACH == 1 ? NT : 1];
+    __shared__ int held_of[EACH == 1 ? NT : 1], len_of[EACH == 1 ? NT : 1], kept_of[EACH == 1 ? NT : 1];
     __shared__ int stop;
     __shared__ uint32_t stop_rows, stop_pages;
     constexpr int kKept = EACH ? EACH : 1;
@@ -174,14 +177,25 @@ __global__ __launch_bounds__(NT) void plan_kernel(const PlanArgs A, int with_row
     Sums own = {0, 0, 0};
     const auto asked = [&](const Request& q) { return Sums{(uint32_t)q.freed, (uint32_t)q.want, (uint32_t)q.grow}; };
     const auto count = [&](const Request& q) { own = plus(own, asked(q), most); };
+    int32_t first[kKept];               // the first page that each gives back
+    i32x4 lens = {-1, -1, -1, -1}, adds = {0, 0, 0, 0};
     if constexpr (EACH > 0) {
+        if (EACH == 4 && b0 + 4 <= b1) {
+            lens = *reinterpret_cast<const i32x4*>(A.lens + b0);
+            adds = *reinterpret_cast<const i32x4*>(A.adds + b0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                if (b0 + i < b1) {
+                    lens[i] = A.lens[b0 + i];
+                    adds[i] = A.adds[b0 + i];
+                }
+        }
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
-            kept[i] = Request{-1, 0, 0, 0, 0, 0, false};
-            if (b0 + i < b1) {
-                kept[i] = request(A, b0 + i);
-                count(kept[i]);
-            }
+            kept[i] = request(A, (int)lens[i], (int)adds[i]);       // a padding row behind the last
+            first[i] = kept[i].freed > 0 ? A.table[(int64_t)(b0 + i) * A.width + kept[i].held - kept[i].freed] : 0;
+            count(kept[i]);
         }
     } else {
         for (int b = b0; b < b1; ++b)
@@ -210,14 +224,6 @@ __global__ __launch_bounds__(NT) void plan_kernel(const PlanArgs A, int with_row
     };
     if (all.freed > 0) {
         if (__syncthreads_and(own.freed <= 8)) {
-            // the first pages' loads do not wait for one another's stores
-            int32_t first[kKept];
-            if constexpr (EACH > 0) {
-#pragma unroll
-                for (int i = 0; i < EACH; ++i)
-                    first[i] = kept[i].freed > 0
-                                   ? A.table[(int64_t)(b0 + i) * A.width + kept[i].held - kept[i].freed] : 0;
-            }
             int64_t k = before.freed;
             walk([&](int b, const Request& q) {
                 for (int in = 0; in < q.freed; ++in, ++k) {
@@ -231,7 +237,7 @@ __global__ __launch_bounds__(NT) void plan_kernel(const PlanArgs A, int with_row
             });
         } else if constexpr (EACH == 1) {
             // four at a time, so that their loads do not wait for one another
-            held_of[tid] = kept[0].held - kept[0].freed;
+            kept_of[tid] = kept[0].held - kept[0].freed;
             __syncthreads();
             for (int64_t k0 = tid; k0 < all.freed; k0 += 4 * NT) {
                 int32_t page[4];
@@ -241,7 +247,7 @@ __global__ __launch_bounds__(NT) void plan_kernel(const PlanArgs A, int with_row
                     page[i] = 0;
                     if (k < all.freed) {
                         const int b = above([&](int t) { return sums[t + 1].freed; }, NT, k);
-                        page[i] = A.table[(int64_t)b * A.width + held_of[b] + (k - sums[b].freed)];
+                        page[i] = A.table[(int64_t)b * A.width + kept_of[b] + (k - sums[b].freed)];
                     }
                 }
 #pragma unroll
@@ -251,7 +257,6 @@ __global__ __launch_bounds__(NT) void plan_kernel(const PlanArgs A, int with_row
                         A.free[top - k] = page[i];
                 }
             }
-            __syncthreads();
         } else {
             for (int64_t k = tid; k < all.freed; k += NT) {
                 const int t = above([&](int i) { return sums[i + 1].freed; }, NT, k);
@@ -264,6 +269,7 @@ __global__ __launch_bounds__(NT) void plan_kernel(const PlanArgs A, int with_row
                 }
                 give(k, b, q, in);
             }
+            __syncthreads();                        // others' lens are read here
         }
     }
     const uint32_t room = (uint32_t)min(top + 1, (int64_t)A.n_pages);
@@ -297,9 +303,35 @@ __global__ __launch_bounds__(NT) void plan_kernel(const PlanArgs A, int with_row
         got_rows = stop_rows;
         got_pages = stop_pages;
     }
-    if (all.freed > 0)
-        __syncthreads();                                // lens is read for the pages above
-    {
+    if constexpr (EACH == 4) {
+        Sums x = before;
+        i32x4 pops, granted, ends;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Request& q = kept[i];
+            const bool ok = b0 + i < last;
+            granted[i] = (ok ? q.grow : 0) - q.drop;
+            lens[i] = granted[i] != 0 ? q.len + granted[i] : lens[i];
+            pops[i] = (int)min(x.want, room);
+            x = plus(x, asked(q), most);
+            ends[i] = (int)(ok ? x.grow : got_rows);
+        }
+        if (b0 + 4 <= b1) {
+            *reinterpret_cast<i32x4*>(A.first_pop + b0) = pops;
+            *reinterpret_cast<i32x4*>(A.granted + b0) = granted;
+            *reinterpret_cast<i32x4*>(A.starts + b0 + 1) = ends;
+            *reinterpret_cast<i32x4*>(A.lens + b0) = lens;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (b0 + i < b1) {
+                    A.first_pop[b0 + i] = pops[i];
+                    A.granted[b0 + i] = granted[i];
+                    A.starts[b0 + i + 1] = ends[i];
+                    A.lens[b0 + i] = lens[i];
+                }
+        }
+    } else {
         Sums x = before;
         walk([&](int b, const Request& q) {
             const bool ok = b < last;
