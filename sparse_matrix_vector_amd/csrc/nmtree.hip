@@ -67,14 +67,15 @@ __device__ __forceinline__ int64_t piece_at(int piece, int g, int nr, int m)
     return ((int64_t)(piece * 2 + g) * nr + m) * 4;
 }
 
-// One wave's tile on its way to LDS.  16-bit rows go there directly (global_load_lds), as they
-// lie in the cache; codes through registers, as operands.  In LDS:
+// One wave's tile on its way to LDS.  16-bit rows go there directly (global_load_lds, 1 KB an
+// instruction), as they lie in the cache; codes through registers, as operands.  In LDS:
 //   keys    [tile][column piece of 8, token] 16 bytes; the tokens m of odd tiles are stored at m ^ 8 (banks)
 //   values  16-bit: [tile][column j of a group][quarter][group] 8 bytes (four tokens);
 //           codes: [pair][column j][quarter][group] 16 bytes (four tokens of each tile)
 template <int DT, int BITS, int D>
 struct Way {
     using S = Stage<DT, BITS, D, nms::kTreeWaves>;
+    static constexpr bool kCodes = BITS != 16;
     static constexpr int kBytes = nms::kTreeWaves * S::kTileBytes;        // keys, or values, of four tiles
     S stage;
 
@@ -82,34 +83,27 @@ struct Way {
     {
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
-            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds + i * 1024),
-                         "v"(tile + i * 1024 + (lane ^ turned) * 16)
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
+                             __builtin_amdgcn_readfirstlane(lds + i * 1024)),
+                         "v"((lane ^ turned) * 16), "s"(tile + i * 1024)
                          : "memory");
     }
     __device__ __forceinline__ void load_k(const AttnArgs& A, const TileRef& t, uint32_t lds, int wave, int lane)
     {
-        if constexpr (BITS == 16)
-            direct(lds + wave * S::kTileBytes, A.k + t.tile * nma::tile_bytes(D, BITS), lane, wave % 2 * 8);
-        else
+        if constexpr (kCodes)
             stage.load_k(A, t, 0, lane);
+        else
+            direct(lds + wave * S::kTileBytes, A.k + t.tile * nma::tile_bytes(D, BITS), lane, wave % 2 * 8);
     }
     __device__ __forceinline__ void load_v(const AttnArgs& A, const TileRef& t, uint32_t lds, int wave, int lane)
     {
-        if constexpr (BITS == 16)
-            direct(lds + wave * S::kTileBytes, A.v + t.tile * nma::tile_bytes(D, BITS), lane, 0);
-        else
+        if constexpr (kCodes)
             stage.load_v(A, t, 0, lane);
+        else
+            direct(lds + wave * S::kTileBytes, A.v + t.tile * nma::tile_bytes(D, BITS), lane, 0);
     }
-    __device__ __forceinline__ void put_k(uint8_t* buf, int wave, int lane) const
-    {
-        if constexpr (BITS != 16)
-            stage.put_k(buf, wave, 0, lane, true);
-    }
-    __device__ __forceinline__ void put_v(uint8_t* buf, int wave, int lane) const
-    {
-        if constexpr (BITS != 16)
-            stage.put_v(buf, wave, 0, lane);
-    }
+    __device__ __forceinline__ void put_k(uint8_t* buf, int wave, int lane) const { stage.put_k(buf, wave, 0, lane, true); }
+    __device__ __forceinline__ void put_v(uint8_t* buf, int wave, int lane) const { stage.put_v(buf, wave, 0, lane); }
 };
 
 template <int DT, int BITS, int D, int SHARES>
@@ -444,8 +438,10 @@ __global__ __launch_bounds__(nms::kTreeWaves * 64, D == 256 ? 1 : 2) void shared
             scores(part);
     };
 
-    // Round t: keys of stage t + 1 and values of stage t lie in LDS, keys of t + 2 and values of t + 1 begin
-    // their way.
+    // Round t: keys of stage t + 1 and values of stage t lie in LDS, keys of t + 2 and values of t + 1 begin their
+    // way.  (Codes without conditions: behind the last stage they are page 0's, which nobody looks at.  With
+    // branches between the products and the loop's end the compiler keeps the sums twice and spills.  Codes
+    // loaded a whole round ahead, at the end of the one before or through LDS, take as long: 102 to 105 us for 100.)
     const auto begin = [&](int t) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
@@ -454,48 +450,48 @@ __global__ __launch_bounds__(nms::kTreeWaves * 64, D == 256 ? 1 : 2) void shared
         x1 = x2;
         x2 = x3;
         x3 = pages_of(t + 3);
-        if (t + 2 < steps) {
+        if (W::kCodes || t + 2 < steps)
             way.load_k(A, own_tile(x2, t + 2), k_buf + (t & 1) * kBytes, wave, lane);
-        }
-        if (t + 1 < steps)
+        if (W::kCodes || t + 1 < steps)
             way.load_v(A, own_tile(x1, t + 1), v_buf + (~t & 1) * kBytes, wave, lane);
     };
     const auto finish = [&](int t) {
-        if (t + 2 < steps)
+        if constexpr (W::kCodes) {
             way.put_k(lds + (t & 1) * kBytes, wave, lane);
-        if (t + 1 < steps)
             way.put_v(lds + (2 + (~t & 1)) * kBytes, wave, lane);
+        }
         k_at ^= kBytes;
         v_at ^= kBytes;
     };
-    way.put_k(lds, wave, lane);
-    for (int t = -1; t < steps;) {
+    if constexpr (W::kCodes)
+        way.put_k(lds, wave, lane);
+    if (!busy)                                      // a wave without rows only loads
+        for (int t = -1; t < steps; ++t) {
+            begin(t);
+            finish(t);
+        }
+    for (int t = busy ? -1 : steps; t < steps;) {
         begin(t);
-        if (busy) {
-            if constexpr (SHARES == 2) {
-                cold_share(t);
-            } else {
+        if constexpr (SHARES == 2) {
+            cold_share(t);
+        } else {
 #pragma unroll 1
-                for (int part = 0; part < 2; ++part)
-                    cold(t, part);
-            }
+            for (int part = 0; part < 2; ++part)
+                cold(t, part);
         }
         finish(t);
         ++t;
         if constexpr (SHARES == 2) {
             for (; t + 1 < steps && is_whole(x1, t); ++t) {
                 begin(t);
-                if (busy)
-                    hot_share();
+                hot_share();
                 finish(t);
             }
         } else {
             for (; t + 1 < steps && is_whole(x1, t) && is_whole(x2, t + 1); ++t) {
                 begin(t);
-                if (busy) {
-                    hot(std::integral_constant<int, 0>());
-                    hot(std::integral_constant<int, 1>());
-                }
+                hot(std::integral_constant<int, 0>());
+                hot(std::integral_constant<int, 1>());
                 finish(t);
             }
         }
