@@ -112,18 +112,34 @@ struct TreePlan {
     int64_t parts;                              // partial rows
 };
 
-inline TreePlan tree_plan(int64_t B, int N, int Hq, int heads, int D, int64_t max_len)
+// Row groups of 32 in a block of the shared form: with two (four waves, two on the same rows) blocks that
+// hold four would leave half their waves without rows (64 rows, 8 sequences of 4096 tokens, us with two / four:
+// 16-bit 34.5 / 38.2, MX8 31.5 / 39.9).
+inline int tree_waves(int64_t rows) { return rows <= 32 ? 1 : rows <= 64 ? 2 : 4; }
+
+// Whether the cache is shared through LDS.  The plain form reads it once for every 32 rows, and
+// converts it as often, but has no barriers and a block has less before and behind its loop.  It is taken for
+// 32 rows and for little work in all (us plain / shared; 128 columns, 8 key heads: 32 rows, 8 sequences of 4096
+// tokens, 16-bit 30.3 / 31.3, MX8 21.8 / 27.7; MX8, 128 rows, 16 of 1024 23.0 / 36.3, 8 of 4096 41.7 / 47.6, 48 of
+// 4096 265 / 197; 72 rows, 4 of 4096 26.8 / 31.3, 8 of 4096 44.5 / 41.6; 64 rows, 8 of 4096 29.9 / 31.5, 8 of
+// 8192 45.0 / 44.3; 16-bit, 64 rows, 1 of 16384 24.2 / 26.3, 8 of 4096 39.0 / 34.5, 72 rows, 4 of 4096 32.4 / 30.7).
+inline bool tree_shared(int64_t rows, int64_t tokens, int D, int format)
+{
+    return D == 256 || (rows > 32 && rows * tokens > (format == NM_KV_16 ? int64_t(1) << 23 : int64_t(1) << 24));
+}
+
+inline TreePlan tree_plan(int64_t B, int N, int Hq, int heads, int D, int format, int64_t max_len)
 {
     TreePlan p;
     p.rows = (int64_t)N * (Hq / heads);
-    p.shared = p.rows > 32 || D == 256;
+    p.shared = tree_shared(p.rows, B * heads * max_len, D, format);
     p.mt = p.rows <= 16 ? 1 : 2;
-    p.waves = p.rows <= 32 ? 1 : p.rows <= 64 ? 2 : 4;
-    p.groups = ceil_div(p.rows, 32 * p.waves);
+    p.waves = tree_waves(p.rows);
+    p.groups = ceil_div(p.rows, p.shared ? 32 * p.waves : 16 * p.mt);
     const int64_t units = B * heads * p.groups;
     // Few tokens are one range: a second launch costs more than it spreads (8 key heads of 128
     // columns, 16-bit, us in one range / ranges of 128: one sequence of 32 rows, 256 tokens 8.5 / 10.4,
-    // 512 10.3 / 10.5, 1024 14.0 / 10.6; four of 128 rows, 256 tokens 17.0 / 18.6, 512 22.9 / 21.2).
+    // 512 10.3 / 10.5, 1024 14.0 / 10.6; shared, four of 128 rows, 256 tokens 17.0 / 18.6, 512 22.9 / 21.2).
     const int64_t blocks = max_len <= (p.shared ? 256 : 512) ? 1 : tree_blocks(p.shared, D, units);
     nma::cut(max_len, units, blocks, kTreeRange, &p.splits, &p.chunk);
     p.direct = p.splits <= 1;
@@ -138,12 +154,13 @@ inline int64_t tree_workspace(const TreePlan& p, int D) { return p.parts * (D + 
 // A workspace that serves every call of no larger B and max_len (and the same N): a
 // sequence has at most ceil(max_len / 128) ranges, and all sequences together at most
 // 512 / u + B while they have fewer than 512 units (u of a sequence), or B times the
-// ranges of at most kTreeRange tokens (nma::cut).
+// ranges of at most kTreeRange tokens (nma::cut); the plain form has no fewer units than the shared.
 inline int64_t tree_workspace_bound(int64_t B, int N, int Hq, int heads, int D, int64_t max_len)
 {
     const auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
     const auto most = [](int64_t a, int64_t b) { return a > b ? a : b; };
-    const int64_t grain = nma::kWaves * nma::kStep, u = heads * tree_plan(1, N, Hq, heads, D, 1).groups;
+    const int64_t grain = nma::kWaves * nma::kStep, rows = (int64_t)N * (Hq / heads);
+    const int64_t u = heads * ceil_div(rows, 32 * tree_waves(rows));
     if (max_len <= grain)
         return 0;
     const int64_t even = most(1, least(nma::kMaxRanges, ceil_div(max_len, kTreeRange)));

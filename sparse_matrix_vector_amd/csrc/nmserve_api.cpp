@@ -120,7 +120,7 @@ int nm_attn_tree(const void* q, int64_t q_stride, int64_t B, int N, int Hq, cons
     if (!tree_shape_ok(B, N, Hq, cache->heads, cache->D, cache->format, max_len) || !stride_ok(B * N, q_stride, width) ||
         !(std::fabs(scale) <= 1e30f))
         return NM_ERR_BAD_SHAPE;
-    const nms::TreePlan plan = nms::tree_plan(B, N, Hq, cache->heads, cache->D, max_len);
+    const nms::TreePlan plan = nms::tree_plan(B, N, Hq, cache->heads, cache->D, cache->format, max_len);
     const int64_t need = nms::tree_workspace(plan, cache->D), pages = nma::ceil_div(max_len, cache->page_size);
     if (max_len > 0 && B > 1 && (table_stride < pages || table_stride > kMaxStride))
         return NM_ERR_BAD_SHAPE;

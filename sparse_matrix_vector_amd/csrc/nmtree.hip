@@ -3,8 +3,9 @@
 // A sequence's rows are its drafts' query heads of one key head, N G of them, and a
 // unit takes up to 128 of them over a range of its tokens, so that the cache comes from
 // memory once for all drafts.  Two forms:
-//   up to 32 rows of up to 128 columns: as in nm_attn_decode (nm_attn_units.h), each wave
-//     reads the cache itself, straight into operands, and takes pairs of tiles in turn;
+//   up to 32 rows of up to 128 columns, or more where there is little work (tree_shared in
+//     nm_serve.h): as in nm_attn_decode (nm_attn_units.h), each wave reads the cache itself,
+//     straight into operands, and takes pairs of tiles in turn;
 //   else (shared_kernel) a block of four waves shares it through LDS, each wave 32 rows:
 //     four tiles at a time are loaded by the block, turned into operands once and written
 //     to one of two buffers, the next four being on their way meanwhile.  One wave's 32
@@ -12,6 +13,10 @@
 //     A pair of tiles is worked on in three rounds, as in nmprompt.hip: its scores beside
 //     the weights of the pair before, its sums beside the scores of the next.  With 64 rows
 //     or fewer two waves share a row group and take a pair of every four tiles each.
+// Many rows are bound by the products (one sequence of 131071 tokens, 64 drafts of 64 heads on 8
+// of 128 columns, MX4: 404 us, 680 TFLOP/s of the formula, half as much again with the weights'
+// second operand), few by the cache's way through LDS and the barriers (32 sequences of 12 drafts, 40
+// heads, up to 2048 tokens, 16-bit: 40.6 us, 3.6 TB/s; 16 of 24, 32 heads, up to 8192, MX8: 100).
 // Only pairs of tiles with drafts, or with fewer tokens than they could hold, look at the
 // masks.  Units of one row are joined by a second launch.
 

@@ -200,7 +200,7 @@ long trees(long n)
         promise(bound >= 0 && bound < (int64_t(1) << 46), "a size for every tree in the limits");
         for (int j = 0; j < 4; ++j) {
             const int64_t b = j & 1 ? size(1, B) : B, m = j & 2 ? size(0, ml) : ml;
-            const nms::TreePlan p = nms::tree_plan(b, N, (int)Hq, heads, D, m);
+            const nms::TreePlan p = nms::tree_plan(b, N, (int)Hq, heads, D, (int)(i % 3), m);
             promise(p.chunk > 0 && p.chunk % nma::kStep == 0 && p.splits * p.chunk >= m && (p.splits - 1) * p.chunk <= m,
                     "tree ranges");
             promise(p.splits * p.chunk <= int64_t(1) << 31, "tokens are counted in int32");

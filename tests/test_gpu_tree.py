@@ -49,7 +49,7 @@ class Case:
 
     def __init__(self, nm, fmt, dtype, D, heads, G, N, lens, page, masks=None, tag=0):
         self.nm, self.fmt, self.dtype, self.D, self.heads, self.G, self.N, self.lens = nm, fmt, dtype, D, heads, G, N, lens
-        self.page = page
+        self.page, self.gone = page, {}
         r = random.Random(I.seed_of(fmt, D, N, tag, len(lens)))
         B, longest = len(lens), max(max(lens), 1)
         per = -(-longest // page)
@@ -76,6 +76,15 @@ class Case:
             self.k.append(ref.quantised(ref.f64(k), fmt, dtype))
             self.v.append(ref.quantised(ref.f64(v), fmt, dtype))
 
+    def widen(self, tokens=0):
+        """A table wide enough (absent pages behind the lengths) that the plan takes the form that shares the cache."""
+        rows = self.N * self.G
+        tokens = max(tokens, (1 << 24) // (rows * len(self.lens) * self.heads) + 1)
+        more = torch.full((len(self.lens), -(-tokens // self.page) - self.table.shape[1]), -1, dtype=torch.int32, device="cuda")
+        self.table = torch.cat((self.table, more), 1)
+        assert rows > 32 and self.table.shape[1] * self.page * len(self.lens) * self.heads * rows > 1 << 24
+        return self
+
     def run(self, **kw):
         return self.nm.attn_tree(self.q, self.cache, self.table, self.lens_t, self.visible, **kw)
 
@@ -91,6 +100,7 @@ class Case:
             j = np.arange(n) - (n - self.N)
             for i in range(self.N) if rows is None else rows:
                 bits = np.array([bool(self.masks[b][i] >> int(x) & 1) if x >= 0 else True for x in j], dtype=bool)
+                bits[self.gone.get(b, [])] = False
                 for h in range(self.heads):
                     at = slice(h * self.G, (h + 1) * self.G)
                     o, l, tol, ltol = sref.attend(q[b, i, at], self.k[b][:n, h], self.v[b][:n, h],
@@ -124,6 +134,79 @@ def test_ranges(nm, fmt, D, G, N):
     """Long tokens cut into ranges that a second launch joins; drafts that lie across a border between ranges."""
     for n in (1024 + N // 2, 2500):
         Case(nm, fmt, F16, D, 1, G, N, [n, 300, 128 + N // 2, N], 64, tag=n).check(rows=sorted({0, N // 2, N - 1}))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", (F16, BF16))
+@pytest.mark.parametrize("D,heads,G,N", [(64, 2, 4, 9), (64, 1, 8, 64), (128, 1, 5, 7), (128, 2, 4, 16), (128, 1, 8, 9),
+                                         (128, 1, 3, 43), (128, 1, 16, 16)])
+def test_shared_form(nm, fmt, dtype, D, heads, G, N):
+    """Row groups of every fullness in the form that shares the cache through LDS; short lengths, and several ranges."""
+    lens = [N, N + 1, 15 + N, 16 + N, 64, 100 + N, 130, -1, 0]
+    Case(nm, fmt, dtype, D, heads, G, N, [max(n, N) if n > 0 else n for n in lens], 16, tag=D + N).widen().check(
+        rows=sorted({0, 1, N // 2, N - 1}))
+    Case(nm, fmt, dtype, D, heads, G, N, [2500, 300, 1024 + N // 2, 5], 64, tag=N).widen().check(rows=sorted({0, N // 2, N - 1}))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("G,N", [(4, 16), (4, 27), (8, 40)])
+def test_shared_form_in_one_range(nm, fmt, G, N):
+    """So many sequences that none is cut: the units write the result."""
+    r = random.Random(N)
+    lens = [r.choice((-1, 0, N, N + r.randint(0, 90))) for _ in range(128)]
+    Case(nm, fmt, BF16, 64, 4, G, N, lens, 16, tag=N).widen(1024).check(rows=(0, N - 1))
+
+
+@pytest.mark.parametrize("dtype,D,G,N", [(BF16, 128, 4, 12), (F16, 64, 8, 20)])
+@pytest.mark.parametrize("odd", (math.nan, math.inf))
+def test_shared_form_unseen_infinities_and_nan(nm, dtype, D, G, N, odd):
+    n = 150
+    c = Case(nm, "16", dtype, D, 1, G, N, [n, n], 64, masks=[[1 << i for i in range(N)], tree(N, random.Random(3))]).widen()
+    clean = c.run()
+    bad = rnd((1, 1, D), dtype, "bad")
+    bad[0, 0, 3] = odd
+    for j in (0, N - 1):
+        for b in (0, 1):
+            at = c.slots[b][n - N + j:n - N + j + 1]
+            k, v = nm.kv_read(c.cache, at)
+            nm.kv_write(c.cache, k, bad, at)
+            got = c.run()
+            nm.kv_write(c.cache, torch.full_like(bad, odd), bad, at)    # keys, too
+            got_k = c.run()
+            nm.kv_write(c.cache, k, v, at)
+            for i in range(N):
+                if c.masks[b][i] >> j & 1:
+                    assert not got[b, i, :, 3].isfinite().any()
+                else:                                                   # another order of fp32 sums at most
+                    for x in (got, got_k):
+                        d = (x[b, i].double() - clean[b, i].double()).abs()
+                        assert (d <= 2 * ref.UNIT[dtype] * (clean[b, i].double().abs() + 2.0 ** -10)).all()
+            assert torch.equal(got[1 - b], clean[1 - b])
+    assert torch.equal(c.run(), clean)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_shared_form_absent_pages(nm, fmt):
+    c = Case(nm, fmt, F16, 64, 1, 4, 12, [300, 300, 90], 16).widen()
+    c.table[0, 2], c.table[1, 18], c.table[1, 0], c.table[2, 0] = -5, 1 << 30, -1, 1 << 20
+    c.gone = {0: np.r_[32:48], 1: np.r_[0:16, 288:300], 2: np.r_[0:16]}
+    c.check()
+
+
+def test_forms_agree_in_a_graph(nm):
+    """One plan serves all lengths below max_len; lengths change between replays."""
+    c = Case(nm, "mx4", F16, 128, 2, 4, 12, [1500, 700], 64).widen()
+    ws, out = nm.attn_tree_workspace(2, 12, 8, c.cache, c.table.shape[1] * 64), torch.zeros_like(c.q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(out=out, ws=ws)
+    for n in (1500, 400, 33, 12):
+        c.lens[0] = n
+        c.lens_t[0] = n
+        ws.fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, c.run())
 
 
 def test_masks(nm):
