@@ -308,3 +308,30 @@ def test_stream_and_graph(nm):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, nm.attn_prompt(q, k, v, st))
+
+
+def test_ranges_in_a_graph_and_on_two_streams(nm):
+    """The second launch reads what this call's first wrote: replays with other lengths, and two calls at once."""
+    q, k, v = rnd((24, 4, 128), BF16, "rg", 0), rnd((6000, 1, 128), BF16, "rg", 1), rnd((6000, 1, 128), BF16, "rg", 2)
+    st, kst = starts_of([8, 16]), starts_of([5000, 1000])
+    ws, out = [nm.attn_prompt_workspace(24, 6000, 2, 4, 1, 128) for _ in range(2)], torch.zeros_like(q)
+    assert ws[0].numel() > 0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nm.attn_prompt(q, k, v, st, kst, out=out, ws=ws[0])
+    for n, nk in ((8, 5000), (1, 64), (24, 6000), (0, 0)):
+        st.copy_(starts_of([n, 24 - n]))
+        kst.copy_(starts_of([nk, 6000 - nk]))
+        ws[0].fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, nm.attn_prompt(q, k, v, st, kst))
+    q2, out2 = rnd((24, 4, 128), BF16, "rg", 3), torch.zeros_like(q)
+    want = nm.attn_prompt(q, k, v, st, kst), nm.attn_prompt(q2, k, v, st, kst)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        nm.attn_prompt(q, k, v, st, kst, out=out, ws=ws[0], stream=streams[0])
+        nm.attn_prompt(q2, k, v, st, kst, out=out2, ws=ws[1], stream=streams[1])
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(out2, want[1])
