@@ -94,9 +94,10 @@ int nm_kv_plan(const nm_kv_pages* pages, const int32_t* adds, int64_t rows, int3
  *     zeros.  Rows that no sequence has are left as they are.
  *   lse [T][Hq]        fp32 (natural log of the softmax's sum; -inf where no key is
  *     seen), or NULL.
- *   workspace          nm_attn_prompt_workspace_bytes(...) bytes of device memory,
- *     256-byte aligned, any contents; may be NULL when that is 0.  So many bytes
- *     also serve every call with the same Hq, heads and D and no larger T, Tk and B.
+ *   workspace          nm_attn_prompt_call_bytes(...) bytes of device memory,
+ *     256-byte aligned, any contents; may be NULL when that is 0.  So many serve
+ *     calls of exactly these sizes; nm_attn_prompt_workspace_bytes(...) bytes serve
+ *     every call with the same Hq, heads and D and no larger T, Tk and B.
  * Scores, softmax statistics and sums are fp32.  The weights of the sum are rounded
  * to dtype, and so the sum that they are divided by adds the rounded ones.
  * Infinities and NaN in a key or value that a query does not see do not reach it; in
@@ -107,6 +108,7 @@ int nm_kv_plan(const nm_kv_pages* pages, const int32_t* adds, int64_t rows, int3
  * elements, |scale| <= 1e30.  o, lse and workspace must not overlap anything else.
  */
 int64_t nm_attn_prompt_workspace_bytes(int64_t T, int64_t Tk, int64_t B, int Hq, int heads, int D);
+int64_t nm_attn_prompt_call_bytes(int64_t T, int64_t Tk, int64_t B, int Hq, int heads, int D);
 int nm_attn_prompt(const void* q, int64_t q_stride, int64_t T, const void* k, int64_t k_stride, const void* v,
                    int64_t v_stride, int64_t Tk, const int32_t* starts, const int32_t* k_starts, int64_t B, int Hq,
                    int heads, int D, int dtype, float scale, void* o, float* lse, void* workspace,
@@ -120,15 +122,18 @@ int nm_attn_prompt(const void* q, int64_t q_stride, int64_t T, const void* k, in
  *   o[b][i][h] = sum_t softmax_t(scale * q[b][i][h] . k[t][h / (Hq / heads)]) v[t][...]
  *   q [B * N][Hq][D]   strided rows, 16-byte aligned; Hq a multiple of heads.
  *   visible [B][N]     64-bit masks, 8-byte aligned; bits N and above are not looked at.
- *   page_table, table_stride, lens, max_len, lse, workspace: as for nm_attn_decode
- *     (lens counts the drafts; a length above max_len counts as max_len; one below N
- *     lacks the first drafts; negative: a padding row, whose rows of o and lse stay).
+ *   page_table, table_stride, lens, max_len, lse: as for nm_attn_decode (lens counts
+ *     the drafts; a length above max_len counts as max_len; one below N lacks the first
+ *     drafts; negative: a padding row, whose rows of o and lse stay).
+ *   workspace: as for nm_attn_prompt, nm_attn_tree_call_bytes(...) for calls of exactly
+ *     these sizes, nm_attn_tree_workspace_bytes(...) for those of no larger B and max_len.
  *   o [B][N][Hq][D], lse [B][N][Hq]; zeros and -inf for a draft that sees no token.
  * Types, rounding, absent pages, infinities and NaN: as for nm_attn_decode; what one
  * draft does not see does not reach it.
  * B and Hq 1..65535, N 1..64, B * N * Hq below 2^26, max_len 0..2^30, |scale| <= 1e30.
  */
 int64_t nm_attn_tree_workspace_bytes(int64_t B, int N, int Hq, int heads, int D, int format, int64_t max_len);
+int64_t nm_attn_tree_call_bytes(int64_t B, int N, int Hq, int heads, int D, int format, int64_t max_len);
 int nm_attn_tree(const void* q, int64_t q_stride, int64_t B, int N, int Hq, const nm_kv_cache* cache,
                  const uint64_t* visible, const int32_t* page_table, int64_t table_stride, const int32_t* lens,
                  int64_t max_len, float scale, void* o, float* lse, void* workspace, int64_t workspace_bytes,

@@ -56,9 +56,11 @@ SERVE_SIGNATURES = {
     "nm_kv_plan_scratch_bytes": (_I64, [_I64]),
     "nm_kv_plan": (_I, [_P, _P, _I64, _P, _P, _P, _P, _P]),
     "nm_attn_prompt_workspace_bytes": (_I64, [_I64, _I64, _I64, _I, _I, _I]),
+    "nm_attn_prompt_call_bytes": (_I64, [_I64, _I64, _I64, _I, _I, _I]),
     "nm_attn_prompt": (_I, [_P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I64, _I, _I, _I, _I, ctypes.c_float, _P,
                             _P, _P, _I64, _P]),
     "nm_attn_tree_workspace_bytes": (_I64, [_I64, _I, _I, _I, _I, _I, _I64]),
+    "nm_attn_tree_call_bytes": (_I64, [_I64, _I, _I, _I, _I, _I, _I64]),
     "nm_attn_tree": (_I, [_P, _I64, _I64, _I, _I, _P, _P, _P, _I64, _P, _I64, ctypes.c_float, _P, _P, _P, _I64, _P]),
 }
 

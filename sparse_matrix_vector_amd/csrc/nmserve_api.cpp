@@ -69,6 +69,13 @@ int64_t nm_attn_prompt_workspace_bytes(int64_t T, int64_t Tk, int64_t B, int Hq,
     return prompt_shape_ok(T, Tk, B, Hq, heads, D) ? nms::prompt_workspace_bound(T, Tk, B, Hq, heads, D) : -1;
 }
 
+int64_t nm_attn_prompt_call_bytes(int64_t T, int64_t Tk, int64_t B, int Hq, int heads, int D)
+{
+    return prompt_shape_ok(T, Tk, B, Hq, heads, D)
+               ? nms::prompt_workspace(nms::prompt_plan(T, Tk, B, Hq, heads, D), heads, D)
+               : -1;
+}
+
 int nm_attn_prompt(const void* q, int64_t q_stride, int64_t T, const void* k, int64_t k_stride, const void* v,
                    int64_t v_stride, int64_t Tk, const int32_t* starts, const int32_t* k_starts, int64_t B, int Hq,
                    int heads, int D, int dtype, float scale, void* o, float* lse, void* workspace,
@@ -105,6 +112,13 @@ int64_t nm_attn_tree_workspace_bytes(int64_t B, int N, int Hq, int heads, int D,
 {
     return tree_shape_ok(B, N, Hq, heads, D, format, max_len)
                ? nms::tree_workspace_bound(B, N, Hq, heads, D, max_len)
+               : -1;
+}
+
+int64_t nm_attn_tree_call_bytes(int64_t B, int N, int Hq, int heads, int D, int format, int64_t max_len)
+{
+    return tree_shape_ok(B, N, Hq, heads, D, format, max_len)
+               ? nms::tree_workspace(nms::tree_plan(B, N, Hq, heads, D, format, max_len), D)
                : -1;
 }
 

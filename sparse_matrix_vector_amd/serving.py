@@ -115,7 +115,7 @@ def attn_prompt(q, k, v, starts, k_starts=None, scale=None, out=None, lse=None, 
     sees keys j <= i + nk - nq, so that more keys than queries are a piece of a prompt behind earlier
     tokens.  scale defaults to 1/sqrt(D).  Returns out [T][Hq][D], zeros where a query sees no key; rows
     that no sequence has are left as they are.  ``lse`` (float32 [T][Hq]) receives the log of the
-    softmax's sum.  ``ws``: an attn_prompt_workspace(), or None to allocate one where it is needed."""
+    softmax's sum.  ``ws``: an attn_prompt_workspace(), or None to allocate what this call needs (often nothing)."""
     shape = _size(q, "q", 3)
     T, hq, D = shape
     Tk, heads, _ = _size(k, "k", 3)
@@ -145,7 +145,7 @@ def attn_prompt(q, k, v, starts, k_starts=None, scale=None, out=None, lse=None, 
         else:
             op = _check(out, "out", dev, dt, shape)
         if ws is None:
-            nbytes = lib.nm_attn_prompt_workspace_bytes(T, Tk, n - 1, hq, heads, D)
+            nbytes = lib.nm_attn_prompt_call_bytes(T, Tk, n - 1, hq, heads, D)
             if nbytes > 0:
                 ws = q.new_empty(nbytes, dtype=torch.uint8)
                 wsp = ws.data_ptr()
@@ -178,7 +178,7 @@ def attn_tree(q, cache, page_table, lens, visible, max_len=None, scale=None, out
     the drafts: draft i sees all tokens before the drafts, and draft j where bit j of visible[b][i] (int64 [B][N]) is
     set.  lens[b] < 0 marks a padding row, which is left as it was.  scale defaults to 1/sqrt(D); max_len to the
     table's width.  Returns out [B][N][Hq][D]; ``lse`` (float32 [B][N][Hq]) receives the log of the softmax's sum.
-    ``ws``: an attn_tree_workspace(), or None to allocate one where it is needed.  The rows of q may be strided
+    ``ws``: an attn_tree_workspace(), or None to allocate what this call needs (often nothing).  The rows of q may be strided
     (draft after draft, sequence after sequence at one stride).  A batch of no sequences gives an empty result."""
     c = _cache(cache)
     dev, dt = c._index, c.dtype
@@ -221,7 +221,7 @@ def attn_tree(q, cache, page_table, lens, visible, max_len=None, scale=None, out
         else:
             op = _check(out, "out", dev, dt, shape)
         if ws is None:
-            nbytes = lib.nm_attn_tree_workspace_bytes(B, N, hq, c.heads, c.D, c._format, max_len)
+            nbytes = lib.nm_attn_tree_call_bytes(B, N, hq, c.heads, c.D, c._format, max_len)
             if nbytes > 0:
                 ws = q.new_empty(nbytes, dtype=torch.uint8)
                 wsp = ws.data_ptr()
