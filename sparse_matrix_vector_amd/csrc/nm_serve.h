@@ -151,20 +151,22 @@ inline TreePlan tree_plan(int64_t B, int N, int Hq, int heads, int D, int format
 
 inline int64_t tree_workspace(const TreePlan& p, int D) { return p.parts * (D + 2) * 4; }
 
-// A workspace that serves every call of no larger B and max_len (and the same N): a
-// sequence has at most ceil(max_len / 128) ranges, and all sequences together at most
-// 512 / u + B while they have fewer than 512 units (u of a sequence), or B times the
-// ranges of at most kTreeRange tokens (nma::cut); the plain form has no fewer units than the shared.
+// A workspace that serves every call of no larger B and max_len (and the same N).  Up to 256
+// tokens no plan has ranges.  Else a sequence has at most ceil(max_len / 128) of them, and
+// all sequences together at most 512 / u + B while they have fewer than 512 units (u of a
+// sequence); with more units a sequence has one range, and so no partial results, unless
+// tokens pass kTreeRange: then B times the ranges of so many (nma::cut).  The plain form has
+// no fewer units than the shared.
 inline int64_t tree_workspace_bound(int64_t B, int N, int Hq, int heads, int D, int64_t max_len)
 {
     const auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
     const auto most = [](int64_t a, int64_t b) { return a > b ? a : b; };
     const int64_t grain = nma::kWaves * nma::kStep, rows = (int64_t)N * (Hq / heads);
     const int64_t u = heads * ceil_div(rows, 32 * tree_waves(rows));
-    if (max_len <= grain)
+    if (max_len <= 256)
         return 0;
-    const int64_t even = most(1, least(nma::kMaxRanges, ceil_div(max_len, kTreeRange)));
-    int64_t ranges = least(B * even, most(B, nma::kMaxBlocks / u));
+    const int64_t even = least(nma::kMaxRanges, ceil_div(max_len, kTreeRange));
+    int64_t ranges = even > 1 ? least(B * even, nma::kMaxBlocks / u) : 0;
     if (u < 2 * nma::kCus)
         ranges = most(ranges, 2 * nma::kCus / u + least(B, (2 * nma::kCus - 1) / u));
     ranges = least(ranges, B * ceil_div(max_len, grain));

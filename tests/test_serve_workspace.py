@@ -73,6 +73,18 @@ def test_one_calls_need_is_within_every_larger_bound():
             assert 0 <= call(t, tk, b, heads * G, heads, D) <= most
 
 
+def test_tree_bound_is_near_some_calls_need():
+    """A sequence that is not cut has no partial results.  Those that are make no more than 512 / u + B' ranges together (u
+    units each, B' u < 512), and about 512 / u for some number of them: within a factor of three with the rounding of ranges."""
+    call, bound = sizes("tree")
+    for heads, G, N, D, fmt, B, ml in ((8, 8, 24, 128, 1, 256, 4096), (8, 4, 24, 128, 1, 64, 4096), (8, 4, 12, 128, 0, 32, 2048),
+                                       (8, 8, 24, 128, 1, 256, 200), (16, 8, 64, 128, 2, 500, 4096), (64, 1, 64, 64, 0, 500, 1000),
+                                       (8, 4, 12, 128, 0, 100, 16384)):
+        args = lambda b, m: (b, N, heads * G, heads, D, fmt, m)                                             # noqa: E731
+        largest = max(call(*args(b, m)) for b in range(1, B + 1) for m in {ml, ml // 2 + 1, min(ml, 512), min(ml, 513)})
+        assert largest <= bound(*args(B, ml)) <= 3 * largest, (heads, G, N, B, ml)
+
+
 # ---- on the GPU ------------------------------------------------------------------
 def taken(f):
     """Most bytes that f() holds of the allocator beyond what is there."""
