@@ -69,6 +69,14 @@ int64_t nm_kv_plan_scratch_bytes(int64_t B);
  *   slots     int64 [rows]  a row's slot (page * page_size + place), for nm_kv_write;
  *             -1 behind the last row, and where a page number is negative.
  *   positions int32 [rows]  a row's place in its sequence; 0 behind the last row.
+ * New rows are packed: a sequence that gets nothing has none.  nm_attn_prompt takes them
+ * as they lie; nm_attn_decode (N = 1) and nm_attn_tree take rows b N .. b N + N - 1 for
+ * sequence b.  Where one may get nothing (a padding row, a row of the table that is too short,
+ * no pages), a step of N tokens a sequence is laid out by b N: row b N + i has slot
+ * slots[starts[b] + i], or -1 where granted[b] is not positive, and such a sequence goes into
+ * attention with the length -1.  A row's place is its position in the text, but for the drafts
+ * of a tree with branches: draft i's is lens[b] - N + its depth.  Dropping takes the last tokens;
+ * kept drafts behind refused ones are moved to their places first (nm_kv_read, nm_kv_write).
  * Dropping what was just granted leaves the stack and lens as they were.
  * Padding rows get and lose nothing.  rows 0 .. 2^31 - 1; lens plus adds must stay below
  * 2^31.  No output or part of the book may overlap anything else.  Calls on one book
@@ -120,7 +128,8 @@ int nm_attn_prompt(const void* q, int64_t q_stride, int64_t T, const void* k, in
  * Draft i sees every token before the drafts, and draft j where bit j of
  * visible[b][i] is set (itself and the drafts that lead to it, in a tree):
  *   o[b][i][h] = sum_t softmax_t(scale * q[b][i][h] . k[t][h / (Hq / heads)]) v[t][...]
- *   q [B * N][Hq][D]   strided rows, 16-byte aligned; Hq a multiple of heads.
+ *   q [B * N][Hq][D]   strided rows, 16-byte aligned; Hq a multiple of heads.  Sequence b's
+ *     drafts are rows b N .. b N + N - 1, whatever nm_kv_plan granted to those before it.
  *   visible [B][N]     64-bit masks, 8-byte aligned; bits N and above are not looked at.
  *   page_table, table_stride, lens, max_len, lse: as for nm_attn_decode (lens counts
  *     the drafts; a length above max_len counts as max_len; one below N lacks the first

@@ -70,7 +70,9 @@ def kv_plan(pages, adds, rows, out=None, stream=None):
     short gets none).  Brings pages.table, .lens, .free and .n_free up to date and returns (starts, slots,
     positions, granted): rows starts[b] .. starts[b+1] - 1 (int32 [sequences + 1]) are b's new tokens, slots (int64
     [rows]) and positions (int32 [rows]) theirs in the cache and the sequence (-1 and 0 behind the last), granted
-    (int32 [sequences]) what each got or lost.  ``out`` is such a tuple."""
+    (int32 [sequences]) what each got or lost.  ``out`` is such a tuple.  New rows are packed, without gaps for
+    sequences that get nothing; attn_decode and attn_tree take sequence b's N rows at b N: see include/nmserve.h for
+    the layout of a step in which some may get nothing."""
     if not isinstance(pages, KVPages):
         raise TypeError("pages must be a KVPages")
     p = pages
@@ -176,7 +178,8 @@ def attn_tree(q, cache, page_table, lens, visible, max_len=None, scale=None, out
     """Attention of a tree of drafted tokens per sequence, q [B][N][Hq][D], over the cache.  Sequence b holds lens[b]
     (int32 [B], device; at most max_len) tokens on its pages page_table[b] (int32 [B][pages]), the last N of which are
     the drafts: draft i sees all tokens before the drafts, and draft j where bit j of visible[b][i] (int64 [B][N]) is
-    set.  lens[b] < 0 marks a padding row, which is left as it was.  scale defaults to 1/sqrt(D); max_len to the
+    set.  lens[b] < 0 marks a padding row, which is left as it was: sequences to which kv_plan granted nothing go in as
+    such.  scale defaults to 1/sqrt(D); max_len to the
     table's width.  Returns out [B][N][Hq][D]; ``lse`` (float32 [B][N][Hq]) receives the log of the softmax's sum.
     ``ws``: an attn_tree_workspace(), or None to allocate what this call needs (often nothing).  The rows of q may be strided
     (draft after draft, sequence after sequence at one stride).  A batch of no sequences gives an empty result."""
