@@ -823,71 +823,94 @@ struct Stage {
         }
     }
 
+    // Codes: keys and values by themselves.
     __device__ __forceinline__ void load_k(const AttnArgs& A, const TileRef& t, int part, int lane)
     {
         const uint8_t* kt = A.k + t.tile * nma::tile_bytes(D, BITS);
-        if constexpr (BITS == 16) {
 #pragma unroll
-            for (int i = 0; i < kMine; ++i)
-                get<16>(k + 4 * i, kt + (part * kMine + i) * 1024 + lane * 16);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int at = (part * kMine + i) * BITS;
-                get<BITS>(k + i * BITS / 4, kt + at / C::kCb * 64 * C::kCb + lane * C::kCb + at % C::kCb);
-            }
-            C::load_k_scale(ks, A.k_scale + t.tile * nma::scale_tile_bytes(D), lane % 16);
+        for (int i = 0; i < kMine; ++i) {
+            const int at = (part * kMine + i) * BITS;
+            get<BITS>(k + i * BITS / 4, kt + at / C::kCb * 64 * C::kCb + lane * C::kCb + at % C::kCb);
         }
+        C::load_k_scale(ks, A.k_scale + t.tile * nma::scale_tile_bytes(D), lane % 16);
     }
 
     __device__ __forceinline__ void load_v(const AttnArgs& A, const TileRef& t, int part, int lane)
     {
         const uint8_t* vt = A.v + t.tile * nma::tile_bytes(D, BITS);
         n = t.n;
+#pragma unroll
+        for (int i = 0; i < kVPairs * kVBytes; i += kVLoad) {
+            const int at = part * kVPairs * kVBytes + i;
+            get<kVLoad>(v + i / 4, vt + at / C::kVb * 64 * C::kVb + lane * C::kVb + at % C::kVb);
+        }
+        C::load_v_scale(vs, A.v_scale + t.tile * nma::scale_tile_bytes(D), lane % 16, lane / 16);
+    }
+
+    // Both.  16-bit pieces of keys and values go in turn, to LDS too: all keys and then all values is slower
+    // (64 heads of 32 sequences behind 32741 tokens and up to 1024 own, us in turn / apart: 72.8 / 74.4).
+    __device__ __forceinline__ void load(const AttnArgs& A, const TileRef& t, int part, int lane)
+    {
         if constexpr (BITS == 16) {
+            const uint8_t* kt = A.k + t.tile * nma::tile_bytes(D, BITS);
+            const uint8_t* vt = A.v + t.tile * nma::tile_bytes(D, BITS);
+            n = t.n;
 #pragma unroll
-            for (int i = 0; i < kMine; ++i)
+            for (int i = 0; i < kMine; ++i) {
+                get<16>(k + 4 * i, kt + (part * kMine + i) * 1024 + lane * 16);
                 get<16>(v + 4 * i, vt + (part * kMine + i) * 1024 + lane * 16);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kVPairs * kVBytes; i += kVLoad) {
-                const int at = part * kVPairs * kVBytes + i;
-                get<kVLoad>(v + i / 4, vt + at / C::kVb * 64 * C::kVb + lane * C::kVb + at % C::kVb);
             }
-            C::load_v_scale(vs, A.v_scale + t.tile * nma::scale_tile_bytes(D), lane % 16, lane / 16);
+        } else {
+            load_k(A, t, part, lane);
+            load_v(A, t, part, lane);
         }
     }
 
-    __device__ __forceinline__ void load(const AttnArgs& A, const TileRef& t, int part, int lane)
-    {
-        load_k(A, t, part, lane);
-        load_v(A, t, part, lane);
-    }
-
-    // Operands of what was loaded into the tile's place among keys, or values, of which those of
+    // Operands of the codes that were loaded into the tile's place among keys, or values, of which those of
     // tokens that do not count become zeros (0 * NaN must not reach o).  With `turned`, the keys'
-    // lanes of an odd tile change places (m with m ^ 8).
+    // lanes of an odd tile change places (m with m ^ 8).  (The operand functions take a lane's whole
+    // part; what this wave did not load is not used.)
     __device__ __forceinline__ void put_k(uint8_t* keys, int tile, int part, int lane, bool turned = false) const
     {
         uint8_t* kd = keys + tile * kTileBytes;
         const int to = lane ^ (turned ? tile % 2 * 8 : 0);
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            u32x4 x;
-            if constexpr (BITS == 16)
-                x = u32x4{k[4 * i], k[4 * i + 1], k[4 * i + 2], k[4 * i + 3]};
-            else                                // (the operand functions take a lane's whole part; what this wave did not load is not used)
-                x = C::k_codes(k + i * BITS / 4, ks, part * kMine + i, lane / 16);
-            *reinterpret_cast<u32x4*>(kd + (part * kMine + i) * 1024 + to * 16) = x;
-        }
+        for (int i = 0; i < kMine; ++i)
+            *reinterpret_cast<u32x4*>(kd + (part * kMine + i) * 1024 + to * 16) =
+                C::k_codes(k + i * BITS / 4, ks, part * kMine + i, lane / 16);
     }
 
     __device__ __forceinline__ void put_v(uint8_t* values, int tile, int part, int lane) const
     {
         uint8_t* vd = values + tile / 2 * 2 * kTileBytes + tile % 2 * 8;
+        const int left = n - 4 * (lane / 16);
+        if constexpr (kVPairs == 2) {
+            uint32_t lo[kPer], hi[kPer];
+            C::v_codes(lo, v, vs);
+            C::v_codes(hi, v + kVBytes / 4, vs >> 16);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                *reinterpret_cast<u32x2*>(vd + j * 1024 + lane * 16) =
+                    u32x2{lo[j] & keep(left, 0), hi[j] & keep(left, 1)};
+        } else {
+            uint32_t out[kPer];
+            C::v_codes(out, v, vs >> (16 * part));
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                *reinterpret_cast<uint32_t*>(vd + j * 1024 + lane * 16 + part * 4) = out[j] & keep(left, part);
+        }
+    }
+
+    // Both, into a buffer of all keys, then all values.
+    __device__ __forceinline__ void put(uint8_t* buf, int tile, int part, int lane) const
+    {
         if constexpr (BITS == 16) {
+            uint8_t* kd = buf + tile * kTileBytes;
+            uint8_t* vd = buf + (kTiles + tile / 2 * 2) * kTileBytes + tile % 2 * 8;
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
+                *reinterpret_cast<u32x4*>(kd + (part * kMine + i) * 1024 + lane * 16) =
+                    u32x4{k[4 * i], k[4 * i + 1], k[4 * i + 2], k[4 * i + 3]};
                 u32x4 x = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
                 if (n < nma::kTile) {
                     // 16 bytes here are two lanes' halves of one column: quarter (lane % 32) / 8
@@ -899,29 +922,9 @@ struct Stage {
                 *reinterpret_cast<u32x2*>(to + 16) = u32x2{x.z, x.w};
             }
         } else {
-            const int left = n - 4 * (lane / 16);
-            if constexpr (kVPairs == 2) {
-                uint32_t lo[kPer], hi[kPer];
-                C::v_codes(lo, v, vs);
-                C::v_codes(hi, v + kVBytes / 4, vs >> 16);
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    *reinterpret_cast<u32x2*>(vd + j * 1024 + lane * 16) =
-                        u32x2{lo[j] & keep(left, 0), hi[j] & keep(left, 1)};
-            } else {
-                uint32_t out[kPer];
-                C::v_codes(out, v, vs >> (16 * part));
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    *reinterpret_cast<uint32_t*>(vd + j * 1024 + lane * 16 + part * 4) = out[j] & keep(left, part);
-            }
+            put_k(buf, tile, part, lane);
+            put_v(buf + kTiles * kTileBytes, tile, part, lane);
         }
-    }
-
-    __device__ __forceinline__ void put(uint8_t* buf, int tile, int part, int lane) const
-    {
-        put_k(buf, tile, part, lane);
-        put_v(buf + kTiles * kTileBytes, tile, part, lane);
     }
 
     // Mask of the token pair (2 i, 2 i + 1) of a quarter of which `left` tokens count.
@@ -946,8 +949,7 @@ constexpr int staged_bytes()
 }
 
 template <int DT, int BITS, int D, int MT, int W>
-__device__ __forceinline__ void attend_staged(const AttnArgs& A, const int32_t* pages, int h, int group, int R, int start,
-                                              int end, int64_t part_row, uint8_t* lds)
+__device__ __forceinline__ void attend_staged(const AttnArgs& A, int unit, uint8_t* lds)
 {
     using S = Stage<DT, BITS, D, W>;
     constexpr int NT = S::kTiles, kSteps = S::kSteps, kPer = S::kPer;
@@ -955,12 +957,14 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, const int32_t* 
     int(*const count)[NT] = reinterpret_cast<int(*)[NT]>(lds + 2 * S::kBytes);
     const int lane = threadIdx.x % 64, m = lane % 16, kg = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int row0 = (group * W + wave) * 16 * MT;
+    const int h = unit % A.heads, split = unit / A.heads % A.prefix_splits;
+    const int row0 = (unit / A.heads / A.prefix_splits * W + wave) * 16 * MT;
+    const int start = split * A.prefix_chunk, end = min(start + A.prefix_chunk, A.prefix_len);
     const int mine = wave % NT, part = wave / NT;            // the tile of each step that this wave loads
-    const bool busy = row0 < R;
+    const bool busy = row0 < A.prefix_rows;
 
     Rows<OneToken, DT, BITS, D, MT> rows;
-    rows.load(A, h, 0, row0, R, m, kg);
+    rows.load(A, h, 0, row0, A.prefix_rows, m, kg);
     f32x4 acc[MT][kPer];
     float mx[MT], sum[MT];
 #pragma unroll
@@ -980,8 +984,8 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, const int32_t* 
         if (part == 0 && lane == 0)
             count[which][mine] = stage.n;
     };
-    stage.load(A, tile_ref(A, page_of(A, pages, at, end), at, end, h), part, lane);
-    int page = page_of(A, pages, at + NT, end);
+    stage.load(A, tile_ref(A, page_of(A, A.prefix_pages, at, end), at, end, h), part, lane);
+    int page = page_of(A, A.prefix_pages, at + NT, end);
     put(0);
     __syncthreads();
     for (int i = 0; i < steps; ++i) {
@@ -989,7 +993,7 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, const int32_t* 
         if (more) {
             at += NT;
             stage.load(A, tile_ref(A, page, at, end, h), part, lane);
-            page = page_of(A, pages, at + NT, end);
+            page = page_of(A, A.prefix_pages, at + NT, end);
         }
         if (busy) {
             const uint8_t* kb = lds + (i & 1) * S::kBytes;
@@ -1072,8 +1076,9 @@ __device__ __forceinline__ void attend_staged(const AttnArgs& A, const int32_t* 
     for (int g = 0; g < MT; ++g) {
         const int r = row0 + 16 * g;
         const float total = quarters_sum(sum[g]);
-        if (r + m < R)
-            store_part<D>(A, part_row + r, min(16, R - r), m, kg, acc[g], mx[g], total);
+        if (r + m < A.prefix_rows)
+            store_part<D>(A, ((int64_t)split * A.heads + h) * A.prefix_rows + r, min(16, A.prefix_rows - r), m, kg,
+                          acc[g], mx[g], total);
     }
 }
 

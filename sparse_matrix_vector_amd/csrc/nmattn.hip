@@ -61,12 +61,11 @@ __global__ __launch_bounds__((W ? W : nma::kWaves) * 64, 2) void units_kernel(co
         return;
     if (block < prefix_blocks) {
         const int unit = block;
-        const int h = unit % A.heads, split = unit / A.heads % A.prefix_splits, group = unit / A.heads / A.prefix_splits;
-        const int start = split * A.prefix_chunk, end = min(start + A.prefix_chunk, A.prefix_len);
         if constexpr (W > 0) {
-            attend_staged<DT, BITS, D, MT, W>(A, A.prefix_pages, h, group, A.prefix_rows, start, end,
-                                              ((int64_t)split * A.heads + h) * A.prefix_rows, lds);
+            attend_staged<DT, BITS, D, MT, W>(A, unit, lds);
         } else {
+            const int h = unit % A.heads, split = unit / A.heads % A.prefix_splits, group = unit / A.heads / A.prefix_splits;
+            const int start = split * A.prefix_chunk, end = min(start + A.prefix_chunk, A.prefix_len);
             const int at = start / nma::kTile + 2 * wave;
             attend<OneToken, DT, BITS, D, MT, NW>(A, A.prefix_pages, h, 0, group * 16 * MT, A.prefix_rows, start, end,
                                                   end, page_of(A, A.prefix_pages, at, end),
