@@ -106,11 +106,16 @@ int nm_kv_plan(const nm_kv_pages* pages, const int32_t* adds, int64_t rows, int3
  *     256-byte aligned, any contents; may be NULL when that is 0.  So many serve
  *     calls of exactly these sizes; nm_attn_prompt_workspace_bytes(...) bytes serve
  *     every call with the same Hq, heads and D and no larger T, Tk and B.
+ * Few rows behind many keys are cut into ranges of keys by the average Tk / B, since lengths
+ * are on the device: one long sequence among many short ones is not cut, and is faster in
+ * a call of its own (a query on 16384 keys beside 31 on 16: 278 us, alone 28).
  * Scores, softmax statistics and sums are fp32.  The weights of the sum are rounded
- * to dtype, and so the sum that they are divided by adds the rounded ones.
+ * to dtype, and so the sum that they are divided by adds the rounded ones (nm_attn_decode and
+ * nm_attn_tree keep more of them: a token's results as a prompt and as a decode step differ by that).
  * Infinities and NaN in a key or value that a query does not see do not reach it; in
- * one that it sees they have the effect that the formula gives them, and so have fp32
- * sums that overflow.  Results do not depend on other calls and repeat bit for bit.
+ * one that it sees they have the effect that the formula gives them (a score of -inf weighs
+ * nothing; a query with no other scores gets zeros), and so have fp32 sums that overflow.
+ * Results do not depend on other calls and repeat bit for bit.
  * B 0 .. 65535, Hq and heads 1 .. 65535, B * heads below 2^30, T * Hq / heads and Tk
  * below 2^31 - 2^16, T * Hq * D and Tk * heads * D below 2^40, row strides up to 2^28
  * elements, |scale| <= 1e30.  o, lse and workspace must not overlap anything else.
@@ -136,6 +141,8 @@ int nm_attn_prompt(const void* q, int64_t q_stride, int64_t T, const void* k, in
  *     drafts; negative: a padding row, whose rows of o and lse stay).
  *   workspace: as for nm_attn_prompt, nm_attn_tree_call_bytes(...) for calls of exactly
  *     these sizes, nm_attn_tree_workspace_bytes(...) for those of no larger B and max_len.
+ *     (max_len also decides the form of the work: 16 sequences of 24 drafts and up to 512 tokens,
+ *     MX8, take 16 us with the longest length, 33 with four times that or more.)
  *   o [B][N][Hq][D], lse [B][N][Hq]; zeros and -inf for a draft that sees no token.
  * Types, rounding, absent pages, infinities and NaN: as for nm_attn_decode; what one
  * draft does not see does not reach it.

@@ -44,10 +44,12 @@ struct PromptPlan {
 };
 
 // Few rows behind many keys leave most of the GPU idle: their keys are cut into ranges (each
-// tile's own into equal ones, on the device).  On the host only the average of the keys is
-// known; a tile of 64 of them takes a lone block about 1 us, the second launch about 6, and
-// partial results go through memory at about 4.5 TB/s both ways together (16 queries behind
-// 16384 tokens, 32 heads on 8 of 128 columns: 283 us in one range, 27.5 in 32).
+// tile's own into equal ones, on the device).  A tile of 64 keys takes a lone block about 1 us,
+// the second launch about 6, and partial results go through memory at about 4.5 TB/s both ways
+// together (16 queries behind 16384 tokens, 32 heads on 8 of 128 columns: 283 us in one range,
+// 27.5 in 32).  On the host only the average of the keys is known, so that one long sequence among
+// many short ones is not cut (32 sequences of a query, one of 16384 keys and 31 of 16: 278 us, 28
+// for the long one alone; one of 131072 among 64: 2270 and 126).
 constexpr int64_t kPromptKeys = 64;             // of a tile of keys
 constexpr int64_t kPromptRanges = 64, kPromptBlocks = 512;
 
@@ -91,8 +93,11 @@ inline int64_t prompt_workspace_bound(int64_t T, int64_t Tk, int64_t B, int Hq, 
 // Units of (rows of a sequence and key head, range of its tokens), one block each, in two
 // forms (nmtree.hip).
 constexpr int kTreeWaves = 4;
-// Tokens of a range at most (us with 1024 / 2048 / 4096: 16 sequences of 24 drafts, 4 heads a key head, up to
-// 8192 tokens, MX8 104 / 109 / 109; 4 of 64 drafts, 16384 tokens, 16-bit 148 / 135 / 134).
+// Tokens of a range at most.  Shorter ones would share out sequences of different lengths better, but each costs
+// a block's start and a partial result (us with 1024 / 2048 / 4096, 32 heads on 8 of 128 columns: 16 sequences of 24
+// drafts and up to 8192 tokens, MX8 104.5 / 103.5 / 102.7, all of 8192 122.5 / 116.1 / 114.0; 8 of 8 drafts, up to 32768,
+// MX4 81.4 / 71.6 / 67.2; 4 of 64 drafts, 16384 tokens, 16-bit 138.5 / 123.6 / 124.0; 64 heads, 64 drafts behind 131071,
+// MX4 427 / 427 / 408; slower only where there are many: 48 of 24 drafts, up to 8192, 16-bit 239.8 / 239.1 / 259.0).
 constexpr int64_t kTreeRange = 4096;
 
 // Blocks that fill the GPU: two a CU, but one where a block of the shared form takes a CU's registers and
