@@ -75,7 +75,7 @@ int64_t nm_kv_plan_scratch_bytes(int64_t B);
  * no pages), a step of N tokens a sequence is laid out by b N: row b N + i has slot
  * slots[starts[b] + i], or -1 where granted[b] is not positive, and such a sequence goes into
  * attention with the length -1.  A row's place is its position in the text, but for the drafts
- * of a tree with branches: draft i's is lens[b] - N + its depth.  Dropping takes the last tokens;
+ * of a tree with branches: draft i's is lens[b] - N + its depth (a root's is 0).  Dropping takes the last tokens;
  * kept drafts behind refused ones are moved to their places first (nm_kv_read, nm_kv_write).
  * Dropping what was just granted leaves the stack and lens as they were.
  * Padding rows get and lose nothing.  rows 0 .. 2^31 - 1; lens plus adds must stay below

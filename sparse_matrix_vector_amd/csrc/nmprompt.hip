@@ -20,9 +20,10 @@
 // A weight enters the second product as one 16-bit operand, where the paged cache's attention has
 // two (the rounding and the rest, nm_attn_units.h).  A prompt's products are what bounds it, and
 // the second operand would make them half as many again; one loses half a step of each weight, in
-// the order of what rounding the output does (root mean square error against 64 bits on the measured prompts:
-// 1.08 to 1.29 times that of 32-bit arithmetic rounded once at the end).  So that the weights still add up to one, the sum they are divided by adds the rounded ones; lse adds
-// them as they were.
+// the order of what rounding the output does (root mean square error against 64 bits on the
+// measured prompts: 1.08 to 1.29 times that of 32-bit arithmetic rounded once at the end).  So
+// that the weights still add up to one, the sum they are divided by adds the rounded ones; lse
+// adds them as they were.
 //
 // Keys and values go from memory to LDS directly (global_load_lds, 1 KB a wave and
 // instruction), one tile ahead.  Rows lie in LDS as in memory but for an exclusive
